@@ -199,6 +199,16 @@ __device__ __forceinline__ float gate_write(float x, bool logits) {
 // ---------------------------------------------------------------------------
 // Host-side helpers
 // ---------------------------------------------------------------------------
+inline int num_sms() {
+  static const int n = [] {
+    int dev = 0, v = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+    return v > 0 ? v : 1;
+  }();
+  return n;
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Records the CUDA error text for gdn_last_cuda_error_string().
@@ -286,6 +296,7 @@ gdn_status_t gather_status_api(int32_t* out, int clear, int first, cudaStream_t 
 gdn_status_t gather_status_conv(int32_t* out, int clear, int first, cudaStream_t st);
 gdn_status_t gather_status_decode(int32_t* out, int clear, int first, cudaStream_t st);
 gdn_status_t gather_status_prefill_tc(int32_t* out, int clear, int first, cudaStream_t st);
+gdn_status_t gather_status_attn_split(int32_t* out, int clear, int first, cudaStream_t st);
 #define GDN_DEFINE_STATUS_GATHER(name)                                                   \
   gdn_status_t name(int32_t* out, int clear, int first, cudaStream_t st) {               \
     gather_status_kernel<<<1, 1, 0, st>>>(out, clear, first);                            \
@@ -359,5 +370,29 @@ gdn_status_t launch_prefill_tc(const void* q, const void* k, int64_t qk_stride, 
                                const uint8_t* has_init, void* o, int32_t Hk, int32_t Hv,
                                int32_t flags, void* workspace, cudaStream_t st,
                                StateSlots slots = {});
+
+// Block tables, positions, slots and page pieces of one engine step.
+gdn_status_t launch_block_tables(const int32_t* cu, const int32_t* ctx, const int32_t* free_blocks,
+                                 int32_t num_free, int32_t N, int32_t T, int32_t block_tokens,
+                                 int32_t* table, int64_t table_stride, int32_t max_blocks,
+                                 int32_t* kv, int32_t* positions, int64_t* slots,
+                                 gdn_page_piece_t* pieces, int32_t piece_cap, int32_t* counts,
+                                 int32_t* status, cudaStream_t st);
+
+gdn_status_t launch_rotary(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const int32_t* positions, const int64_t* phases, void* q_out,
+                           int64_t q_out_stride, void* k_out, int64_t k_out_stride, int32_t T,
+                           int32_t Hq, int32_t Hk, int32_t d, int32_t rot, float scale,
+                           int32_t interleaved, int32_t inverse, cudaStream_t st);
+
+gdn_status_t launch_rotary_kv_append(const void* q, int64_t q_stride, const void* k,
+                                     int64_t k_stride, const void* v, int64_t v_stride,
+                                     const int32_t* positions, const int64_t* phases,
+                                     const gdn_page_piece_t* pieces, const int32_t* num_pieces,
+                                     int32_t piece_cap, void* q_out, int64_t q_out_stride,
+                                     void* kc, void* vc, float* ks, float* vs, int32_t num_blocks,
+                                     int32_t block_tokens, int32_t T, int32_t Hq, int32_t Hk,
+                                     int32_t d, int32_t rot, float scale, int32_t interleaved,
+                                     cudaStream_t st);
 
 }  // namespace gdn

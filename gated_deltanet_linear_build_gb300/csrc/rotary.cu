@@ -1,0 +1,399 @@
+// Rotary positions, alone and fused with the append of k and v to an 8-bit
+// paged cache.
+//
+// Pair i of a head at position p turns by the angle 2 pi frac(p phase_i), with
+// phase_i = f_i / (2 pi) turns per token held as a 64-bit fixed-point fraction.
+// The product wraps modulo 2^64, which IS the reduction to one turn: exact for
+// every 32-bit position, where a float32 product p f_i is off by 0.06 rad at a
+// million tokens. The top 32 bits, as a signed fraction of a turn, give an
+// angle in [-pi, pi], where the hardware sine and cosine are within 2^-21:
+// far below the BF16 or 8-bit rounding of the results.
+//
+// Both kernels are one pass over memory. A thread owns two 8-element vectors
+// of a head (the two halves of its 8 pairs) and keeps its 8 sines and cosines
+// in registers over kHeads heads, all of whose loads are issued first.
+#include <algorithm>
+
+#include <cuda_fp8.h>
+
+#include "gdn_internal.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kRotThreads = 256;
+constexpr int kHeads = 4;               // heads per thread
+
+struct RotArgs {
+  const __nv_bfloat16 *q, *k;
+  __nv_bfloat16 *q_out, *k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;   // elements per token
+  const int32_t* positions;
+  const uint64_t* phases;
+  int T, Hq, Hk, log_j, rot;            // d = 16 << log_j
+  float scale;
+  int interleaved, inverse;
+};
+
+// Element offsets of vector pair j of a head: the pairs of a rotated unit in
+// the half layout lie rot / 2 apart; otherwise 16 elements are contiguous.
+__device__ __forceinline__ void unit_offsets(int j, int rot, int interleaved, int& oa, int& ob) {
+  const bool split = !interleaved && j * 16 < rot;
+  oa = split ? j * 8 : j * 16;
+  ob = split ? rot / 2 + j * 8 : j * 16 + 8;
+}
+
+__device__ __forceinline__ void load_phases(const uint64_t* phases, int j, uint64_t (&ph)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const ulonglong2 v = __ldg(reinterpret_cast<const ulonglong2*>(phases + j * 8) + i);
+    ph[2 * i] = v.x;
+    ph[2 * i + 1] = v.y;
+  }
+}
+
+__device__ __forceinline__ void angles(const uint64_t (&ph)[8], int pos, float scale, int inverse,
+                                       float (&co)[8], float (&si)[8]) {
+  constexpr float kTurn = 1.4629180792671596e-09f;     // 2 pi / 2^32
+  const float ss = inverse ? -scale : scale;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t turn = (uint64_t)(int64_t)pos * ph[i];
+    const float a = (float)(int32_t)(turn >> 32) * kTurn;
+    float s, c;
+    __sincosf(a, &s, &c);
+    co[i] = c * scale;
+    si[i] = s * ss;
+  }
+}
+
+// x[0..8) and x[8..16) are the unit's two vectors.
+__device__ __forceinline__ void rotate16(float (&x)[16], const float (&co)[8],
+                                         const float (&si)[8], int interleaved) {
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = x[2 * i], b = x[2 * i + 1];
+      x[2 * i] = a * co[i] - b * si[i];
+      x[2 * i + 1] = a * si[i] + b * co[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = x[i], b = x[i + 8];
+      x[i] = a * co[i] - b * si[i];
+      x[i + 8] = a * si[i] + b * co[i];
+    }
+  }
+}
+
+__device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float (&x)[16]) {
+  unpack8(a, x);
+  unpack8(b, x + 8);
+}
+
+// Unit `u` of the rotation of q (heads [0, Hq)) and k (heads [Hq, Hq + Hk)):
+// vector pair j of the kHeads heads of one group of one token.
+__device__ __forceinline__ void rotate_unit(const RotArgs& p, int64_t u) {
+  const int J = 1 << p.log_j;
+  const int H = p.Hq + p.Hk, groups = (H + kHeads - 1) / kHeads;
+  const int j = (int)(u & (J - 1));
+  const int64_t rest = u >> p.log_j;
+  const int64_t tok = rest / groups;
+  if (tok >= p.T) return;
+  const int h0 = (int)(rest - tok * groups) * kHeads;
+  int oa, ob;
+  unit_offsets(j, p.rot, p.interleaved, oa, ob);
+  const bool turn = j * 16 < p.rot;
+  const int d = 16 << p.log_j;
+  uint4 a[kHeads], b[kHeads];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    const int h = h0 + i;
+    if (h < H) {
+      const __nv_bfloat16* src = h < p.Hq ? p.q + tok * p.q_stride + h * d
+                                          : p.k + tok * p.k_stride + (h - p.Hq) * d;
+      // Plain loads: the output may be the input itself.
+      a[i] = *reinterpret_cast<const uint4*>(src + oa);
+      b[i] = *reinterpret_cast<const uint4*>(src + ob);
+    }
+  }
+  float co[8], si[8];
+  if (turn) {
+    uint64_t ph[8];
+    load_phases(p.phases, j, ph);
+    angles(ph, __ldg(p.positions + tok), p.scale, p.inverse, co, si);
+  }
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    const int h = h0 + i;
+    if (h < H) {
+      __nv_bfloat16* dst = h < p.Hq ? p.q_out + tok * p.q_out_stride + h * d
+                                    : p.k_out + tok * p.k_out_stride + (h - p.Hq) * d;
+      if (turn) {
+        float x[16];
+        unpack16(a[i], b[i], x);
+        rotate16(x, co, si, p.interleaved);
+        a[i] = pack8(x);
+        b[i] = pack8(x + 8);
+      }
+      *reinterpret_cast<uint4*>(dst + oa) = a[i];
+      *reinterpret_cast<uint4*>(dst + ob) = b[i];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotArgs p) {
+  pdl_wait();
+  pdl_trigger();
+  rotate_unit(p, (int64_t)blockIdx.x * kRotThreads + threadIdx.x);
+}
+
+// ---------------------------------------------------------------------------
+// Append to the cache.
+//
+// One CTA per (page piece, head, K or V): a block of at most 128 tokens x 256
+// values is held in registers between the reduction that gives its scale and
+// the rounding, so k and v are read once. The scale is the smallest power of
+// two that brings the largest finite magnitude of the piece within 448 (for a
+// rotated k with the headroom of the rotation, so that it follows from the
+// inputs' exponents alone and no rounding can move it). Powers of two cost an
+// 8-bit float nothing: only its exponent field moves. A block that already
+// holds tokens keeps the larger of the two scales, and where it grew its older
+// codes are rounded once more to the coarser grid of subnormals.
+// ---------------------------------------------------------------------------
+struct AppendArgs {
+  RotArgs r;                            // q only: Hk = 0 in the rotation
+  const __nv_bfloat16 *k, *v;
+  int64_t k_stride, v_stride;
+  const gdn_page_piece_t* pieces;
+  const int32_t* num_pieces;
+  int piece_cap, Hk, log_b, num_blocks, k_grow;
+  uint8_t *kc, *vc;
+  float *ks, *vs;
+  int q_ctas;
+};
+
+constexpr int kMinExp = -100;           // smallest exponent of a scale
+
+// Smallest e with top <= 448 * 2^e, 448 = 0.875 * 2^9.
+__device__ __forceinline__ int scale_exp(float top, int grow) {
+  if (!(top > 0.f)) return kMinExp;
+  int ex;
+  const float m = frexpf(top, &ex);
+  return max(kMinExp, ex - 9 + (m > 0.875f ? 1 : 0) + grow);
+}
+
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+__device__ __forceinline__ uint2 to_codes8(const float* x, float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv),
+                                    __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3);
+  return __half2float(__half(h));
+}
+
+// Largest finite magnitude of 8 BF16 values.
+__device__ __forceinline__ float finite_max8(const uint4& u, float m) {
+  float f[8];
+  unpack8(u, f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = fabsf(f[i]);
+    m = fmaxf(m, x <= 3.4e38f ? x : 0.f);          // NaN and infinities do not count
+  }
+  return m;
+}
+
+template <int kPasses>
+__device__ __forceinline__ void append_piece(const AppendArgs& p, int unit, float* red) {
+  const int is_v = unit & 1;
+  const int rest = unit >> 1;
+  const int head = rest % p.Hk, pi = rest / p.Hk;
+  if (pi >= __ldg(p.num_pieces)) return;
+  const int4 pc = __ldg(reinterpret_cast<const int4*>(p.pieces) + pi);
+  const int block = pc.x, first = pc.y, len = pc.z, off = pc.w;
+  const int B = 1 << p.log_b;
+  if (block < 0 || block >= p.num_blocks || off < 0 || len <= 0 || off + len > B || first < 0 ||
+      first + len > p.r.T)
+    return;
+  const int J = 1 << p.r.log_j, d = 16 << p.r.log_j;
+  const int j = threadIdx.x & (J - 1), row0 = threadIdx.x >> p.r.log_j;
+  const int rows = kRotThreads >> p.r.log_j;
+  const int rot = is_v ? 0 : p.r.rot;
+  int oa, ob;
+  unit_offsets(j, rot, p.r.interleaved, oa, ob);
+  const __nv_bfloat16* src = (is_v ? p.v + (int64_t)first * p.v_stride
+                                   : p.k + (int64_t)first * p.k_stride) + head * d;
+  const int64_t stride = is_v ? p.v_stride : p.k_stride;
+  uint4 a[kPasses], b[kPasses];
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = row0 + i * rows;
+    a[i] = b[i] = make_uint4(0, 0, 0, 0);
+    if (r < len) {
+      a[i] = ldg16(src + r * stride + oa);
+      b[i] = ldg16(src + r * stride + ob);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) top = finite_max8(b[i], finite_max8(a[i], top));
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
+  float* scale_at = (is_v ? p.vs : p.ks) + (int64_t)block * p.Hk + head;
+  const float old = off > 0 ? *scale_at : 0.f;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kRotThreads / 32; ++i) top = fmaxf(top, red[i]);
+  const int e = scale_exp(top, is_v ? 0 : p.k_grow);
+  const float scale = fmaxf(pow2i(min(e, 127)), old);
+  uint8_t* page = (is_v ? p.vc : p.kc) + ((int64_t)block * p.Hk + head) * ((int64_t)B * d);
+  if (off > 0 && scale != old) {
+    // The tokens that the block held, on the grown scale.
+    const float ratio = old / scale;
+    for (int i = threadIdx.x; i < off * d / 4; i += kRotThreads) {
+      uint32_t w = reinterpret_cast<uint32_t*>(page)[i], o = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float x = e4m3_value((w >> (8 * c)) & 0xffu) * ratio;
+        o |= (uint32_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3) << (8 * c);
+      }
+      reinterpret_cast<uint32_t*>(page)[i] = o;
+    }
+  }
+  if (threadIdx.x == 0) *scale_at = scale;
+  const float inv = 1.f / scale;
+  const bool turn = j * 16 < rot;
+  uint64_t ph[8];
+  if (turn) load_phases(p.r.phases, j, ph);
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = row0 + i * rows;
+    if (r < len) {
+      float x[16];
+      unpack16(a[i], b[i], x);
+      if (turn) {
+        float co[8], si[8];
+        angles(ph, __ldg(p.r.positions + first + r), p.r.scale, p.r.inverse, co, si);
+        rotate16(x, co, si, p.r.interleaved);
+      }
+      uint8_t* dst = page + (int64_t)(off + r) * d;
+      *reinterpret_cast<uint2*>(dst + oa) = to_codes8(x, inv);
+      *reinterpret_cast<uint2*>(dst + ob) = to_codes8(x + 8, inv);
+    }
+  }
+}
+
+// CTAs [0, q_ctas): rotation of q; the others: one unit of the append each.
+template <int kPasses>
+__global__ void __launch_bounds__(kRotThreads) rotary_append_kernel(const AppendArgs p) {
+  __shared__ float red[kRotThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  if ((int)blockIdx.x < p.q_ctas)
+    rotate_unit(p.r, (int64_t)blockIdx.x * kRotThreads + threadIdx.x);
+  else
+    append_piece<kPasses>(p, (int)blockIdx.x - p.q_ctas, red);
+}
+
+int64_t rotary_units(int T, int H, int log_j) {
+  return ((int64_t)T * ((H + kHeads - 1) / kHeads)) << log_j;
+}
+
+RotArgs rot_args(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                 const int32_t* positions, const int64_t* phases, void* q_out,
+                 int64_t q_out_stride, void* k_out, int64_t k_out_stride, int T, int Hq, int Hk,
+                 int d, int rot, float scale, int interleaved, int inverse) {
+  RotArgs r;
+  r.q = static_cast<const __nv_bfloat16*>(q);
+  r.k = static_cast<const __nv_bfloat16*>(k);
+  r.q_out = static_cast<__nv_bfloat16*>(q_out);
+  r.k_out = static_cast<__nv_bfloat16*>(k_out);
+  r.q_stride = q_stride;
+  r.k_stride = k_stride;
+  r.q_out_stride = q_out_stride;
+  r.k_out_stride = k_out_stride;
+  r.positions = positions;
+  r.phases = reinterpret_cast<const uint64_t*>(phases);
+  r.T = T;
+  r.Hq = Hq;
+  r.Hk = Hk;
+  r.log_j = __builtin_ctz((unsigned)d / 16u);
+  r.rot = rot;
+  r.scale = scale;
+  r.interleaved = interleaved;
+  r.inverse = inverse;
+  return r;
+}
+
+}  // namespace
+
+gdn_status_t launch_rotary(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const int32_t* positions, const int64_t* phases, void* q_out,
+                           int64_t q_out_stride, void* k_out, int64_t k_out_stride, int32_t T,
+                           int32_t Hq, int32_t Hk, int32_t d, int32_t rot, float scale,
+                           int32_t interleaved, int32_t inverse, cudaStream_t st) {
+  const RotArgs r = rot_args(q, q_stride, k, k_stride, positions, phases, q_out, q_out_stride,
+                             k_out, k_out_stride, T, Hq, Hk, d, rot, scale, interleaved, inverse);
+  const int64_t ctas = (rotary_units(T, Hq + Hk, r.log_j) + kRotThreads - 1) / kRotThreads;
+  if (ctas > 0x7fffffff) return GDN_ERR_UNSUPPORTED;
+  return check_launch(launch_pdl(rotary_kernel, dim3((unsigned)ctas), dim3(kRotThreads), 0, st, r));
+}
+
+gdn_status_t launch_rotary_kv_append(const void* q, int64_t q_stride, const void* k,
+                                     int64_t k_stride, const void* v, int64_t v_stride,
+                                     const int32_t* positions, const int64_t* phases,
+                                     const gdn_page_piece_t* pieces, const int32_t* num_pieces,
+                                     int32_t piece_cap, void* q_out, int64_t q_out_stride,
+                                     void* kc, void* vc, float* ks, float* vs, int32_t num_blocks,
+                                     int32_t block_tokens, int32_t T, int32_t Hq, int32_t Hk,
+                                     int32_t d, int32_t rot, float scale, int32_t interleaved,
+                                     cudaStream_t st) {
+  AppendArgs p;
+  p.r = rot_args(q, q_stride, nullptr, 0, positions, phases, q_out, q_out_stride, nullptr, 0, T,
+                 Hq, 0, d, rot, scale, interleaved, 0);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.pieces = pieces;
+  p.num_pieces = num_pieces;
+  p.piece_cap = piece_cap;
+  p.Hk = Hk;
+  p.log_b = __builtin_ctz((unsigned)block_tokens);
+  p.num_blocks = num_blocks;
+  // A rotation grows a coordinate by sqrt(2) at most, and `scale` multiplies it.
+  int grow = 0;
+  if (rot > 0) {
+    grow = 1;
+    for (float s = 1.f; s < scale; s *= 2.f) ++grow;
+    for (float s = 0.5f; s >= scale; s *= 0.5f) --grow;
+  }
+  p.k_grow = grow;
+  p.kc = static_cast<uint8_t*>(kc);
+  p.vc = static_cast<uint8_t*>(vc);
+  p.ks = ks;
+  p.vs = vs;
+  const int64_t q_ctas = q ? (rotary_units(T, Hq, p.r.log_j) + kRotThreads - 1) / kRotThreads : 0;
+  const int64_t ctas = q_ctas + 2 * (int64_t)piece_cap * Hk;
+  if (ctas > 0x7fffffff) return GDN_ERR_UNSUPPORTED;
+  if (ctas == 0) return GDN_OK;
+  p.q_ctas = (int)q_ctas;
+  const int passes = block_tokens * d / 16 / kRotThreads;
+  auto kern = passes <= 1   ? rotary_append_kernel<1>
+              : passes == 2 ? rotary_append_kernel<2>
+              : passes == 4 ? rotary_append_kernel<4>
+                            : rotary_append_kernel<8>;
+  return check_launch(launch_pdl(kern, dim3((unsigned)ctas), dim3(kRotThreads), 0, st, p));
+}
+
+}  // namespace gdn

@@ -44,6 +44,13 @@ EXPORTED_SYMBOLS = (
     "gdn_causal_conv1d_update_slots",
     "gdn_delta_rule_decode_slots",
     "gdn_delta_rule_prefill_chunked_slots",
+    "gdn_build_block_tables",
+    "gdn_rotary_phases",
+    "gdn_rotary",
+    "gdn_rotary_kv_append",
+    "gdn_paged_attention_workspace_size",
+    "gdn_paged_attention_plan",
+    "gdn_paged_attention",
     "gdn_selftest_bounded_wait",
     "gdn_device_status",
     "gdn_status_string",
@@ -64,6 +71,8 @@ _LIB = None
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
+_F32 = ctypes.c_float
+_F64 = ctypes.c_double
 
 _SIGNATURES = {
     "gdn_build_conv_chunks": (ctypes.c_int, [_P, _I32, _I32, _P, _I32, _P, _P, _P]),
@@ -97,6 +106,20 @@ _SIGNATURES = {
                                                             _I32, _I32, _P, _P, _P, _I32, _I32,
                                                             _I32, _I32, _I32, _I32, _P,
                                                             ctypes.c_size_t, _P, _I32, _P]),
+    "gdn_build_block_tables": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _I32, _P, _I64, _I32,
+                                              _P, _P, _P, _P, _I32, _P, _P, _P]),
+    "gdn_rotary_phases": (ctypes.c_int, [_I32, _F64, _I32, _F64, _F64, _F64, _F64, _P]),
+    "gdn_rotary": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _I64, _I32, _I32,
+                                  _I32, _I32, _I32, _I32, _I32, _F32, _P]),
+    "gdn_rotary_kv_append": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I32,
+                                            _P, _I64, _P, _P, _P, _P, _I32, _I32, _I32, _I32,
+                                            _I32, _I32, _I32, _I32, _F32, _P]),
+    "gdn_paged_attention_workspace_size": (ctypes.c_size_t, [_I32, _I32, _I32, _I32, _I32]),
+    "gdn_paged_attention_plan": (ctypes.c_int, [_P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                                                _I32, _P, ctypes.c_size_t, _P]),
+    "gdn_paged_attention": (ctypes.c_int, [_P, _I64, _P, _P, _P, _P, _I32, _I32, _P, _I64, _I32,
+                                           _P, _P, _I32, _I32, _I32, _P, _I32, _I32, _I32, _F32,
+                                           _I32, _P, ctypes.c_size_t, _P]),
     "gdn_selftest_bounded_wait": (ctypes.c_int, [_P, _I64, _P]),
     "gdn_device_status": (ctypes.c_int, [_P, _I32, _P]),
     "gdn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -336,6 +359,161 @@ def delta_rule_prefill_chunked_slots(q, k, v, a, b, cu_seqlens, S, has_initial_s
         _ptr(cu_seqlens), N, T, _ptr(S), _ptr(has_initial_state), _ptr(o), Hk, Hv, dk, dv,
         chunk, _flags(qk_l2norm, gate_logits), _ptr(workspace), nbytes, _ptr(state_indices), ns, _stream(stream))
     _check(rc, "gdn_delta_rule_prefill_chunked_slots")
+
+
+# ----------------------------------------------------------------------------
+# Softmax-attention layers over a paged 8-bit cache. The cache of one layer:
+# k_cache, v_cache [num_blocks, Hk, B, d] of e4m3 codes (torch.float8_e4m3fn or
+# uint8), k_scale, v_scale [num_blocks, Hk] float32, all contiguous; B is 16,
+# 32, 64 or 128 tokens.
+# ----------------------------------------------------------------------------
+
+ROTARY_SCALINGS = {"plain": 0, "linear": 1, "by_parts": 2}
+
+
+def _heads(t, name: str):
+    """Token stride of a [T, H, d] tensor whose heads are contiguous."""
+    if t.dtype != torch.bfloat16 or (t.shape[2] > 1 and t.stride(2) != 1) or (
+            t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name}: bfloat16 [T, H, d] with contiguous heads expected")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale):
+    for c in (k_cache, v_cache):
+        if c.element_size() != 1 or not c.is_contiguous() or c.shape != k_cache.shape:
+            raise ValueError("k_cache, v_cache: contiguous 8-bit [num_blocks, Hk, B, d] expected")
+    for s in (k_scale, v_scale):
+        if s.dtype != torch.float32 or not s.is_contiguous() or s.shape != k_cache.shape[:2]:
+            raise ValueError("k_scale, v_scale: contiguous float32 [num_blocks, Hk] expected")
+
+
+def _ints(t, name: str, dtype=torch.int32):
+    if t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} expected")
+    return t.data_ptr()
+
+
+def build_block_tables(cu_seqlens, context_lens, free_blocks, block_table, kv_lens, positions,
+                       slots, pieces, counts, *, block_tokens: int, device_status=None,
+                       stream=None):
+    """Block tables, positions, slots and page pieces of one engine step.
+
+    cu_seqlens int32 [N+1] (new tokens), context_lens int32 [N], free_blocks
+    int32 [F]; block_table int32 [N, M] (rows extended in place). Outputs:
+    kv_lens int32 [N], positions int32 [T], slots int64 [T], pieces int32
+    [capacity, 4] ({block, tok_start, len, offset}; T // block_tokens + 2 N
+    always suffice), counts int32 [2] (pieces, blocks taken)."""
+    if block_table.dtype != torch.int32 or block_table.stride(1) != 1:
+        raise ValueError("block_table: int32 [N, M] with contiguous rows expected")
+    N = cu_seqlens.numel() - 1
+    if (context_lens.numel(), block_table.shape[0], kv_lens.numel()) != (N, N, N) or (
+            slots.numel() != positions.numel()) or counts.numel() < 2 or pieces.shape[1] != 4:
+        raise ValueError("build_block_tables: sizes do not agree")
+    rc = _lib().gdn_build_block_tables(
+        _ints(cu_seqlens, "cu_seqlens"), _ints(context_lens, "context_lens"),
+        _ints(free_blocks, "free_blocks"), free_blocks.numel(), N, positions.numel(),
+        block_tokens, block_table.data_ptr(), max(block_table.stride(0), block_table.shape[1]),
+        block_table.shape[1], _ints(kv_lens, "kv_lens"), _ints(positions, "positions"),
+        _ints(slots, "slots", torch.int64), _ints(pieces, "pieces"), pieces.shape[0],
+        _ints(counts, "counts"), _ptr(device_status), _stream(stream))
+    _check(rc, "gdn_build_block_tables")
+
+
+def rotary_phases(rot_dim: int, base: float, *, scaling: str = "plain", factor: float = 1.0,
+                  original_length: float = 0.0, fast: float = 32.0, slow: float = 1.0,
+                  device="cuda"):
+    """Turns per token of each rotary pair, int64 [rot_dim // 2] on ``device``
+    (64-bit fixed point). scaling: "plain", "linear" or "by_parts"."""
+    out = torch.empty(rot_dim // 2, dtype=torch.int64)
+    rc = _lib().gdn_rotary_phases(rot_dim, base, ROTARY_SCALINGS[scaling], factor,
+                                  original_length, fast, slow, out.data_ptr())
+    _check(rc, "gdn_rotary_phases")
+    return out.to(device)
+
+
+def rotary(q, k, positions, phases, q_out, k_out, *, interleaved: bool = False,
+           inverse: bool = False, scale: float = 1.0, stream=None):
+    """Rotary positions on q [T, Hq, d] and k [T, Hk, d] (k and k_out may be
+    None) into q_out, k_out (which may be q, k). positions int32 [T], phases
+    int64 [rot_dim // 2]. ``inverse`` turns the other way (the gradient)."""
+    T, Hq, d = q.shape
+    Hk = 0 if k is None else k.shape[1]
+    if q_out.shape != q.shape or positions.numel() != T or (
+            k is not None and (k.shape != (T, Hk, d) or k_out.shape != k.shape)):
+        raise ValueError("rotary: shapes do not agree")
+    rc = _lib().gdn_rotary(
+        _ptr(q), _heads(q, "q"), _ptr(k), 0 if k is None else _heads(k, "k"),
+        _ints(positions, "positions"), _ints(phases, "phases", torch.int64), _ptr(q_out),
+        _heads(q_out, "q_out"), _ptr(k_out), 0 if k is None else _heads(k_out, "k_out"), T, Hq,
+        Hk, d, 2 * phases.numel(), int(interleaved), int(inverse), scale, _stream(stream))
+    _check(rc, "gdn_rotary")
+
+
+def rotary_kv_append(q, k, v, positions, phases, pieces, num_pieces, q_out, k_cache, v_cache,
+                     k_scale, v_scale, *, interleaved: bool = False, scale: float = 1.0,
+                     stream=None):
+    """Rotate q into q_out, rotate k, and append k and v [T, Hk, d] to the
+    cache by the step's page pieces (build_block_tables; num_pieces = counts).
+    phases None appends without rotation; q and q_out may then be None."""
+    T, Hk, d = k.shape
+    rot = 0 if phases is None else 2 * phases.numel()
+    Hq = 0 if q is None else q.shape[1]
+    _cache(k_cache, v_cache, k_scale, v_scale)
+    if v.shape != k.shape or k_cache.shape[1] != Hk or k_cache.shape[3] != d or (
+            rot and positions.numel() != T) or (
+            q is not None and (q.shape != (T, Hq, d) or q_out.shape != q.shape)):
+        raise ValueError("rotary_kv_append: shapes do not agree")
+    rc = _lib().gdn_rotary_kv_append(
+        _ptr(q), 0 if q is None else _heads(q, "q"), _ptr(k), _heads(k, "k"), _ptr(v),
+        _heads(v, "v"), _ints(positions, "positions") if rot else None,
+        _ints(phases, "phases", torch.int64) if rot else None, _ints(pieces, "pieces"),
+        _ints(num_pieces, "num_pieces"), pieces.shape[0], _ptr(q_out),
+        0 if q is None else _heads(q_out, "q_out"), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+        _ptr(v_scale), k_cache.shape[0], k_cache.shape[2], T, Hq, Hk, d, rot, int(interleaved),
+        scale, _stream(stream))
+    _check(rc, "gdn_rotary_kv_append")
+
+
+def paged_attention_workspace_size(T: int, N: int, Hq: int, Hk: int, d: int) -> int:
+    return int(_lib().gdn_paged_attention_workspace_size(T, N, Hq, Hk, d))
+
+
+def paged_attention_plan(cu_seqlens, kv_lens, workspace, *, T: int, Hq: int, Hk: int, d: int,
+                         block_tokens: int, max_blocks: int, max_new_tokens: int, stream=None):
+    """Build the step's row tiles into ``workspace``; the step's attention
+    calls then pass planned=True. max_blocks = block_table.shape[1]."""
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    rc = _lib().gdn_paged_attention_plan(
+        _ints(cu_seqlens, "cu_seqlens"), _ints(kv_lens, "kv_lens"), cu_seqlens.numel() - 1, T,
+        Hq, Hk, d, block_tokens, max_blocks, max_new_tokens, _ptr(workspace), nbytes,
+        _stream(stream))
+    _check(rc, "gdn_paged_attention_plan")
+
+
+def paged_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, kv_lens, o,
+                    workspace, *, softmax_scale: float, max_new_tokens: int,
+                    planned: bool = False, stream=None):
+    """Causal attention of a step's tokens q [T, Hq, d] over the paged cache
+    that already holds them, into o [T, Hq, d]. block_table int32 [N, M],
+    cu_seqlens int32 [N+1], kv_lens int32 [N]; max_new_tokens bounds the new
+    tokens of a sequence (1 for a decode step)."""
+    T, Hq, d = q.shape
+    N = cu_seqlens.numel() - 1
+    _cache(k_cache, v_cache, k_scale, v_scale)
+    if k_cache.shape[3] != d or o.shape != q.shape or not o.is_contiguous() or (
+            o.dtype != torch.bfloat16) or kv_lens.numel() != N or block_table.shape[0] != N or (
+            block_table.dtype != torch.int32) or block_table.stride(1) != 1:
+        raise ValueError("paged_attention: shapes do not agree")
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    rc = _lib().gdn_paged_attention(
+        _ptr(q), _heads(q, "q"), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+        k_cache.shape[0], k_cache.shape[2], block_table.data_ptr(),
+        max(block_table.stride(0), block_table.shape[1]), block_table.shape[1],
+        _ints(cu_seqlens, "cu_seqlens"), _ints(kv_lens, "kv_lens"), N, T, max_new_tokens,
+        _ptr(o), Hq, k_cache.shape[1], d, softmax_scale, GDN_FLAG_PLANNED if planned else 0,
+        _ptr(workspace), nbytes, _stream(stream))
+    _check(rc, "gdn_paged_attention")
 
 
 def selftest_bounded_wait(device_status, *, max_cycles: int = 2_000_000, stream=None):

@@ -442,6 +442,189 @@ GDN_API gdn_status_t gdn_delta_rule_prefill_chunked_slots(
     int32_t chunk, int32_t flags, void* workspace, size_t workspace_bytes,
     const int32_t* state_indices, int32_t num_slots, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Softmax-attention layers of a hybrid model, beside the GDN layers: block
+ * tables, rotary positions, a paged cache held in 8 bits, and causal attention
+ * over it. One engine step calls
+ *   gdn_build_block_tables       once (every attention layer reuses its maps),
+ *   gdn_paged_attention_plan     once (the row tiles of the step),
+ *   gdn_rotary_kv_append         per layer: q and k rotated, k and v appended,
+ *   gdn_paged_attention          per layer, with GDN_FLAG_PLANNED.
+ *
+ * The cache of one layer is a pool of blocks of B tokens (B = 16, 32, 64 or
+ * 128, the same in all calls):
+ *   k_cache, v_cache  e4m3 [num_blocks, Hk, B, d] contiguous (one byte a value:
+ *                     4 exponent and 3 fraction bits, no infinity),
+ *   k_scale, v_scale  float32 [num_blocks, Hk]: value = code * scale.
+ * Head widths d: 64, 128 and 256. Other widths or block sizes are
+ * GDN_ERR_UNSUPPORTED.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * One page piece: `len` consecutive tokens of a step, from packed token
+ * `tok_start`, that lie in one block from its token `offset` on. 16 bytes.
+ */
+typedef struct gdn_page_piece_t {
+  int32_t block;
+  int32_t tok_start;
+  int32_t len;
+  int32_t offset;
+} gdn_page_piece_t;
+
+/*
+ * Maps of one engine step, from the requests' lengths. Sequence n has
+ * context_lens[n] tokens in its blocks and gets cu_seqlens[n+1] - cu_seqlens[n]
+ * new ones. It takes ceil((context + new) / B) - ceil(context / B) blocks from
+ * the free list, in sequence order from the front of the list, and its row of
+ * the block table is extended by them.
+ *
+ *   cu_seqlens    device int32 [N + 1], from 0 to T, non-decreasing.
+ *   context_lens  device int32 [N], >= 0.
+ *   free_blocks   device int32 [num_free]: blocks that may be taken.
+ *   block_table   device int32 [N, table_stride], read and written: entries
+ *                 [0, ceil(context / B)) of a row are read, the taken blocks are
+ *                 written behind them, other entries are left alone.
+ *   max_blocks    entries of a row that may be used (<= table_stride).
+ *   kv_lens       device int32 [N] (output): context + new.
+ *   positions     device int32 [T] (output): the position of each token in its
+ *                 sequence.
+ *   slots         device int64 [T] (output): block * B + position % B.
+ *   pieces        device gdn_page_piece_t [piece_capacity], 16-byte aligned
+ *                 (output), sequence-major, positions ascending; at most
+ *                 floor(T / B) + 2 N are written.
+ *   counts        device int32 [2] (output): pieces written, blocks taken.
+ *   device_status device int32 [1] or NULL (output): GDN_OK, or
+ *                 GDN_ERR_INVALID_ARG for malformed lengths, or
+ *                 GDN_ERR_WORKSPACE when the free list, a row of the table or
+ *                 `pieces` is too short. In both cases the counts are 0, every
+ *                 slot is -1, and nothing else is written.
+ * One launch. N = 0 enqueues nothing; T = 0 writes kv_lens and the counts.
+ */
+GDN_API gdn_status_t gdn_build_block_tables(
+    const int32_t* cu_seqlens, const int32_t* context_lens, const int32_t* free_blocks,
+    int32_t num_free, int32_t N, int32_t T, int32_t block_tokens, int32_t* block_table,
+    int64_t table_stride, int32_t max_blocks, int32_t* kv_lens, int32_t* positions,
+    int64_t* slots, gdn_page_piece_t* pieces, int32_t piece_capacity, int32_t* counts,
+    int32_t* device_status, void* stream);
+
+/* Scaling of the rotary frequencies f_i = base^(-2 i / rot_dim). */
+#define GDN_ROTARY_PLAIN 0    /* none */
+#define GDN_ROTARY_LINEAR 1   /* f_i / factor */
+#define GDN_ROTARY_BY_PARTS 2 /* f_i / factor where the wavelength is long against the
+                               * original context, f_i where it is short, a linear
+                               * ramp over the pairs between */
+
+/*
+ * Turns per token of each rotary pair, as 64-bit fixed point fractions (bit
+ * patterns of floor(f_i / (2 pi) * 2^64)). Host only: `phases` is HOST memory,
+ * int64 [rot_dim / 2]; copy it to the device once.
+ *   rot_dim          rotated values of a head: a multiple of 16, at most 256.
+ *   base, factor     > 1 and >= 1.
+ *   original_length  GDN_ROTARY_BY_PARTS: the context that the frequencies were
+ *                    made for; pairs that turn more than `fast` times over it
+ *                    keep f_i, pairs that turn less than `slow` times are
+ *                    divided (fast > slow > 0). Ignored otherwise.
+ */
+GDN_API gdn_status_t gdn_rotary_phases(int32_t rot_dim, double base, int32_t scaling,
+                                       double factor, double original_length, double fast,
+                                       double slow, int64_t* phases);
+
+/*
+ * Rotary positions on q and k. Pair i of a head turns by positions[t] *
+ * phases[i] turns (the 64-bit product wraps, so the angle is exact for every
+ * position) and is multiplied by `scale`; values from rot_dim on are copied.
+ *
+ *   q, k        BF16; element (t, h, i) at t * stride + h * d + i. k may be NULL
+ *               with Hk = 0. The outputs have strides of their own; an output
+ *               may be its input (same pointer and stride), else they must not
+ *               overlap.
+ *   positions   device int32 [T].   phases  device int64 [rot_dim / 2], 16-byte
+ *               aligned (gdn_rotary_phases).
+ *   d           16, 32, 64, 128 or 256.  rot_dim  a multiple of 16, at most d.
+ *   interleaved 1: pairs (2 i, 2 i + 1); 0: pairs (i, i + rot_dim / 2).
+ *   inverse     1 turns the other way: the gradient of q and k from those of
+ *               the outputs.
+ *   scale       > 0, at most 1024.
+ */
+GDN_API gdn_status_t gdn_rotary(const void* q, int64_t q_stride, const void* k,
+                                int64_t k_stride, const int32_t* positions,
+                                const int64_t* phases, void* q_out, int64_t q_out_stride,
+                                void* k_out, int64_t k_out_stride, int32_t T, int32_t Hq,
+                                int32_t Hk, int32_t d, int32_t rot_dim, int32_t interleaved,
+                                int32_t inverse, float scale, void* stream);
+
+/*
+ * Rotary positions on q and k, and the append of k and v to the cache, in one
+ * launch: q goes to q_out as in gdn_rotary, the rotated k and v are written as
+ * codes by the step's pieces.
+ *
+ * Scales are powers of two, at least 2^-100. A piece that begins its block
+ * (offset 0) sets the block's scale from its own tokens: the smallest power of
+ * two that brings their largest finite magnitude to at most 448 (for a rotated
+ * k, times 2 * 2^ceil(log2 scale): the most that the rotation can add). A piece
+ * that continues a block keeps the larger of the block's scale and its own; if
+ * the scale grew, the codes before `offset` are rounded to it. Rounding is to
+ * nearest even; infinities become +-448 * scale and NaN stays NaN.
+ *
+ *   v           BF16 like k.   rot_dim  0 appends without rotation (q and q_out
+ *               may then be NULL: nothing is done to q).
+ *   pieces, num_pieces, piece_capacity  from gdn_build_block_tables (num_pieces
+ *               = its counts). Pieces outside the cache or the step are skipped.
+ *   The other arguments as above; distinct pieces must name distinct blocks.
+ */
+GDN_API gdn_status_t gdn_rotary_kv_append(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, const int32_t* positions, const int64_t* phases,
+    const gdn_page_piece_t* pieces, const int32_t* num_pieces, int32_t piece_capacity,
+    void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache, float* k_scale,
+    float* v_scale, int32_t num_blocks, int32_t block_tokens, int32_t T, int32_t Hq,
+    int32_t Hk, int32_t d, int32_t rot_dim, int32_t interleaved, float scale, void* stream);
+
+/*
+ * Bytes of device workspace that the attention of such a step needs (0 for
+ * invalid sizes). Pure host arithmetic. The workspace is 256-byte aligned; one
+ * step uses it at a time.
+ */
+GDN_API size_t gdn_paged_attention_workspace_size(int32_t T, int32_t N, int32_t Hq, int32_t Hk,
+                                                  int32_t d);
+
+/*
+ * The step's row tiles, built into the workspace once and shared by the
+ * gdn_paged_attention calls of every layer with GDN_FLAG_PLANNED. The arguments
+ * are those of the calls that follow.
+ */
+GDN_API gdn_status_t gdn_paged_attention_plan(const int32_t* cu_seqlens, const int32_t* kv_lens,
+                                              int32_t N, int32_t T, int32_t Hq, int32_t Hk,
+                                              int32_t d, int32_t block_tokens,
+                                              int32_t max_blocks, int32_t max_new_tokens,
+                                              void* workspace, size_t workspace_bytes,
+                                              void* stream);
+
+/*
+ * Causal attention of a step's tokens over the cache that already holds them:
+ * token i of sequence n (l_n new ones) sees keys [0, kv_lens[n] - l_n + i + 1),
+ *   o = sum_j p_j v_j,  p = softmax(softmax_scale * q . k_j),
+ * with query head h on kv head h / (Hq / Hk). A token that sees no key gets
+ * zeros. Bytes of the cache past a sequence's end are never used, whatever they
+ * hold. Scales may be any positive numbers from 2^-100 to 2^100.
+ *
+ *   q           BF16 as above.   o  BF16 [T, Hq, d] contiguous (output).
+ *   block_table device int32 [N, table_stride], row n naming the blocks of
+ *               sequence n; kv_lens beyond max_blocks * B are cut off there. A
+ *               block outside [0, num_blocks) reads as zeros and is reported as
+ *               GDN_ERR_INVALID_ARG by gdn_device_status.
+ *   max_new_tokens  an upper bound of the l_n (1 for a decode step).
+ *   flags       0 or GDN_FLAG_PLANNED.
+ * Sums, maxima and the accumulator are float32. Hq % Hk == 0, Hq / Hk <= 16.
+ */
+GDN_API gdn_status_t gdn_paged_attention(
+    const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+    const float* k_scale, const float* v_scale, int32_t num_blocks, int32_t block_tokens,
+    const int32_t* block_table, int64_t table_stride, int32_t max_blocks,
+    const int32_t* cu_seqlens, const int32_t* kv_lens, int32_t N, int32_t T,
+    int32_t max_new_tokens, void* o, int32_t Hq, int32_t Hk, int32_t d, float softmax_scale,
+    int32_t flags, void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * Self-test of the bounded device-side waits every kernel of this library
  * uses on its mbarriers. Launches one CTA that waits, with that same wait, for

@@ -1,0 +1,256 @@
+"""Causal attention over the paged 8-bit cache against a 64-bit form.
+
+Tolerance. The output is rounded to BF16 once: 2^-9 of its magnitude. The weights carry a relative
+error: their rounding to 16-bit floats for the tensor cores (2^-11 with BF16-free f16 operands) and
+the error of the scores (q is represented to 2^-17 of its row's largest magnitude, products are exact,
+float32 accumulation of scores of at most about 16: together below 2^-10). A weight's error e moves the
+output by at most e * sum_j p_j |v_j| =: e * a twice over (numerator and normalisation). So
+    |o - ref| <= 2^-8 |ref| + 2^-8 a + 1e-6 max(a).
+"""
+import numpy as np
+import pytest
+import torch
+
+import attnref as R
+
+pytestmark = pytest.mark.gpu
+
+
+def make(seed, new, kv, Hq, Hk, d, B, *, stale=True, spare=3, extra_cols=2, **cache):
+    """Tensors of a step: sequence n has kv[n] keys in the cache, its last new[n] tokens are queries."""
+    rng = np.random.default_rng(seed)
+    dev = "cuda"
+    N, T = len(new), sum(new)
+    want = [-(-c // B) for c in kv]
+    blocks = sum(want) + spare
+    ids = rng.permutation(blocks)
+    width = max(want + [1]) + extra_cols
+    table = np.full((N, width), blocks - 1, np.int32)
+    at = 0
+    for n, m in enumerate(want):
+        table[n, :m] = ids[at:at + m]
+        at += m
+    kc, vc, ks, vs = R.fill_cache(rng, blocks, Hk, B, d, dev, **cache)
+    if stale:
+        for n, c in enumerate(kv):
+            if c % B:
+                kc.view(torch.uint8)[int(table[n, c // B]), :, c % B:] = 0x7F
+                vc.view(torch.uint8)[int(table[n, c // B]), :, c % B:] = 0xFF
+    qkv = torch.from_numpy(rng.standard_normal((max(T, 1), (Hq + 2 * Hk) * d)).astype(np.float32)).bfloat16().to(dev)
+    q = qkv[:T, Hk * d:(Hk + Hq) * d].view(T, Hq, d)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device=dev)
+    return dict(q=q, kc=kc, vc=vc, ks=ks, vs=vs, table=torch.from_numpy(table).to(dev), cu=cu,
+                kv=torch.tensor(kv, dtype=torch.int32, device=dev), new=new, kvl=kv, scale=d ** -0.5)
+
+
+def run(s, planned=False, workspace=None, **kw):
+    from gated_deltanet_linear_build_gb300 import gdn
+    T, Hq, d = s["q"].shape
+    N, Hk = len(s["new"]), s["kc"].shape[1]
+    o = torch.full((T, Hq, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    if workspace is None:
+        workspace = torch.empty(gdn.paged_attention_workspace_size(T, N, Hq, Hk, d), dtype=torch.uint8,
+                                device="cuda")
+        workspace.fill_(0xA5)
+    gdn.paged_attention(s["q"], s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["cu"], s["kv"], o,
+                        workspace, softmax_scale=s["scale"], max_new_tokens=max(s["new"] + [0]),
+                        planned=planned, **kw)
+    return o
+
+
+def check(s, o):
+    ref, a = R.attention(s["q"], s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["new"], s["kvl"], s["scale"])
+    o = o.cpu().double()
+    assert torch.isfinite(o).all()
+    bad = (o - ref).abs() - (2.0 ** -8 * ref.abs() + 2.0 ** -8 * a + 1e-6 * a.max())
+    assert bad.max() <= 0, (float(bad.max()), np.unravel_index(int(bad.argmax()), bad.shape))
+
+
+HEADS = [(16, 2, 256), (32, 8, 128), (8, 8, 64), (12, 1, 128), (16, 1, 256), (6, 2, 64), (3, 1, 256), (32, 2, 64)]
+
+
+@pytest.mark.parametrize("Hq,Hk,d", HEADS)
+@pytest.mark.parametrize("B", [16, 64])
+def test_decode_lengths(Hq, Hk, d, B):
+    kv = [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 255, 256, 257, 700]
+    s = make(1, [1] * len(kv), kv, Hq, Hk, d, B)
+    check(s, run(s))
+
+
+@pytest.mark.parametrize("B", [16, 32, 64, 128])
+@pytest.mark.parametrize("Hq,Hk,d", [(16, 2, 256), (32, 8, 128), (10, 2, 64)])
+def test_long_contexts_split_over_ctas(Hq, Hk, d, B):
+    s = make(2, [1, 1, 1], [9001, 5, 4096], Hq, Hk, d, B)
+    check(s, run(s))
+
+
+@pytest.mark.parametrize("Hq,Hk,d", HEADS)
+def test_several_tokens_per_sequence(Hq, Hk, d):
+    new = [1, 2, 3, 4, 5, 7, 1, 20]
+    kv = [40, 2, 300, 4, 77, 500, 1, 90]
+    s = make(3, new, kv, Hq, Hk, d, 32)
+    check(s, run(s))
+
+
+@pytest.mark.parametrize("Hq,Hk,d", [(16, 2, 256), (32, 8, 128), (4, 4, 64), (24, 2, 128)])
+@pytest.mark.parametrize("B", [16, 128])
+def test_prefill_and_mixed(Hq, Hk, d, B):
+    new = [129, 1, 64, 1, 200, 33]
+    kv = [129, 300, 500, 1, 201, 33 + 256]
+    s = make(4, new, kv, Hq, Hk, d, B)
+    check(s, run(s))
+
+
+def test_rows_that_see_no_key_are_zero():
+    # More new tokens than keys: the first ones see nothing; and sequences without tokens or keys.
+    new, kv = [4, 0, 3, 2, 0], [2, 7, 0, 50, 0]
+    s = make(5, new, kv, 8, 2, 128, 16)
+    o = run(s)
+    check(s, o)
+    assert (o[:2] == 0).all() and (o[4:7] == 0).all()
+
+
+@pytest.mark.parametrize("new,kv", [([1, 1], [777, 60]), ([150], [400])])
+def test_scales_of_any_size(new, kv):
+    # Blocks whose scales differ by 2^30, and scales that are no powers of two.
+    s = make(6, new, kv, 8, 2, 128, 16, scale_exps=(-40, -10))
+    s["ks"].copy_(torch.full_like(s["ks"], 2.0 ** -7))
+    check(s, run(s))
+    s = make(7, new, kv, 8, 2, 64, 32, odd_scales=True)
+    check(s, run(s))
+
+
+def test_a_flat_tail_behind_a_peak_keeps_its_weight():
+    # One key takes almost all of the softmax; thousands of others share 2^-14 each.
+    s = make(8, [1], [6000], 4, 1, 128, 64)
+    s["kc"].view(torch.uint8)[:] = 0
+    s["q"].fill_(0.0)
+    s["q"][..., 0] = 8.0
+    first = int(s["table"][0, 0])
+    s["ks"].fill_(2.0 ** -6)
+    s["kc"][first, 0, 0, 0] = torch.tensor(448.0, device="cuda").to(torch.float8_e4m3fn)
+    s["scale"] = 14.0 / (8.0 * 448.0 / 64.0) * 0.6931471805599453
+    check(s, run(s))
+
+
+def test_planned_calls_and_reuse_of_a_workspace_give_the_same_bits():
+    from gated_deltanet_linear_build_gb300 import gdn
+    s = make(9, [1] * 9 + [70], [3000, 64, 1, 500, 501, 1000, 31, 9000, 2, 800], 16, 2, 256, 64)
+    T, N = sum(s["new"]), len(s["new"])
+    ws = torch.empty(gdn.paged_attention_workspace_size(T, N, 16, 2, 256), dtype=torch.uint8, device="cuda")
+    a = run(s, workspace=ws)
+    gdn.paged_attention_plan(s["cu"], s["kv"], ws, T=T, Hq=16, Hk=2, d=256, block_tokens=64,
+                             max_blocks=s["table"].shape[1], max_new_tokens=70)
+    for _ in range(5):
+        b = run(s, workspace=ws, planned=True)
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_on_another_stream():
+    s = make(10, [1] * 4, [1000, 70, 3, 400], 8, 2, 128, 32)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        o = run(s)
+    st.synchronize()
+    check(s, o)
+    o2 = run(s, stream=st)
+    st.synchronize()
+    check(s, o2)
+
+
+@pytest.mark.parametrize("new,kv", [([1, 1], [90, 200]), ([40], [90])])
+def test_non_finite_values_stay_where_they_belong(new, kv):
+    # A NaN query row gives NaN rows of its own head and token, nothing else.
+    s = make(11, new, kv, 8, 2, 128, 16)
+    clean = run(s)
+    s["q"][0, 1, 5] = float("inf")
+    s["q"][sum(new) - 1, 6, 0] = float("nan")
+    o = run(s)
+    assert torch.isnan(o[0, 1]).all() and torch.isnan(o[sum(new) - 1, 6]).all()
+    keep = torch.ones(o.shape[:2], dtype=torch.bool, device="cuda")
+    keep[0, 1] = keep[sum(new) - 1, 6] = False
+    assert torch.equal(o[keep], clean[keep])
+
+
+@pytest.mark.parametrize("Hq,Hk,d", [(4, 2, 64), (4, 2, 128), (8, 1, 256), (12, 1, 64)])
+@pytest.mark.parametrize("new,kv", [([3], [100]), ([140], [300]), ([1, 40, 1], [64, 64, 3])])
+def test_non_finite_keys_and_values_reach_only_rows_that_see_them(Hq, Hk, d, new, kv):
+    s = make(12, new, kv, Hq, Hk, d, 16)
+    n = int(np.argmax(new))
+    clean = run(s)
+    first = sum(new[:n])
+    for which, cache in (("k", "kc"), ("v", "vc")):
+        for pos in (kv[n] - 1, kv[n] - new[n] // 2):
+            block, off = int(s["table"][n, pos // 16]), pos % 16
+            saved = s[cache].view(torch.uint8)[block, :, off].clone()
+            s[cache].view(torch.uint8)[block, 0, off, 3] = 0x7F
+            o = run(s)
+            s[cache].view(torch.uint8)[block, :, off] = saved
+            seen = first + pos - (kv[n] - new[n])     # the first token that sees the key
+            keep = torch.ones(sum(new), dtype=torch.bool, device="cuda")
+            keep[seen:first + new[n]] = False
+            assert torch.equal(o[keep], clean[keep]), (which, pos)
+            G = Hq // Hk
+            hit = o[seen:first + new[n], :G]
+            assert torch.isnan(hit).all() if which == "k" else torch.isnan(hit[..., 3]).all(), (which, pos)
+            if which == "v":                          # other values of the head are not touched
+                other = [i for i in range(d) if i != 3]
+                assert torch.equal(hit[..., other], clean[seen:first + new[n], :G][..., other])
+            assert torch.equal(o[:, G:], clean[:, G:])
+
+
+def test_a_block_outside_the_cache_is_reported_and_reads_as_zeros():
+    from gated_deltanet_linear_build_gb300 import gdn
+    st = torch.empty(1, dtype=torch.int32, device="cuda")
+    gdn.device_status(st, clear=True)
+    s = make(13, [1, 1], [40, 40], 4, 1, 64, 16)
+    run(s)
+    gdn.device_status(st)
+    assert int(st) == gdn.GDN_OK
+    s["table"][1, 1] = s["kc"].shape[0]
+    s["table"][0, 0] = -1
+    o = run(s)
+    gdn.device_status(st, clear=True)
+    assert int(st) == gdn.GDN_ERR_INVALID_ARG
+    assert torch.isfinite(o).all()
+    gdn.device_status(st)
+    assert int(st) == gdn.GDN_OK
+
+
+def test_lengths_beyond_the_table_are_cut_off():
+    s = make(14, [1], [64], 4, 1, 64, 16, extra_cols=0)
+    a = run(s)
+    s["kv"].fill_(1 << 30)
+    assert torch.equal(a, run(s))
+
+
+def test_offsets_past_32_bits():
+    # Blocks whose bytes lie beyond 2^32 in the pool.
+    Hk, B, d = 8, 128, 256
+    blocks = (1 << 32) // (Hk * B * d) + 4
+    dev = "cuda"
+    kc = torch.zeros((blocks, Hk, B, d), dtype=torch.uint8, device=dev)
+    vc = torch.zeros_like(kc)
+    s = make(15, [1, 1], [130, 5], 8, Hk, d, B, spare=0, extra_cols=0)
+    small = s["kc"].shape[0]
+    o = run(s)
+    kc[blocks - small:] = s["kc"].view(torch.uint8)
+    vc[blocks - small:] = s["vc"].view(torch.uint8)
+    ks = torch.ones((blocks, Hk), device=dev)
+    vs = torch.ones((blocks, Hk), device=dev)
+    ks[blocks - small:], vs[blocks - small:] = s["ks"], s["vs"]
+    s.update(kc=kc, vc=vc, ks=ks, vs=vs, table=s["table"] + (blocks - small))
+    assert torch.equal(o, run(s))
+
+
+def test_refusals():
+    from gated_deltanet_linear_build_gb300 import gdn
+    s = make(16, [1, 1], [20, 30], 4, 2, 64, 16)
+    with pytest.raises(gdn.GdnError) as e:
+        run(s, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == gdn.GDN_ERR_WORKSPACE
+    for key, bad in (("q", s["q"].float()), ("kc", s["kc"][:, :, ::2]), ("ks", s["ks"].double()),
+                     ("table", s["table"].long()), ("kv", s["kv"].long()), ("cu", s["cu"].long())):
+        with pytest.raises(ValueError):
+            run(dict(s, **{key: bad}))
