@@ -266,7 +266,17 @@ gdn_status_t gdn_paged_attention(const void* q, int64_t q_stride, const void* k_
   a.tiles = reinterpret_cast<attn::Item*>(ws + l.tiles);
   a.split_rows = l.split_rows;
   a.split_grid = attn::split_grid(d);
-  return launch_attn_split(a, st);
+  a.tile_grid = attn::tile_grid();
+  a.tile_counters = reinterpret_cast<int*>(ws + l.tile_counters);
+  a.tile_partials = reinterpret_cast<float*>(ws + l.tile_partials);
+  // The two kernels share a step's sequences by their rows; a step whose
+  // lengths rule one of them out launches the other alone. One sequence is
+  // exactly as long as the step.
+  const int64_t G = Hq / Hk, limit = attn::split_limit((int)G);
+  const int64_t longest = N == 1 ? T : max_new_tokens;
+  if (!(N == 1 && T * G > limit)) rc = launch_attn_split(a, st);
+  if (rc == GDN_OK && longest * G > limit) rc = launch_attn_tile(a, st);
+  return rc;
 }
 
 }  // extern "C"

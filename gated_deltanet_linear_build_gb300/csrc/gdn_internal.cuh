@@ -297,6 +297,7 @@ gdn_status_t gather_status_conv(int32_t* out, int clear, int first, cudaStream_t
 gdn_status_t gather_status_decode(int32_t* out, int clear, int first, cudaStream_t st);
 gdn_status_t gather_status_prefill_tc(int32_t* out, int clear, int first, cudaStream_t st);
 gdn_status_t gather_status_attn_split(int32_t* out, int clear, int first, cudaStream_t st);
+gdn_status_t gather_status_attn_tile(int32_t* out, int clear, int first, cudaStream_t st);
 #define GDN_DEFINE_STATUS_GATHER(name)                                                   \
   gdn_status_t name(int32_t* out, int clear, int first, cudaStream_t st) {               \
     gather_status_kernel<<<1, 1, 0, st>>>(out, clear, first);                            \

@@ -22,18 +22,27 @@ struct Header {
   int num_items;         // row tiles of the split kernel
   int units;             // their kv units, one head's
   int per_cta;           // units per CTA, over all heads
-  int num_tiles;         // row tiles of the tensor-core kernel
-  int ticket;            // its next (tile, head)
-  int pad[59];
+  int num_tiles;         // row tiles of the tensor-core kernel,
+  int tile_units;        // their kv units, one head's,
+  int tile_per_cta;      // units per CTA
+  int pad[58];
 };
 static_assert(sizeof(Header) == 256, "header is 256 bytes");
 
-constexpr int kUnit = 32;              // kv tokens per unit of the split kernel
+constexpr int kUnit = 32;              // keys per unit of the split kernel
+constexpr int kTileKeys = 128;         // keys per unit of the tensor-core kernel
 
 struct Layout {
-  size_t items, counters, partials, tiles, total;
+  size_t items, counters, partials, tiles, tile_counters, tile_partials, total;
   int item_cap, tile_cap, split_rows, tile_rows;
 };
+
+// Rows of a tile of the tensor-core kernel.
+inline int tile_rows(int d) { return d == 256 ? 128 : 256; }
+inline int tile_grid() { return num_sms() < 160 ? num_sms() : 160; }
+
+// Sequences of at most this many rows (new tokens x G) go to the split kernel.
+inline int split_limit(int G) { return 64; }
 
 // Rows of a split tile: 16 where the query heads of a token need more than 8.
 inline int split_rows(int G) { return G > 8 ? 16 : 8; }
@@ -63,7 +72,9 @@ struct Args {
   int* counters;                       // [item][head]: partial results that have arrived
   float* partials;
   Item* tiles;
-  int split_rows, split_grid;
+  int split_rows, split_grid, tile_grid;
+  int* tile_counters;                  // [tile][head][128-row half]
+  float* tile_partials;
 };
 
 // Lengths of sequence n, malformed ones as an empty sequence.
@@ -90,5 +101,6 @@ __device__ __forceinline__ int visible(const Seq& s, int token) {
 gdn_status_t launch_attn_plan(const int32_t* cu, const int32_t* kv, int N, int T, int Hq, int Hk,
                               int d, int64_t kv_max, void* workspace, cudaStream_t st);
 gdn_status_t launch_attn_split(const attn::Args& a, cudaStream_t st);
+gdn_status_t launch_attn_tile(const attn::Args& a, cudaStream_t st);
 
 }  // namespace gdn

@@ -45,7 +45,7 @@ Layout layout(int T, int N, int Hq, int Hk, int d) {
   const int64_t G = Hq / Hk;
   l.split_rows = split_rows((int)G);
   l.item_cap = (int)std::min<int64_t>((int64_t)T * G / l.split_rows + N, 0x7fffffff / 16);
-  l.tile_rows = 128;
+  l.tile_rows = tile_rows(d);
   l.tile_cap = (int)std::min<int64_t>((int64_t)T * G / l.tile_rows + N, 0x7fffffff / 16);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   size_t at = sizeof(Header);
@@ -55,8 +55,12 @@ Layout layout(int T, int N, int Hq, int Hk, int d) {
   at = up(at + (size_t)l.item_cap * Hk * sizeof(int));
   l.tiles = at;
   at = up(at + (size_t)l.tile_cap * sizeof(Item));
+  l.tile_counters = at;
+  at = up(at + (size_t)l.tile_cap * Hk * 2 * sizeof(int));
   l.partials = at;
   at = up(at + (size_t)kSplitGridMax * 2 * (size_t)l.split_rows * (d + 2) * sizeof(float));
+  l.tile_partials = at;
+  at = up(at + (size_t)tile_grid() * 2 * (size_t)l.tile_rows * (d + 2) * sizeof(float));
   l.total = at;
   return l;
 }
@@ -74,11 +78,13 @@ constexpr int kPlanThreads = 1024;
 
 struct PlanArgs {
   const int32_t *cu, *kv;
-  int N, T, G, Hk, rows, item_cap, grid;
+  int N, T, G, Hk, limit;
   int64_t kv_max;
+  int rows, item_cap, grid;            // split kernel
+  int tile_rows, tile_cap, tile_grid;  // tensor-core kernel
   Header* hdr;
-  Item* items;
-  int* counters;
+  Item *items, *tiles;
+  int *counters, *tile_counters;
 };
 
 __device__ __forceinline__ int block_scan(int v, int* sums, int& tot) {
@@ -105,24 +111,29 @@ __device__ __forceinline__ int block_scan(int v, int* sums, int& tot) {
   return v + (w > 0 ? sums[w - 1] : 0);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs p) {
-  __shared__ int sums[32];
-  __shared__ int s_first[kPlanThreads], s_tiles[kPlanThreads];
-  pdl_wait();
-  pdl_trigger();
+// Row tiles of `rows` rows, with units of `keys` keys, of the sequences with
+// more than `above` and at most `upto` rows.
+struct ListArgs {
+  int rows, keys, above, upto, cap, per_item;   // per_item: counters of a tile
+  Item* items;
+  int* counters;
+};
+
+__device__ void build_list(const PlanArgs& p, const ListArgs& a, int* sums, int* s_first,
+                           int& items, int& units) {
   const int tid = threadIdx.x;
-  int items = 0, units = 0;
+  items = units = 0;
   for (int n0 = 0; n0 < p.N; n0 += kPlanThreads) {
     // Tiles of this thread's sequence, then one thread per tile.
     int tiles = 0;
     if (n0 + tid < p.N) {
       const Seq s = seq_of(p.cu, p.kv, n0 + tid, p.T, p.kv_max);
-      tiles = (int)(((int64_t)s.len * p.G + p.rows - 1) / p.rows);
+      const int64_t r = (int64_t)s.len * p.G;
+      if (r > a.above && r <= a.upto) tiles = (int)((r + a.rows - 1) / a.rows);
     }
     int tot;
     const int inc = block_scan(tiles, sums, tot);
     s_first[tid] = inc - tiles;
-    s_tiles[tid] = tiles;
     __syncthreads();
     for (int i0 = 0; i0 < tot; i0 += kPlanThreads) {
       const int i = i0 + tid;
@@ -134,30 +145,46 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
           if (s_first[mid] <= i) lo = mid; else hi = mid - 1;
         }
         it.seq = n0 + lo;
-        it.row0 = (i - s_first[lo]) * p.rows;
+        it.row0 = (i - s_first[lo]) * a.rows;
         const Seq s = seq_of(p.cu, p.kv, it.seq, p.T, p.kv_max);
-        const int last = min(s.len - 1, (it.row0 + p.rows - 1) / p.G);
+        const int last = min(s.len - 1, (it.row0 + a.rows - 1) / p.G);
         // An item without keys still has one unit, which writes its zeros.
-        it.units = max(1, (visible(s, last) + kUnit - 1) / kUnit);
-        if (items + i >= p.item_cap) it.units = 0;     // malformed offsets only
+        it.units = max(1, (visible(s, last) + a.keys - 1) / a.keys);
+        if (items + i >= a.cap) it.units = 0;      // malformed offsets only
       }
       int tot_units;
       const int cum = block_scan(it.units, sums, tot_units);
       it.cum = units + cum - it.units;
-      if (i < tot && items + i < p.item_cap) {
-        p.items[items + i] = it;
-        for (int h = 0; h < p.Hk; ++h) p.counters[(int64_t)(items + i) * p.Hk + h] = 0;
+      if (i < tot && items + i < a.cap) {
+        a.items[items + i] = it;
+        for (int h = 0; h < a.per_item; ++h) a.counters[(int64_t)(items + i) * a.per_item + h] = 0;
       }
       units += tot_units;
     }
     items += tot;
     __syncthreads();
   }
-  if (tid == 0) {
-    p.hdr->num_items = min(items, p.item_cap);
+  items = min(items, a.cap);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs p) {
+  __shared__ int sums[32];
+  __shared__ int s_first[kPlanThreads];
+  pdl_wait();
+  pdl_trigger();
+  int items, units, tiles, tile_units;
+  build_list(p, {p.rows, kUnit, 0, p.limit, p.item_cap, p.Hk, p.items, p.counters}, sums, s_first,
+             items, units);
+  build_list(p, {p.tile_rows, kTileKeys, p.limit, 0x7fffffff, p.tile_cap, 2 * p.Hk, p.tiles,
+                 p.tile_counters}, sums, s_first, tiles, tile_units);
+  if (threadIdx.x == 0) {
+    const int64_t all = (int64_t)units * p.Hk, tile_all = (int64_t)tile_units * p.Hk;
+    p.hdr->num_items = items;
     p.hdr->units = units;
-    const int64_t all = (int64_t)units * p.Hk;
     p.hdr->per_cta = (int)max((int64_t)1, (all + p.grid - 1) / p.grid);
+    p.hdr->num_tiles = tiles;
+    p.hdr->tile_units = tile_units;
+    p.hdr->tile_per_cta = (int)max((int64_t)1, (tile_all + p.tile_grid - 1) / p.tile_grid);
   }
 }
 
@@ -750,6 +777,12 @@ gdn_status_t launch_attn_plan(const int32_t* cu, const int32_t* kv, int N, int T
   p.hdr = reinterpret_cast<Header*>(ws);
   p.items = reinterpret_cast<Item*>(ws + l.items);
   p.counters = reinterpret_cast<int*>(ws + l.counters);
+  p.limit = split_limit(p.G);
+  p.tile_rows = l.tile_rows;
+  p.tile_cap = l.tile_cap;
+  p.tile_grid = tile_grid();
+  p.tiles = reinterpret_cast<Item*>(ws + l.tiles);
+  p.tile_counters = reinterpret_cast<int*>(ws + l.tile_counters);
   return check_launch(launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p));
 }
 

@@ -1,0 +1,820 @@
+// Attention of many query rows over a paged 8-bit cache, on the 5th-generation
+// tensor cores.
+//
+// Bound: 4 d operations per visible (query row, key) pair at the BF16 rate, as
+// long as the softmax (one exponential a pair) and the widening of V keep up.
+// One CTA per SM; a tile is 256 rows (d <= 128: two 128-row halves that take
+// turns on the tensor core) or 128 rows (d = 256, whose float32 output fills
+// half of the tensor memory; two score buffers take turns instead). Per 128
+// keys:
+//
+// * S = Q K^T as e4m3 MMAs (kind::f8f6f4): K as it lies in the cache, Q as the
+//   sum of two e4m3 parts hi + lo, which hold BF16's 8 significand bits. Two
+//   passes at twice the BF16 rate cost what one BF16 pass would, without
+//   widening K.
+// * softmax: one thread per row, scores read once from tensor memory; P goes
+//   back as f16 over the scores' columns and is the A operand of
+// * O += P V (kind::f16). V's codes become f16 (exact) in the registers of the
+//   loading warps on their way to shared memory.
+// * Scales: K's joins the score's factor, V's the exponent, P' = 2^(s + log2 vs
+//   - m), with P' / vs in the sum, per 16 keys (the smallest block). O is
+//   rescaled only when a row's maximum grows by more than 2^8.
+//
+// Work split: as in the split kernel, all (tile, kv head, 128 keys) units form
+// one line cut into equal pieces, one per SM; a tile cut by the end of a piece
+// leaves float32 partial results, joined in a fixed order by the warps that
+// arrive last.
+//
+// Roles (four warpgroups): 0 .. kM - 1: softmax of one 128-row tile each; the
+// others up to 2: copies of K, widening of V; warp 12: MMAs.
+// Shared-memory operands lie as 8 x 16-byte core matrices (no swizzle).
+#include <algorithm>
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "paged_attn.cuh"
+
+namespace gdn {
+namespace {
+using namespace attn;
+
+constexpr int kThreads = 512;
+constexpr int kKeys = kTileKeys;         // keys per unit
+constexpr int kHalf = 64;                // keys per V stage
+// Registers: four warpgroups are launched with 128 a thread; their shares add
+// up to no more than 4 x 128.
+constexpr int kLaunchRegs = 128;
+
+template <int D>
+struct TC {
+  static constexpr int M = D == 256 ? 1 : 2;            // 128-row tiles
+  static constexpr int KS = D == 256 ? 2 : 3;           // K stages of 128 keys
+  static constexpr int VS = D == 256 ? 3 : 6;           // V stages of 64 keys
+  static constexpr int loaders = (3 - M) * 128;
+  static constexpr int q_part = 128 * D;                // one part (hi or lo) of one tile
+  static constexpr int k_stage = kKeys * D;
+  static constexpr int v_stage = kHalf * D * 2;
+  static constexpr int o_q = 0;
+  static constexpr int o_k = o_q + M * 2 * q_part;
+  static constexpr int o_v = o_k + KS * k_stage;
+  // Scales of a unit's 8 groups of 16 keys, float [4 units][ks | log2 vs | 1 / vs][8].
+  // A unit is copied at most 3 units ahead of the softmax that reads its scales.
+  static constexpr int o_sc = o_v + VS * v_stage;
+  // First key of a segment whose V is NaN in a column, uint16 [4 segments][D]. V
+  // is written at most 3 units, hence segments, ahead of the results.
+  static constexpr int o_nan = o_sc + 4 * 24 * 4;
+  static constexpr int o_bar = o_nan + 4 * D * 2;
+  static constexpr int n_bar = 2 * KS + 2 * VS + 4 + 2 + 2 + 2 + 2 + 2 + 2;
+  static constexpr int o_misc = o_bar + n_bar * 8;      // tmem base, abort, flags
+  static constexpr int total = o_misc + 32;
+  static_assert(total <= 232448, "shared memory of one CTA");
+  static constexpr int soft_regs = M == 2 ? 184 : 216, load_regs = M == 2 ? 88 : 120,
+                       mma_regs = 56;
+  static_assert(M * soft_regs + (3 - M) * load_regs + mma_regs <= 4 * kLaunchRegs,
+                "registers of the launch");
+  // Tensor-memory columns.
+  static constexpr int c_s(int i) { return i * 128; }
+  static constexpr int c_o(int m) { return 256 + m * D; }
+};
+
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n"
+      :: "r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+// kind::f8f6f4: e4m3 A and B (format 0), float32 D. kind::f16: f16 A and B.
+__host__ __device__ constexpr uint32_t idesc_f32(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Factor of a score: kept from 0, which would turn a masked score's -inf into
+// NaN (a row's or block's scale may be that small); NaN marks a row and stays.
+__device__ __forceinline__ float factor(float a) { return a < 1e-37f ? 1e-37f : a; }
+
+// 32 columns of this warp's 32 lanes, without the wait.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st32_async(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+         "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
+         "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
+         "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}"
+      : "=r"(r) : "r"(two));
+  return r;
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegs));
+}
+
+// A bounded wait of a whole warp: all lanes go on, or none does.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait_abortable(bar, parity, abort));
+}
+
+// One contiguous run of units of one (tile, head).
+struct Seg {
+  int lo, head, seq, row0, n_units, cum, first_unit, count;
+  Seq s;
+  int n_rows, key_end;
+};
+
+struct Line {
+  int num, units1, per_cta;
+  long long u, u_end;
+};
+
+__device__ __forceinline__ Line line_of(const Args& p) {
+  Line l;
+  l.num = p.hdr->num_tiles;
+  l.units1 = p.hdr->tile_units;
+  l.per_cta = p.hdr->tile_per_cta;
+  const long long total = (long long)l.units1 * p.Hk;
+  l.u = (long long)blockIdx.x * l.per_cta;
+  l.u_end = min(total, l.u + l.per_cta);
+  return l;
+}
+
+__device__ __forceinline__ Seg seg_at(const Args& p, const Line& l, int tile_rows) {
+  Seg g;
+  g.head = (int)(l.u / l.units1);
+  const int x = (int)(l.u - (long long)g.head * l.units1);
+  int lo = 0, hi = l.num - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(&p.tiles[mid].cum) <= x) lo = mid; else hi = mid - 1;
+  }
+  const int4 raw = __ldg(reinterpret_cast<const int4*>(p.tiles) + lo);
+  g.lo = lo;
+  g.seq = raw.x;
+  g.row0 = raw.y;
+  g.n_units = raw.z;
+  g.cum = raw.w;
+  g.first_unit = x - g.cum;
+  g.count = (int)min((long long)(g.n_units - g.first_unit), l.u_end - l.u);
+  g.s = seq_of(p.cu, p.kv, g.seq, p.T, (int64_t)p.max_blocks << p.log_b);
+  const int G = p.Hq / p.Hk;
+  g.n_rows = min(tile_rows, g.s.len * G - g.row0);
+  g.key_end = visible(g.s, (g.row0 + g.n_rows - 1) / G);
+  return g;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const Args p) {
+  using C = TC<D>;
+  constexpr int kM = C::M, kRows = kM * 128;
+  extern __shared__ __align__(128) unsigned char smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::o_bar);
+  uint64_t* k_full = bars;
+  uint64_t* k_empty = k_full + C::KS;
+  uint64_t* v_full = k_empty + C::KS;
+  uint64_t* v_empty = v_full + C::VS;
+  uint64_t* sc_full = v_empty + C::VS;       // [4]
+  uint64_t* s_full = sc_full + 4;            // [2] score buffers
+  uint64_t* p_full = s_full + 2;             // [2]
+  uint64_t* o_done = p_full + 2;             // [kM]
+  uint64_t* q_full = o_done + 2;             // [kM]
+  uint64_t* wg_sync = q_full + 2;            // [kM] a softmax warpgroup among itself
+  uint64_t* nan_sync = wg_sync + 2;          // the loaders among themselves
+  uint64_t* drained = nan_sync + 1;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::o_misc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::o_misc + 4);
+  int* s_flag = reinterpret_cast<int*>(smem + C::o_misc + 8);     // [2] this warpgroup joins
+  volatile int* s_any_nan = reinterpret_cast<volatile int*>(smem + C::o_misc + 16);
+  float* s_sc = reinterpret_cast<float*>(smem + C::o_sc);
+  unsigned short* s_nan = reinterpret_cast<unsigned short*>(smem + C::o_nan);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = tid >> 7;
+  const int G = p.Hq / p.Hk, B = 1 << p.log_b;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::KS; ++i) {
+      tc::mbar_init(k_full + i, C::loaders);
+      tc::mbar_init(k_empty + i, 1);
+    }
+    for (int i = 0; i < C::VS; ++i) {
+      tc::mbar_init(v_full + i, C::loaders);
+      tc::mbar_init(v_empty + i, 1);
+    }
+    for (int i = 0; i < 4; ++i) tc::mbar_init(sc_full + i, 8);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(s_full + i, 1);
+      tc::mbar_init(p_full + i, 128);
+      tc::mbar_init(o_done + i, 1);
+      tc::mbar_init(q_full + i, 128);
+      tc::mbar_init(wg_sync + i, 128);
+    }
+    tc::mbar_init(nan_sync, C::loaders);
+    tc::mbar_init(drained, 1);
+    *s_abort = 0;
+    *s_any_nan = 0;
+  }
+  if (warp == 12) {
+    tc::tmem_alloc(s_tmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *s_tmem;
+  pdl_wait();
+  pdl_trigger();
+  Line l = line_of(p);
+
+  if (wg == 3) {
+    // ======================= MMA warp ==========================================
+    regs_down<C::mma_regs>();
+    if (warp == 12 && lane == 0) {
+      const uint32_t id_qk = idesc_f32(128, kKeys);
+      const uint32_t id_pv = idesc_f32(128, D) | tc::kTransB;
+      const uint32_t sq = tc::smem_u32(smem + C::o_q), sk = tc::smem_u32(smem + C::o_k),
+                     sv = tc::smem_u32(smem + C::o_v);
+      int unit = 0, halves = 0, segs = 0;      // running counts: stages and phases
+      int n_p[2] = {0, 0};
+      bool ok = true;
+      auto qk = [&](int m, int buf, int stage) {
+        const uint32_t d = tmem + C::c_s(buf);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          const uint64_t a = tc::tile_desc(sq + (m * 2 + part) * C::q_part, D / 2, 0);
+          const uint64_t b = tc::tile_desc(sk + stage * C::k_stage, D / 2, 0);
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            mma_f8(d, a + k * 16, b + k * 16, id_qk, part | k);
+        }
+        tc::mma_commit(s_full + buf);
+      };
+      auto wait_k = [&](int u) {
+        ok = ok && mbar_wait_abortable(k_full + u % C::KS, (u / C::KS) & 1, s_abort);
+        tc::fence_after_sync();
+      };
+      auto pv = [&](int m, int buf, int h0, bool first, bool wait_v, bool free_v) {
+        const uint32_t d = tmem + C::c_o(m), a = tmem + C::c_s(buf);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int h = h0 + half, st = h % C::VS;
+          if (wait_v) {
+            ok = ok && mbar_wait_abortable(v_full + st, (h / C::VS) & 1, s_abort);
+            tc::fence_after_sync();
+          }
+          if (!ok) return;
+          const uint64_t b = tc::mn_desc(sv + st * C::v_stage, D, 0);
+#pragma unroll
+          for (int k = 0; k < kHalf / 16; ++k)
+            tc::mma_bf16_tmem_a(d, a + half * 32 + k * 8, b + (uint64_t)(k * 2 * D * 16 >> 4), id_pv,
+                                !(first && half == 0 && k == 0));
+          if (free_v) tc::mma_commit(v_empty + st);
+        }
+        tc::mma_commit(o_done + m);
+      };
+      for (; ok && l.u < l.u_end;) {
+        const Seg g = seg_at(p, l, kRows);
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+          ok = ok && mbar_wait_abortable(q_full + m, segs & 1, s_abort);
+        tc::fence_after_sync();
+        if constexpr (kM == 2) {
+          wait_k(unit);
+          if (!ok) break;
+          qk(0, 0, unit % C::KS);
+          qk(1, 1, unit % C::KS);
+          tc::mma_commit(k_empty + unit % C::KS);
+          for (int j = 0; ok && j < g.count; ++j) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              ok = ok && mbar_wait_abortable(p_full + m, n_p[m] & 1, s_abort);
+              ++n_p[m];
+              tc::fence_after_sync();
+              if (!ok) break;
+              pv(m, m, halves, j == 0, m == 0, m == 1);
+              if (j + 1 < g.count) {
+                if (m == 0) wait_k(unit + 1);
+                if (!ok) break;
+                qk(m, m, (unit + 1) % C::KS);
+                if (m == 1) tc::mma_commit(k_empty + (unit + 1) % C::KS);
+              }
+            }
+            ++unit;
+            halves += 2;
+          }
+        } else {
+          wait_k(unit);
+          if (!ok) break;
+          qk(0, unit & 1, unit % C::KS);
+          tc::mma_commit(k_empty + unit % C::KS);
+          for (int j = 0; ok && j < g.count; ++j) {
+            if (j + 1 < g.count) {
+              wait_k(unit + 1);
+              if (!ok) break;
+              qk(0, (unit + 1) & 1, (unit + 1) % C::KS);
+              tc::mma_commit(k_empty + (unit + 1) % C::KS);
+            }
+            const int b = unit & 1;
+            ok = ok && mbar_wait_abortable(p_full + b, n_p[b] & 1, s_abort);
+            ++n_p[b];
+            tc::fence_after_sync();
+            if (!ok) break;
+            pv(0, b, halves, j == 0, true, true);
+            ++unit;
+            halves += 2;
+          }
+        }
+        ++segs;
+        l.u += g.count;
+      }
+      // Nothing of this CTA's tensor work is in flight when TMEM is freed.
+      tc::mma_commit(drained);
+      if (!tc::mbar_wait(drained, 0)) record_device_status(GDN_ERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (wg >= kM) {
+    // ======================= K copies, V widening ================================
+    regs_down<C::load_regs>();
+    const int dt = tid - kM * 128;                    // 0 .. loaders - 1
+    constexpr int chunks = D / 16;
+    constexpr int k_it = kKeys * chunks / C::loaders;
+    constexpr int v_it = kHalf * chunks / C::loaders;
+    const size_t block_bytes = (size_t)B * D;
+    int k_unit = 0, v_half = 0, sc_unit = 0;          // running counts
+    bool ok = true;
+    Line lk = l;                                      // runs ahead: what K to copy next
+    Seg gk;
+    int jk = 0;
+    bool have_k = lk.u < lk.u_end;
+    if (have_k) gk = seg_at(p, lk, kRows);
+    // Copies the next K unit (and leaves its scales), if there is one.
+    auto issue_k = [&]() {
+      if (have_k) {
+        const int st = k_unit % C::KS;
+        if (k_unit >= C::KS)
+          ok = ok && warp_wait(k_empty + st, (k_unit / C::KS - 1) & 1, s_abort);
+        if (ok) {
+          const int key0 = (gk.first_unit + jk) * kKeys;
+          const int32_t* table = p.table + (int64_t)gk.seq * p.table_stride;
+          unsigned char* dst = smem + C::o_k + st * C::k_stage;
+#pragma unroll
+          for (int it = 0; it < k_it; ++it) {
+            const int idx = it * C::loaders + dt;
+            const int r = (idx & 7) + ((idx / (8 * chunks)) << 3), c = (idx >> 3) % chunks;
+            const int key = key0 + r;
+            bool in = key < gk.key_end;
+            const uint8_t* src = p.kc;
+            if (in) {
+              const int blk = __ldg(table + (key >> p.log_b));
+              in = (unsigned)blk < (unsigned)p.num_blocks;
+              if (in) src += ((size_t)blk * p.Hk + gk.head) * block_bytes + (size_t)(key & (B - 1)) * D + c * 16;
+              else record_device_status(GDN_ERR_INVALID_ARG);
+            }
+            tc::cp_async16(dst + idx * 16, src, in ? 16u : 0u);
+          }
+          // Scales of the unit's 8 groups of 16 keys.
+          if (dt < 8) {
+            float* sc = s_sc + (sc_unit & 3) * 24;
+            const int key = key0 + dt * 16;
+            float a = 1.f, v = 1.f;
+            if (key < gk.key_end) {
+              const int blk = __ldg(table + (key >> p.log_b));
+              if ((unsigned)blk < (unsigned)p.num_blocks) {
+                a = __ldg(p.ks + (size_t)blk * p.Hk + gk.head);
+                v = __ldg(p.vs + (size_t)blk * p.Hk + gk.head);
+              }
+            }
+            v = fmaxf(v, 7.888609052210118e-31f);      // 2^-100
+            sc[dt] = a;
+            sc[8 + dt] = lg2_approx(v);
+            sc[16 + dt] = __fdividef(1.f, v);
+            tc::mbar_arrive(sc_full + (sc_unit & 3));
+          }
+          ++sc_unit;
+          ++k_unit;
+          if (++jk == gk.count) {
+            jk = 0;
+            lk.u += gk.count;
+            have_k = lk.u < lk.u_end;
+            if (have_k) gk = seg_at(p, lk, kRows);
+          }
+        }
+      }
+      tc::cp_async_commit();
+    };
+    // V runs two halves ahead of its conversion, in registers.
+    Line lv = l;
+    Seg gv;
+    int jv = 0;                                       // half of the segment
+    bool have_v = lv.u < lv.u_end;
+    if (have_v) gv = seg_at(p, lv, kRows);
+    struct VMeta { int key0, nan_base, seg, opens; };
+    int v_seg = 0, nan_phase = 0;
+    uint4 raw[2][v_it];
+    VMeta meta[2];
+    auto load_v = [&](uint4 (&dst)[v_it], VMeta& mt) {
+      if (!have_v) return;
+      const int key0 = gv.first_unit * kKeys + jv * kHalf;
+      const int32_t* table = p.table + (int64_t)gv.seq * p.table_stride;
+      mt.key0 = key0;
+      mt.nan_base = visible(gv.s, gv.row0 / G) - kHalf;   // every row sees the 64 keys behind it
+      mt.seg = v_seg & 3;
+      mt.opens = jv == 0;
+#pragma unroll
+      for (int it = 0; it < v_it; ++it) {
+        const int idx = it * C::loaders + dt;
+        const int r = (idx & 7) + ((idx / (8 * chunks)) << 3), c = (idx >> 3) % chunks;
+        const int key = key0 + r;
+        dst[it] = make_uint4(0, 0, 0, 0);
+        if (key < gv.key_end) {
+          const int blk = __ldg(table + (key >> p.log_b));
+          if ((unsigned)blk < (unsigned)p.num_blocks)
+            dst[it] = ldg16(p.vc + ((size_t)blk * p.Hk + gv.head) * block_bytes +
+                            (size_t)(key & (B - 1)) * D + c * 16);
+        }
+      }
+      if (++jv == 2 * gv.count) {
+        jv = 0;
+        ++v_seg;
+        lv.u += gv.count;
+        have_v = lv.u < lv.u_end;
+        if (have_v) gv = seg_at(p, lv, kRows);
+      }
+    };
+    auto put_v = [&](uint4 (&src)[v_it], const VMeta& mt) {
+      const int st = v_half % C::VS;
+      if (v_half >= C::VS)
+        ok = ok && warp_wait(v_empty + st, (v_half / C::VS - 1) & 1, s_abort);
+      if (!ok) return;
+      unsigned char* dst = smem + C::o_v + st * C::v_stage;
+      // Where the tile's rows do not see the same keys, a weight of zero must not
+      // meet a NaN (0 x NaN is NaN): a NaN of V is written as zero and kept as
+      // the first key whose column has one.
+      const bool mixed = mt.key0 > mt.nan_base;
+      unsigned short* first_nan = s_nan + mt.seg * D;
+      if (mt.opens) {
+        for (int i = dt; i < D; i += C::loaders) first_nan[i] = 0xffff;
+        tc::mbar_arrive(nan_sync);
+        ok = warp_wait(nan_sync, nan_phase & 1, s_abort);
+        ++nan_phase;
+        if (!ok) return;
+      }
+#pragma unroll
+      for (int it = 0; it < v_it; ++it) {
+        const int idx = it * C::loaders + dt;
+        const int r = (idx & 7) + ((idx / (8 * chunks)) << 3), c = (idx >> 3) % chunks;
+        uint32_t w[4] = {src[it].x, src[it].y, src[it].z, src[it].w};
+        if (mixed) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if ((((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0) {
+              for (int b = 0; b < 4; ++b)
+                if (((w[k] >> (8 * b)) & 0x7fu) == 0x7fu) {
+                  unsigned short* at = first_nan + c * 16 + k * 4 + b;
+                  const unsigned short key = (unsigned short)(mt.key0 + r - mt.nan_base);
+                  unsigned short old = *reinterpret_cast<volatile unsigned short*>(at);
+                  while (key < old) {
+                    const unsigned short was = atomicCAS(at, old, key);
+                    if (was == old) break;
+                    old = was;
+                  }
+                  *s_any_nan = 1;
+                  w[k] &= ~(0xffu << (8 * b));
+                }
+            }
+          }
+        }
+        unsigned char* at = dst + (r >> 3) * (D * 16) + c * 256 + (r & 7) * 16;
+        *reinterpret_cast<uint4*>(at) = make_uint4(e4m3x2_half2(w[0]), e4m3x2_half2(w[0] >> 16),
+                                                   e4m3x2_half2(w[1]), e4m3x2_half2(w[1] >> 16));
+        *reinterpret_cast<uint4*>(at + 128) = make_uint4(e4m3x2_half2(w[2]), e4m3x2_half2(w[2] >> 16),
+                                                         e4m3x2_half2(w[3]), e4m3x2_half2(w[3] >> 16));
+      }
+      tc::fence_smem_to_async();
+      tc::mbar_arrive(v_full + st);
+      ++v_half;
+    };
+    long long left = max(0LL, l.u_end - l.u);         // units of this CTA
+#pragma unroll
+    for (int i = 0; i < C::KS; ++i) issue_k();
+    load_v(raw[0], meta[0]);
+    load_v(raw[1], meta[1]);
+    // K of unit `n` has landed: hand it over.
+    auto give_k = [&](int n) {
+      tc::fence_smem_to_async();
+      tc::mbar_arrive(k_full + n % C::KS);
+    };
+    if (left > 0 && ok) {
+      tc::cp_async_wait_group<C::KS - 1>();
+      give_k(0);
+    }
+    for (int n = 0; ok && n < left; ++n) {
+      tc::cp_async_wait_group<C::KS - 2>();
+      if (n + 1 < left) give_k(n + 1);
+      put_v(raw[0], meta[0]);
+      load_v(raw[0], meta[0]);
+      if (ok) {
+        put_v(raw[1], meta[1]);
+        load_v(raw[1], meta[1]);
+      }
+      issue_k();
+    }
+    tc::cp_async_wait_group<0>();
+  } else {
+    // ======================= softmax of 128 rows ================================
+    regs_up<C::soft_regs>();
+    const int m = wg, r = tid & 127;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    int n_o = 0, unit = 0, seg = 0, n_sync = 0;
+    // All 128 threads of the warpgroup, or false when the CTA gave up.
+    auto wg_barrier = [&]() {
+      tc::mbar_arrive(wg_sync + m);
+      return warp_wait(wg_sync + m, n_sync++ & 1, s_abort);
+    };
+    bool ok = true;
+    for (; ok && l.u < l.u_end;) {
+      const Seg g = seg_at(p, l, kRows);
+      const int row = g.row0 + m * 128 + r;
+      const bool live = m * 128 + r < g.n_rows;
+      const int tok = row / G, hq = g.head * G + row - tok * G;
+      // ---- Q: hi and lo codes of this thread's row ------------------------------
+      float rs = 0.f;
+      {
+        const __nv_bfloat16* src = p.q + (int64_t)(g.s.first + tok) * p.q_stride + (int64_t)hq * D;
+        uint32_t top_bits = 0;                         // largest magnitude, as bits
+        if (live) {
+#pragma unroll 4
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 u = ldg16(src + c * 8);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              top_bits = max(top_bits, max((w[k] & 0x7fffu) << 16, w[k] & 0x7fff0000u));
+          }
+        }
+        const bool bad = top_bits >= 0x7f800000u;      // an infinity or NaN in the row
+        const int ex = max((int)(top_bits >> 23) - 127 - 7, -126);
+        const float inv = __int_as_float((127 - min(ex, 126)) << 23);
+        rs = bad ? __int_as_float(0x7fffffff) : __int_as_float((min(ex, 126) + 127) << 23);
+        rs *= fabsf(p.scale_log2);
+        const float sgn = p.scale_log2 < 0.f ? -inv : inv;
+        unsigned char* hi = smem + C::o_q + (m * 2) * C::q_part + (r >> 3) * (D * 8) + (r & 7) * 16;
+#pragma unroll 2
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t h4[4] = {0, 0, 0, 0}, l4[4] = {0, 0, 0, 0};
+          if (live && !bad) {
+            const uint4 ua = ldg16(src + c * 16), ub = ldg16(src + c * 16 + 8);
+            const uint32_t w[8] = {ua.x, ua.y, ua.z, ua.w, ub.x, ub.y, ub.z, ub.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float a = bf16lo(w[k]) * sgn, b = bf16hi(w[k]) * sgn;
+              const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+              const uint32_t f = e4m3x2_half2(h2);
+              const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&f));
+              const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(a - hf.x, b - hf.y),
+                                                           __NV_SATFINITE, __NV_E4M3);
+              h4[k >> 1] |= h2 << (16 * (k & 1));
+              l4[k >> 1] |= l2 << (16 * (k & 1));
+            }
+          }
+          *reinterpret_cast<uint4*>(hi + c * 128) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
+          *reinterpret_cast<uint4*>(hi + C::q_part + c * 128) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
+        }
+        tc::fence_smem_to_async();
+        tc::mbar_arrive(q_full + m);
+      }
+      const int lim = live ? visible(g.s, tok) : 0;
+      const int min_lim = visible(g.s, (g.row0 + m * 128) / G);
+      const int nan_base = visible(g.s, g.row0 / G) - kHalf;
+      const bool part_tile = m * 128 + 128 > g.n_rows;
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < g.count; ++j, ++unit) {
+        const int buf = kM == 2 ? m : (unit & 1);
+        const int ph = kM == 2 ? (unit & 1) : ((unit >> 1) & 1);
+        ok = ok && warp_wait(s_full + buf, ph, s_abort);
+        ok = ok && warp_wait(sc_full + (unit & 3), (unit >> 2) & 1, s_abort);
+        if (!ok) break;
+        tc::fence_after_sync();
+        float x[128];
+        const uint32_t ts = tmem + lane_base + C::c_s(buf);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32_async(ts + c * 32, x + c * 32);
+        tmem_wait_ld();
+        const float* sc = s_sc + (unit & 3) * 24;
+        const int key0 = (g.first_unit + j) * kKeys;
+        if (part_tile || key0 + kKeys > min_lim) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k)
+            if (key0 + k >= lim) x[k] = -INFINITY;
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int gr = 0; gr < 8; ++gr) {
+          float gm = x[gr * 16];
+#pragma unroll
+          for (int k = 1; k < 16; ++k) gm = fmaxf(gm, x[gr * 16 + k]);
+          mx = fmaxf(mx, fmaf(gm, factor(rs * sc[gr]), sc[8 + gr]));
+        }
+        if (__any_sync(0xffffffffu, mx > m_run + 8.f)) {
+          const float m_new = fmaxf(mx, m_run);
+          const float al = m_new > m_run ? ex2_approx(m_run - m_new) : 1.f;
+          m_run = m_new;
+          l_run *= al;
+          if (j > 0) {
+            // The products of the previous unit are in O; this unit's wait for P.
+            ok = ok && warp_wait(o_done + m, (n_o - 1) & 1, s_abort);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const uint32_t to = tmem + lane_base + C::c_o(m);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float v[32];
+              tmem_ld32_async(to + c, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] *= al;
+              tmem_st32_async(to + c, reinterpret_cast<uint32_t*>(v));
+            }
+            tmem_wait_st();
+          }
+        }
+        const float ref = (m_run == -INFINITY ? 0.f : m_run) - 7.f;
+        uint32_t pk[64];
+        float lsum = 0.f;
+#pragma unroll
+        for (int gr = 0; gr < 8; ++gr) {
+          const float a = factor(rs * sc[gr]), b = sc[8 + gr] - ref;
+          const float2 a2 = make_float2(a, a), b2 = make_float2(b, b);
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float2 v = make_float2(x[gr * 16 + 2 * k], x[gr * 16 + 2 * k + 1]);
+            v = fma2(v, a2, b2);
+            v.x = ex2_approx(v.x);
+            v.y = ex2_approx(v.y);
+            sum = add2(sum, v);
+            const __half2 h = __floats2half2_rn(v.x, v.y);
+            pk[gr * 8 + k] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          lsum = fmaf(sum.x + sum.y, sc[16 + gr], lsum);
+        }
+        l_run += lsum;
+        tmem_st32_async(ts, pk);
+        tmem_st32_async(ts + 32, pk + 32);
+        tmem_wait_st();
+        tc::fence_before_sync();
+        tc::mbar_arrive(p_full + buf);
+        ++n_o;
+      }
+      if (!ok) break;
+      // ---- results -------------------------------------------------------------
+      // With two score buffers the last scores do not imply that the products
+      // before them are done, and a parity wait cannot see two phases ahead.
+      if (kM == 1 && n_o > 1) ok = warp_wait(o_done + m, (n_o - 2) & 1, s_abort);
+      ok = ok && warp_wait(o_done + m, (n_o - 1) & 1, s_abort);
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint32_t to = tmem + lane_base + C::c_o(m);
+      const bool whole = g.count == g.n_units;
+      __nv_bfloat16* out = p.o + ((int64_t)(g.s.first + tok) * p.Hq + hq) * D;
+      const float il = l_run == 0.f ? 0.f : 1.f / l_run;
+      const size_t part_sz = (size_t)(D + 2) * 128;
+      float* parts = p.tile_partials + (size_t)m * part_sz;
+      float* part = parts + ((size_t)blockIdx.x * 2 + (g.first_unit == 0 ? 1 : 0)) * kM * part_sz;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float v[32];
+        tmem_ld32_async(to + c, v);
+        tmem_wait_ld();
+        if (*s_any_nan) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const int first = s_nan[(seg & 3) * D + c + k];
+            if (first != 0xffff && lim > nan_base + first) v[k] = NAN;
+          }
+        }
+        if (whole) {
+          if (live) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] *= il;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(out + c + 8 * k) = pack8(v + 8 * k);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) __stcg(part + (size_t)(2 + c + k) * 128 + r, v[k]);
+        }
+      }
+      if (!whole) {
+        __stcg(part + r, m_run);
+        __stcg(part + 128 + r, l_run);
+        __threadfence();
+        ok = wg_barrier();
+        if (!ok) break;
+        const long long at0 = (long long)g.head * l.units1 + g.cum;
+        const int c0 = (int)(at0 / l.per_cta), c1 = (int)((at0 + g.n_units - 1) / l.per_cta);
+        if (r == 0) {
+          int* counter = p.tile_counters + ((size_t)g.lo * p.Hk + g.head) * kM + m;
+          const int seen = atomicAdd(counter, 1);
+          s_flag[m] = seen == c1 - c0;
+          if (seen == c1 - c0) *counter = 0;           // ready for the next call on this plan
+        }
+        ok = wg_barrier();
+        if (!ok) break;
+        if (s_flag[m]) {
+          __threadfence();
+          float top = -INFINITY;
+          for (int c = c0; c <= c1; ++c)
+            top = fmaxf(top, __ldcg(parts + ((size_t)c * 2 + (c == c0)) * kM * part_sz + r));
+          float lt = 0.f;
+          for (int c = c0; c <= c1; ++c) {
+            const float* q = parts + ((size_t)c * 2 + (c == c0)) * kM * part_sz;
+            const float mc = __ldcg(q + r);
+            lt += __ldcg(q + 128 + r) * (mc == -INFINITY ? 1.f : ex2_approx(mc - top));
+          }
+          const float it = lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll 1
+          for (int cb = 0; cb < D; cb += 32) {
+            float v[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = 0.f;
+            for (int c = c0; c <= c1; ++c) {
+              const float* q = parts + ((size_t)c * 2 + (c == c0)) * kM * part_sz;
+              const float mc = __ldcg(q + r);
+              const float f = mc == -INFINITY ? 1.f : ex2_approx(mc - top);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = fmaf(__ldcg(q + (size_t)(2 + cb + k) * 128 + r), f, v[k]);
+            }
+            if (live) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] *= it;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(out + cb + 8 * k) = pack8(v + 8 * k);
+            }
+          }
+        }
+        ok = wg_barrier();                             // s_flag is free again
+        if (!ok) break;
+      }
+      tc::fence_before_sync();
+      l.u += g.count;
+      ++seg;
+    }
+  }
+  // Every role is here, done or given up.
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 12) tc::tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+gdn_status_t launch_tile(const Args& a, cudaStream_t st) {
+  static const cudaError_t set = cudaFuncSetAttribute(
+      attn_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TC<D>::total);
+  if (set != cudaSuccess) return check_launch(set);
+  return check_launch(launch_pdl(attn_tile_kernel<D>, dim3(a.tile_grid), dim3(kThreads),
+                                 TC<D>::total, st, a));
+}
+
+}  // namespace
+
+gdn_status_t launch_attn_tile(const Args& a, cudaStream_t st) {
+  if (a.d == 64) return launch_tile<64>(a, st);
+  if (a.d == 128) return launch_tile<128>(a, st);
+  return launch_tile<256>(a, st);
+}
+
+GDN_DEFINE_STATUS_GATHER(gather_status_attn_tile)
+
+}  // namespace gdn

@@ -101,6 +101,13 @@ def test_prefill_and_mixed(Hq, Hk, d, B):
     check(s, run(s))
 
 
+@pytest.mark.parametrize("Hq,Hk,d", [(16, 2, 256), (32, 8, 128), (4, 4, 64), (24, 2, 128), (3, 1, 256)])
+@pytest.mark.parametrize("new,kv", [([127], [127]), ([300], [5000]), ([65, 700, 90], [65, 1400, 4000])])
+def test_chunks_of_prompts(Hq, Hk, d, new, kv):
+    s = make(17, new, kv, Hq, Hk, d, 64)
+    check(s, run(s))
+
+
 def test_rows_that_see_no_key_are_zero():
     # More new tokens than keys: the first ones see nothing; and sequences without tokens or keys.
     new, kv = [4, 0, 3, 2, 0], [2, 7, 0, 50, 0]
