@@ -221,6 +221,7 @@ gdn_status_t gdn_paged_attention(const void* q, int64_t q_stride, const void* k_
   if ((flags & ~GDN_FLAG_PLANNED) != 0 || table_stride < max_blocks || num_blocks < 0)
     return GDN_ERR_INVALID_ARG;
   if (!(std::fabs(softmax_scale) <= 3.0e38f)) return GDN_ERR_INVALID_ARG;
+  if (Hk > 0 && (int64_t)num_blocks * Hk >= 0x7fffffff) return GDN_ERR_UNSUPPORTED;
   gdn_status_t rc = check_plan(cu_seqlens, kv_lens, N, T, Hq, Hk, d, block_tokens, max_blocks,
                                max_new_tokens, workspace, workspace_bytes, &nothing);
   if (rc != GDN_OK || nothing) return rc;
@@ -264,6 +265,8 @@ gdn_status_t gdn_paged_attention(const void* q, int64_t q_stride, const void* k_
   a.counters = reinterpret_cast<int*>(ws + l.counters);
   a.partials = reinterpret_cast<float*>(ws + l.partials);
   a.tiles = reinterpret_cast<attn::Item*>(ws + l.tiles);
+  a.starts = reinterpret_cast<const attn::Start*>(ws + l.starts);
+  a.tile_starts = reinterpret_cast<const attn::Start*>(ws + l.tile_starts);
   a.split_rows = l.split_rows;
   a.split_grid = attn::split_grid(d);
   a.tile_grid = attn::tile_grid();

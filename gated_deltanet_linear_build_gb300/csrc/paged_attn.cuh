@@ -32,8 +32,13 @@ static_assert(sizeof(Header) == 256, "header is 256 bytes");
 constexpr int kUnit = 32;              // keys per unit of the split kernel
 constexpr int kTileKeys = 128;         // keys per unit of the tensor-core kernel
 
+// Where a CTA's piece of the work line begins.
+struct Start {
+  int item, head;
+};
+
 struct Layout {
-  size_t items, counters, partials, tiles, tile_counters, tile_partials, total;
+  size_t starts, tile_starts, items, counters, partials, tiles, tile_counters, tile_partials, total;
   int item_cap, tile_cap, split_rows, tile_rows;
 };
 
@@ -73,6 +78,7 @@ struct Args {
   float* partials;
   Item* tiles;
   int split_rows, split_grid, tile_grid;
+  const Start *starts, *tile_starts;
   int* tile_counters;                  // [tile][head][128-row half]
   float* tile_partials;
 };

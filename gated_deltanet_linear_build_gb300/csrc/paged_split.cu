@@ -49,6 +49,10 @@ Layout layout(int T, int N, int Hq, int Hk, int d) {
   l.tile_cap = (int)std::min<int64_t>((int64_t)T * G / l.tile_rows + N, 0x7fffffff / 16);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   size_t at = sizeof(Header);
+  l.starts = at;
+  at += kSplitGridMax * sizeof(Start);
+  l.tile_starts = at;
+  at = up(at + tile_grid() * sizeof(Start));
   l.items = at;
   at = up(at + (size_t)l.item_cap * sizeof(Item));
   l.counters = at;
@@ -85,6 +89,7 @@ struct PlanArgs {
   Header* hdr;
   Item *items, *tiles;
   int *counters, *tile_counters;
+  Start *starts, *tile_starts;
 };
 
 __device__ __forceinline__ int block_scan(int v, int* sums, int& tot) {
@@ -167,6 +172,29 @@ __device__ void build_list(const PlanArgs& p, const ListArgs& a, int* sums, int*
   items = min(items, a.cap);
 }
 
+// Units per CTA, and where each CTA's piece of the line begins.
+__device__ int cut_line(const Item* items, int num, int units, int Hk, int grid, Start* starts) {
+  const int64_t all = (int64_t)units * Hk;
+  const int per_cta = (int)max((int64_t)1, (all + grid - 1) / grid);
+  __syncthreads();                              // the list is written
+  for (int c = threadIdx.x; c < grid; c += kPlanThreads) {
+    const int64_t u = (int64_t)c * per_cta;
+    Start at = {0, 0};
+    if (u < all) {
+      at.head = (int)(u / units);
+      const int x = (int)(u - (int64_t)at.head * units);
+      int lo = 0, hi = num - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (items[mid].cum <= x) lo = mid; else hi = mid - 1;
+      }
+      at.item = lo;
+    }
+    starts[c] = at;
+  }
+  return per_cta;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs p) {
   __shared__ int sums[32];
   __shared__ int s_first[kPlanThreads];
@@ -177,14 +205,15 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
              items, units);
   build_list(p, {p.tile_rows, kTileKeys, p.limit, 0x7fffffff, p.tile_cap, 2 * p.Hk, p.tiles,
                  p.tile_counters}, sums, s_first, tiles, tile_units);
+  const int per_cta = cut_line(p.items, items, units, p.Hk, p.grid, p.starts);
+  const int tile_per_cta = cut_line(p.tiles, tiles, tile_units, p.Hk, p.tile_grid, p.tile_starts);
   if (threadIdx.x == 0) {
-    const int64_t all = (int64_t)units * p.Hk, tile_all = (int64_t)tile_units * p.Hk;
     p.hdr->num_items = items;
     p.hdr->units = units;
-    p.hdr->per_cta = (int)max((int64_t)1, (all + p.grid - 1) / p.grid);
+    p.hdr->per_cta = per_cta;
     p.hdr->num_tiles = tiles;
     p.hdr->tile_units = tile_units;
-    p.hdr->tile_per_cta = (int)max((int64_t)1, (tile_all + p.tile_grid - 1) / p.tile_grid);
+    p.hdr->tile_per_cta = tile_per_cta;
   }
 }
 
@@ -286,15 +315,12 @@ attn_split_kernel(const Args p) {
   long long u = (long long)blockIdx.x * per_cta;
   const long long u_end = min(total, u + per_cta);
 
+  const int2 at = *reinterpret_cast<const int2*>(p.starts + blockIdx.x);
+  int lo = at.x, head = at.y;
+
   while (u < u_end) {
     // ---- the item that holds unit u ------------------------------------------
-    const int head = (int)(u / units1);
     const int x = (int)(u - (long long)head * units1);
-    int lo = 0, hi = num_items - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(&p.items[mid].cum) <= x) lo = mid; else hi = mid - 1;
-    }
     const int4 raw = __ldg(reinterpret_cast<const int4*>(p.items) + lo);
     const int seq = raw.x, row0 = raw.y, n_units = raw.z, cum = raw.w;
     const int first_unit = x - cum;
@@ -745,6 +771,10 @@ attn_split_kernel(const Args p) {
     }
     __syncthreads();                     // the ring, Q and s_ml are free again
     u += seg;
+    if (first_unit + seg == n_units && ++lo == num_items) {
+      lo = 0;
+      ++head;
+    }
   }
 }
 
@@ -783,6 +813,8 @@ gdn_status_t launch_attn_plan(const int32_t* cu, const int32_t* kv, int N, int T
   p.tile_grid = tile_grid();
   p.tiles = reinterpret_cast<Item*>(ws + l.tiles);
   p.tile_counters = reinterpret_cast<int*>(ws + l.tile_counters);
+  p.starts = reinterpret_cast<Start*>(ws + l.starts);
+  p.tile_starts = reinterpret_cast<Start*>(ws + l.tile_starts);
   return check_launch(launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p));
 }
 

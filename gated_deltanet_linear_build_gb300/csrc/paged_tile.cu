@@ -26,10 +26,15 @@
 // arrive last.
 //
 // Roles (four warpgroups): 0 .. kM - 1: softmax of one 128-row tile each; the
-// others up to 2: copies of K, widening of V; warp 12: MMAs.
-// Shared-memory operands lie as 8 x 16-byte core matrices (no swizzle).
+// others up to 2: widening of V; warp 12: MMAs; warp 13: TMA copies of K, and
+// the blocks' scales; warp 14: TMA copies of V's codes.
+// K and V's codes lie as TMA leaves them, rows of 128 (64 for d = 64) bytes
+// with their 16-byte chunks XOR-swizzled; Q and the widened V as 8 x 16-byte
+// core matrices. Copies issued by threads instead (cp.async and register
+// prefetches of 16 bytes each) held the tensor cores to a fifth of their rate.
 #include <algorithm>
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -50,22 +55,27 @@ template <int D>
 struct TC {
   static constexpr int M = D == 256 ? 1 : 2;            // 128-row tiles
   static constexpr int KS = D == 256 ? 2 : 3;           // K stages of 128 keys
-  static constexpr int VS = D == 256 ? 3 : 6;           // V stages of 64 keys
+  static constexpr int VR = D == 256 ? 2 : 4;           // stages of 64 keys of V's codes
+  static constexpr int VS = D == 256 ? 2 : 4;           // and of V widened
   static constexpr int loaders = (3 - M) * 128;
+  static constexpr int row = D == 64 ? 64 : 128;        // bytes of a row in a TMA box
+  static constexpr int boxes = D / row;                 // boxes across a cache row
   static constexpr int q_part = 128 * D;                // one part (hi or lo) of one tile
   static constexpr int k_stage = kKeys * D;
+  static constexpr int vr_stage = kHalf * D;
   static constexpr int v_stage = kHalf * D * 2;
   static constexpr int o_q = 0;
   static constexpr int o_k = o_q + M * 2 * q_part;
-  static constexpr int o_v = o_k + KS * k_stage;
+  static constexpr int o_vr = o_k + KS * k_stage;
+  static constexpr int o_v = o_vr + VR * vr_stage;
   // Scales of a unit's 8 groups of 16 keys, float [4 units][ks | log2 vs | 1 / vs][8].
   // A unit is copied at most 3 units ahead of the softmax that reads its scales.
   static constexpr int o_sc = o_v + VS * v_stage;
   // First key of a segment whose V is NaN in a column, uint16 [4 segments][D]. V
-  // is written at most 3 units, hence segments, ahead of the results.
+  // is widened at most 3 units, hence segments, ahead of the results.
   static constexpr int o_nan = o_sc + 4 * 24 * 4;
   static constexpr int o_bar = o_nan + 4 * D * 2;
-  static constexpr int n_bar = 2 * KS + 2 * VS + 4 + 2 + 2 + 2 + 2 + 2 + 2;
+  static constexpr int n_bar = 2 * KS + 2 * VR + 2 * VS + 4 + 2 + 2 + 2 + 2 + 2 + 2;
   static constexpr int o_misc = o_bar + n_bar * 8;      // tmem base, abort, flags
   static constexpr int total = o_misc + 32;
   static_assert(total <= 232448, "shared memory of one CTA");
@@ -77,6 +87,27 @@ struct TC {
   static constexpr int c_s(int i) { return i * 128; }
   static constexpr int c_o(int m) { return 256 + m * D; }
 };
+
+// TMA box: rows of one (block, head) to shared memory.
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                        uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];"
+      :: "r"(tc::smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+// K-major operand of 128-byte (64-byte) swizzled rows: 8-row groups 8 rows apart.
+template <int kRow>
+__device__ __forceinline__ uint64_t desc_swizzled(uint32_t addr) {
+  return tc::smem_desc(addr, 16, 8 * kRow) | ((uint64_t)(kRow == 128 ? 2 : 4) << 61);
+}
+// Byte of chunk c of row r under that swizzle.
+template <int kRow>
+__device__ __forceinline__ int swizzled(int r, int c) {
+  if constexpr (kRow == 128) return r * 128 + ((c ^ (r & 7)) << 4);
+  return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
 
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -143,6 +174,13 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegs));
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+
 // A bounded wait of a whole warp: all lanes go on, or none does.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, mbar_wait_abortable(bar, parity, abort));
@@ -150,14 +188,23 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 
 // One contiguous run of units of one (tile, head).
 struct Seg {
-  int lo, head, seq, row0, n_units, cum, first_unit, count;
+  int seq, row0, n_units, cum, first_unit, count;
   Seq s;
   int n_rows, key_end;
 };
 
+// This CTA's piece of the work line; lo and head are those of its next unit.
 struct Line {
-  int num, units1, per_cta;
+  int num, units1, per_cta, lo, head;
   long long u, u_end;
+  __device__ bool more() const { return u < u_end; }
+  __device__ void pass(const Seg& g) {
+    u += g.count;
+    if (g.first_unit + g.count == g.n_units && ++lo == num) {
+      lo = 0;
+      ++head;
+    }
+  }
 };
 
 __device__ __forceinline__ Line line_of(const Args& p) {
@@ -168,25 +215,20 @@ __device__ __forceinline__ Line line_of(const Args& p) {
   const long long total = (long long)l.units1 * p.Hk;
   l.u = (long long)blockIdx.x * l.per_cta;
   l.u_end = min(total, l.u + l.per_cta);
+  const int2 at = *reinterpret_cast<const int2*>(p.tile_starts + blockIdx.x);
+  l.lo = at.x;
+  l.head = at.y;
   return l;
 }
 
 __device__ __forceinline__ Seg seg_at(const Args& p, const Line& l, int tile_rows) {
   Seg g;
-  g.head = (int)(l.u / l.units1);
-  const int x = (int)(l.u - (long long)g.head * l.units1);
-  int lo = 0, hi = l.num - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(&p.tiles[mid].cum) <= x) lo = mid; else hi = mid - 1;
-  }
-  const int4 raw = __ldg(reinterpret_cast<const int4*>(p.tiles) + lo);
-  g.lo = lo;
+  const int4 raw = __ldg(reinterpret_cast<const int4*>(p.tiles) + l.lo);
   g.seq = raw.x;
   g.row0 = raw.y;
   g.n_units = raw.z;
   g.cum = raw.w;
-  g.first_unit = x - g.cum;
+  g.first_unit = (int)(l.u - (long long)l.head * l.units1) - g.cum;
   g.count = (int)min((long long)(g.n_units - g.first_unit), l.u_end - l.u);
   g.s = seq_of(p.cu, p.kv, g.seq, p.T, (int64_t)p.max_blocks << p.log_b);
   const int G = p.Hq / p.Hk;
@@ -196,14 +238,18 @@ __device__ __forceinline__ Seg seg_at(const Args& p, const Line& l, int tile_row
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, 1)
+attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
+                 const __grid_constant__ CUtensorMap v_map) {
   using C = TC<D>;
   constexpr int kM = C::M, kRows = kM * 128;
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ __align__(1024) unsigned char smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::o_bar);
   uint64_t* k_full = bars;
   uint64_t* k_empty = k_full + C::KS;
-  uint64_t* v_full = k_empty + C::KS;
+  uint64_t* vr_full = k_empty + C::KS;
+  uint64_t* vr_empty = vr_full + C::VR;
+  uint64_t* v_full = vr_empty + C::VR;
   uint64_t* v_empty = v_full + C::VS;
   uint64_t* sc_full = v_empty + C::VS;       // [4]
   uint64_t* s_full = sc_full + 4;            // [2] score buffers
@@ -224,8 +270,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const Args p) {
 
   if (tid == 0) {
     for (int i = 0; i < C::KS; ++i) {
-      tc::mbar_init(k_full + i, C::loaders);
+      tc::mbar_init(k_full + i, 1);
       tc::mbar_init(k_empty + i, 1);
+    }
+    for (int i = 0; i < C::VR; ++i) {
+      tc::mbar_init(vr_full + i, 1);
+      tc::mbar_init(vr_empty + i, C::loaders);
     }
     for (int i = 0; i < C::VS; ++i) {
       tc::mbar_init(v_full + i, C::loaders);
@@ -251,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const Args p) {
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *s_tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
   pdl_wait();
   pdl_trigger();
   Line l = line_of(p);
@@ -259,7 +309,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const Args p) {
   if (wg == 3) {
     // ======================= MMA warp ==========================================
     regs_down<C::mma_regs>();
-    if (warp == 12 && lane == 0) {
+    // The whole warp walks the role, so that descriptors stay in uniform
+    // registers, and one elected lane issues: 66 cycles per 128 x 128 MMA, the
+    // tensor core's own rate, where a lone lane's loop took above 200.
+    if (warp == 12) {
+      const bool one = elect_one();
       const uint32_t id_qk = idesc_f32(128, kKeys);
       const uint32_t id_pv = idesc_f32(128, D) | tc::kTransB;
       const uint32_t sq = tc::smem_u32(smem + C::o_q), sk = tc::smem_u32(smem + C::o_k),
@@ -269,18 +323,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const Args p) {
       bool ok = true;
       auto qk = [&](int m, int buf, int stage) {
         const uint32_t d = tmem + C::c_s(buf);
+        const uint64_t b = desc_swizzled<C::row>(sk + stage * C::k_stage);
+        const uint64_t a = tc::tile_desc(sq + m * 2 * C::q_part, D / 2, 0);
+        if (one) {
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          const uint64_t a = tc::tile_desc(sq + (m * 2 + part) * C::q_part, D / 2, 0);
-          const uint64_t b = tc::tile_desc(sk + stage * C::k_stage, D / 2, 0);
+          for (int part = 0; part < 2; ++part)
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k)
-            mma_f8(d, a + k * 16, b + k * 16, id_qk, part | k);
+            for (int k = 0; k < D / 32; ++k)
+              mma_f8(d, a + part * (C::q_part / 16) + k * 16,
+                     b + (k * 32 / C::row) * (kKeys * C::row / 16) + (k * 32 % C::row) / 16, id_qk,
+                     part | k);
+          tc::mma_commit(s_full + buf);
         }
-        tc::mma_commit(s_full + buf);
       };
       auto wait_k = [&](int u) {
-        ok = ok && mbar_wait_abortable(k_full + u % C::KS, (u / C::KS) & 1, s_abort);
+        ok = ok && warp_wait(k_full + u % C::KS, (u / C::KS) & 1, s_abort);
         tc::fence_after_sync();
       };
       auto pv = [&](int m, int buf, int h0, bool first, bool wait_v, bool free_v) {
@@ -289,35 +346,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const Args p) {
         for (int half = 0; half < 2; ++half) {
           const int h = h0 + half, st = h % C::VS;
           if (wait_v) {
-            ok = ok && mbar_wait_abortable(v_full + st, (h / C::VS) & 1, s_abort);
+            ok = ok && warp_wait(v_full + st, (h / C::VS) & 1, s_abort);
             tc::fence_after_sync();
           }
           if (!ok) return;
           const uint64_t b = tc::mn_desc(sv + st * C::v_stage, D, 0);
+          if (one) {
 #pragma unroll
-          for (int k = 0; k < kHalf / 16; ++k)
-            tc::mma_bf16_tmem_a(d, a + half * 32 + k * 8, b + (uint64_t)(k * 2 * D * 16 >> 4), id_pv,
-                                !(first && half == 0 && k == 0));
-          if (free_v) tc::mma_commit(v_empty + st);
+            for (int k = 0; k < kHalf / 16; ++k)
+              tc::mma_bf16_tmem_a(d, a + half * 32 + k * 8, b + k * 2 * D, id_pv,
+                                  !(first && half == 0 && k == 0));
+            if (free_v) tc::mma_commit(v_empty + st);
+            if (half == 1) tc::mma_commit(o_done + m);
+          }
         }
-        tc::mma_commit(o_done + m);
       };
-      for (; ok && l.u < l.u_end;) {
+      while (ok && l.more()) {
         const Seg g = seg_at(p, l, kRows);
 #pragma unroll
         for (int m = 0; m < kM; ++m)
-          ok = ok && mbar_wait_abortable(q_full + m, segs & 1, s_abort);
+          ok = ok && warp_wait(q_full + m, segs & 1, s_abort);
         tc::fence_after_sync();
         if constexpr (kM == 2) {
           wait_k(unit);
           if (!ok) break;
           qk(0, 0, unit % C::KS);
           qk(1, 1, unit % C::KS);
-          tc::mma_commit(k_empty + unit % C::KS);
+          if (one) tc::mma_commit(k_empty + unit % C::KS);
           for (int j = 0; ok && j < g.count; ++j) {
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-              ok = ok && mbar_wait_abortable(p_full + m, n_p[m] & 1, s_abort);
+              ok = ok && warp_wait(p_full + m, n_p[m] & 1, s_abort);
               ++n_p[m];
               tc::fence_after_sync();
               if (!ok) break;
@@ -326,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const Args p) {
                 if (m == 0) wait_k(unit + 1);
                 if (!ok) break;
                 qk(m, m, (unit + 1) % C::KS);
-                if (m == 1) tc::mma_commit(k_empty + (unit + 1) % C::KS);
+                if (m == 1 && one) tc::mma_commit(k_empty + (unit + 1) % C::KS);
               }
             }
             ++unit;
@@ -336,16 +395,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const Args p) {
           wait_k(unit);
           if (!ok) break;
           qk(0, unit & 1, unit % C::KS);
-          tc::mma_commit(k_empty + unit % C::KS);
+          if (one) tc::mma_commit(k_empty + unit % C::KS);
           for (int j = 0; ok && j < g.count; ++j) {
             if (j + 1 < g.count) {
               wait_k(unit + 1);
               if (!ok) break;
               qk(0, (unit + 1) & 1, (unit + 1) % C::KS);
-              tc::mma_commit(k_empty + (unit + 1) % C::KS);
+              if (one) tc::mma_commit(k_empty + (unit + 1) % C::KS);
             }
             const int b = unit & 1;
-            ok = ok && mbar_wait_abortable(p_full + b, n_p[b] & 1, s_abort);
+            ok = ok && warp_wait(p_full + b, n_p[b] & 1, s_abort);
             ++n_p[b];
             tc::fence_after_sync();
             if (!ok) break;
@@ -355,201 +414,174 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const Args p) {
           }
         }
         ++segs;
-        l.u += g.count;
+        l.pass(g);
       }
       // Nothing of this CTA's tensor work is in flight when TMEM is freed.
-      tc::mma_commit(drained);
+      if (one) tc::mma_commit(drained);
       if (!tc::mbar_wait(drained, 0)) record_device_status(GDN_ERR_TIMEOUT);
+      __syncwarp();
+    } else if (warp == 13 || warp == 14) {
+      // ===================== TMA copies ==========================================
+      // Warp 13: K units and their scales; warp 14: halves of V. Lane i posts box
+      // i: one page (or its part in the unit) times one of the boxes across a row.
+      const bool is_k = warp == 13;
+      const int keys = is_k ? kKeys : kHalf;
+      const int box_keys = min(B, keys), log_box = p.log_b < (is_k ? 7 : 6) ? p.log_b : (is_k ? 7 : 6);
+      const int pages = keys >> log_box;
+      const int page = lane % pages, bx = lane / pages;
+      const bool posts = lane < pages * C::boxes;
+      const CUtensorMap* map = is_k ? &k_map : &v_map;
+      uint64_t* full = is_k ? k_full : vr_full;
+      uint64_t* empty = is_k ? k_empty : vr_empty;
+      const int stages = is_k ? C::KS : C::VR, stage_bytes = is_k ? C::k_stage : C::vr_stage;
+      unsigned char* base = smem + (is_k ? C::o_k : C::o_vr);
+      const int absent = max(p.num_blocks * p.Hk, 1);   // a box past the end reads zeros
+      int st = 0, round = 0, unit = 0;
+      bool ok = true;
+      while (ok && l.more()) {
+        const Seg g = seg_at(p, l, kRows);
+        const int32_t* table = p.table + (int64_t)g.seq * p.table_stride;
+        const int key_first = g.first_unit * kKeys;
+        const int n = is_k ? g.count : 2 * g.count;
+        auto id_at = [&](int i) {
+          const int key = key_first + i * keys + page * box_keys;
+          return i < n && key < g.key_end ? __ldg(table + (key >> p.log_b)) : -1;
+        };
+        int next = id_at(0);
+        for (int i = 0; i < n; ++i) {
+          const int id = next;
+          next = id_at(i + 1);
+          if (round > 0) ok = ok && warp_wait(empty + st, (round - 1) & 1, s_abort);
+          if (!ok) break;
+          const int key0 = key_first + i * keys;
+          const int key = key0 + page * box_keys;
+          if (lane == 0) tc::mbar_arrive_expect_tx(full + st, stage_bytes);
+          __syncwarp();
+          if (posts) {
+            const bool in = (unsigned)id < (unsigned)p.num_blocks;
+            if (!in && is_k && key < g.key_end) record_device_status(GDN_ERR_INVALID_ARG);
+            tma_box(base + st * stage_bytes + (bx * keys + page * box_keys) * C::row, map, bx * C::row,
+                    key & (B - 1), in ? id * p.Hk + l.head : absent, full + st);
+          }
+          if (is_k) {
+            // Scales of the unit's 8 groups of 16 keys.
+            const int blk = __shfl_sync(0xffffffffu, id, ((lane & 7) * 16) >> log_box);
+            if (lane < 8) {
+              float a = 1.f, v = 1.f;
+              if (key0 + lane * 16 < g.key_end && (unsigned)blk < (unsigned)p.num_blocks) {
+                a = __ldg(p.ks + (size_t)blk * p.Hk + l.head);
+                v = __ldg(p.vs + (size_t)blk * p.Hk + l.head);
+              }
+              v = fmaxf(v, 7.888609052210118e-31f);     // 2^-100
+              float* sc = s_sc + (unit & 3) * 24;
+              sc[lane] = a;
+              sc[8 + lane] = lg2_approx(v);
+              sc[16 + lane] = __fdividef(1.f, v);
+              tc::mbar_arrive(sc_full + (unit & 3));
+            }
+            __syncwarp();
+            ++unit;
+          }
+          if (++st == stages) {
+            st = 0;
+            ++round;
+          }
+        }
+        l.pass(g);
+      }
+      // The copies in flight land before the CTA may end: a giving-up reader
+      // would not have waited for them.
+      if (*s_abort) {
+        for (int i = 0; i < stages; ++i)
+          if (round > 0 || i < st)
+            tc::mbar_wait(full + i, (round - (i < st ? 0 : 1)) & 1);
+      }
     }
-    __syncwarp();
   } else if (wg >= kM) {
-    // ======================= K copies, V widening ================================
+    // ======================= widening of V ======================================
     regs_down<C::load_regs>();
     const int dt = tid - kM * 128;                    // 0 .. loaders - 1
     constexpr int chunks = D / 16;
-    constexpr int k_it = kKeys * chunks / C::loaders;
     constexpr int v_it = kHalf * chunks / C::loaders;
-    const size_t block_bytes = (size_t)B * D;
-    int k_unit = 0, v_half = 0, sc_unit = 0;          // running counts
+    const int r_in = dt & 7, c = (dt >> 3) % chunks;  // this thread's row of 8, its chunk
+    const int rg_in = dt / (8 * chunks);              // and its group of 8 rows in a pass
+    constexpr int rg_per = C::loaders / (8 * chunks); // groups of 8 rows per pass
+    int half = 0, nan_phase = 0, seg = 0;             // running counts
     bool ok = true;
-    Line lk = l;                                      // runs ahead: what K to copy next
-    Seg gk;
-    int jk = 0;
-    bool have_k = lk.u < lk.u_end;
-    if (have_k) gk = seg_at(p, lk, kRows);
-    // Copies the next K unit (and leaves its scales), if there is one.
-    auto issue_k = [&]() {
-      if (have_k) {
-        const int st = k_unit % C::KS;
-        if (k_unit >= C::KS)
-          ok = ok && warp_wait(k_empty + st, (k_unit / C::KS - 1) & 1, s_abort);
-        if (ok) {
-          const int key0 = (gk.first_unit + jk) * kKeys;
-          const int32_t* table = p.table + (int64_t)gk.seq * p.table_stride;
-          unsigned char* dst = smem + C::o_k + st * C::k_stage;
+    while (ok && l.more()) {
+      const Seg g = seg_at(p, l, kRows);
+      const int nan_base = visible(g.s, g.row0 / G) - kHalf;   // every row sees the 64 keys behind it
+      unsigned short* first_nan = s_nan + (seg & 3) * D;
+      for (int i = 0; ok && i < 2 * g.count; ++i, ++half) {
+        const int key0 = g.first_unit * kKeys + i * kHalf;
+        const int sr = half % C::VR, st = half % C::VS;
+        ok = ok && warp_wait(vr_full + sr, (half / C::VR) & 1, s_abort);
+        if (half >= C::VS)
+          ok = ok && warp_wait(v_empty + st, (half / C::VS - 1) & 1, s_abort);
+        if (!ok) break;
+        if (i == 0) {
+          for (int k = dt; k < D; k += C::loaders) first_nan[k] = 0xffff;
+          tc::mbar_arrive(nan_sync);
+          ok = warp_wait(nan_sync, nan_phase & 1, s_abort);
+          ++nan_phase;
+          if (!ok) break;
+        }
+        const unsigned char* src = smem + C::o_vr + sr * C::vr_stage +
+                                   (c * 16 / C::row) * (kHalf * C::row);
+        uint4 raw[v_it];
 #pragma unroll
-          for (int it = 0; it < k_it; ++it) {
-            const int idx = it * C::loaders + dt;
-            const int r = (idx & 7) + ((idx / (8 * chunks)) << 3), c = (idx >> 3) % chunks;
-            const int key = key0 + r;
-            bool in = key < gk.key_end;
-            const uint8_t* src = p.kc;
-            if (in) {
-              const int blk = __ldg(table + (key >> p.log_b));
-              in = (unsigned)blk < (unsigned)p.num_blocks;
-              if (in) src += ((size_t)blk * p.Hk + gk.head) * block_bytes + (size_t)(key & (B - 1)) * D + c * 16;
-              else record_device_status(GDN_ERR_INVALID_ARG);
-            }
-            tc::cp_async16(dst + idx * 16, src, in ? 16u : 0u);
-          }
-          // Scales of the unit's 8 groups of 16 keys.
-          if (dt < 8) {
-            float* sc = s_sc + (sc_unit & 3) * 24;
-            const int key = key0 + dt * 16;
-            float a = 1.f, v = 1.f;
-            if (key < gk.key_end) {
-              const int blk = __ldg(table + (key >> p.log_b));
-              if ((unsigned)blk < (unsigned)p.num_blocks) {
-                a = __ldg(p.ks + (size_t)blk * p.Hk + gk.head);
-                v = __ldg(p.vs + (size_t)blk * p.Hk + gk.head);
+        for (int it = 0; it < v_it; ++it)
+          raw[it] = *reinterpret_cast<const uint4*>(
+              src + swizzled<C::row>((it * rg_per + rg_in) * 8 + r_in, c % (C::row / 16)));
+        unsigned char* dst = smem + C::o_v + st * C::v_stage;
+        // Keys past the end hold stale bytes: zeros instead. And where the tile's
+        // rows do not see the same keys, a weight of zero must not meet a NaN (0 x
+        // NaN is NaN): a NaN of V is written as zero and kept as the first key
+        // whose column has one.
+        if (key0 > nan_base) {
+#pragma unroll
+          for (int it = 0; it < v_it; ++it) {
+            const int r = (it * rg_per + rg_in) * 8 + r_in;
+            uint32_t w[4] = {raw[it].x, raw[it].y, raw[it].z, raw[it].w};
+            const bool past = key0 + r >= g.key_end;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (past) w[k] = 0;
+              if ((((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0) {
+                for (int b = 0; b < 4; ++b)
+                  if (((w[k] >> (8 * b)) & 0x7fu) == 0x7fu) {
+                    unsigned short* at = first_nan + c * 16 + k * 4 + b;
+                    const unsigned short key = (unsigned short)(key0 + r - nan_base);
+                    unsigned short old = *reinterpret_cast<volatile unsigned short*>(at);
+                    while (key < old) {
+                      const unsigned short was = atomicCAS(at, old, key);
+                      if (was == old) break;
+                      old = was;
+                    }
+                    *s_any_nan = 1;
+                    w[k] &= ~(0xffu << (8 * b));
+                  }
               }
             }
-            v = fmaxf(v, 7.888609052210118e-31f);      // 2^-100
-            sc[dt] = a;
-            sc[8 + dt] = lg2_approx(v);
-            sc[16 + dt] = __fdividef(1.f, v);
-            tc::mbar_arrive(sc_full + (sc_unit & 3));
-          }
-          ++sc_unit;
-          ++k_unit;
-          if (++jk == gk.count) {
-            jk = 0;
-            lk.u += gk.count;
-            have_k = lk.u < lk.u_end;
-            if (have_k) gk = seg_at(p, lk, kRows);
+            raw[it] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
-      }
-      tc::cp_async_commit();
-    };
-    // V runs two halves ahead of its conversion, in registers.
-    Line lv = l;
-    Seg gv;
-    int jv = 0;                                       // half of the segment
-    bool have_v = lv.u < lv.u_end;
-    if (have_v) gv = seg_at(p, lv, kRows);
-    struct VMeta { int key0, nan_base, seg, opens; };
-    int v_seg = 0, nan_phase = 0;
-    uint4 raw[2][v_it];
-    VMeta meta[2];
-    auto load_v = [&](uint4 (&dst)[v_it], VMeta& mt) {
-      if (!have_v) return;
-      const int key0 = gv.first_unit * kKeys + jv * kHalf;
-      const int32_t* table = p.table + (int64_t)gv.seq * p.table_stride;
-      mt.key0 = key0;
-      mt.nan_base = visible(gv.s, gv.row0 / G) - kHalf;   // every row sees the 64 keys behind it
-      mt.seg = v_seg & 3;
-      mt.opens = jv == 0;
+        tc::mbar_arrive(vr_empty + sr);
 #pragma unroll
-      for (int it = 0; it < v_it; ++it) {
-        const int idx = it * C::loaders + dt;
-        const int r = (idx & 7) + ((idx / (8 * chunks)) << 3), c = (idx >> 3) % chunks;
-        const int key = key0 + r;
-        dst[it] = make_uint4(0, 0, 0, 0);
-        if (key < gv.key_end) {
-          const int blk = __ldg(table + (key >> p.log_b));
-          if ((unsigned)blk < (unsigned)p.num_blocks)
-            dst[it] = ldg16(p.vc + ((size_t)blk * p.Hk + gv.head) * block_bytes +
-                            (size_t)(key & (B - 1)) * D + c * 16);
+        for (int it = 0; it < v_it; ++it) {
+          const uint4 w = raw[it];
+          unsigned char* at = dst + (it * rg_per + rg_in) * (D * 16) + c * 256 + r_in * 16;
+          *reinterpret_cast<uint4*>(at) = make_uint4(e4m3x2_half2(w.x), e4m3x2_half2(w.x >> 16),
+                                                     e4m3x2_half2(w.y), e4m3x2_half2(w.y >> 16));
+          *reinterpret_cast<uint4*>(at + 128) = make_uint4(e4m3x2_half2(w.z), e4m3x2_half2(w.z >> 16),
+                                                           e4m3x2_half2(w.w), e4m3x2_half2(w.w >> 16));
         }
+        tc::fence_smem_to_async();
+        tc::mbar_arrive(v_full + st);
       }
-      if (++jv == 2 * gv.count) {
-        jv = 0;
-        ++v_seg;
-        lv.u += gv.count;
-        have_v = lv.u < lv.u_end;
-        if (have_v) gv = seg_at(p, lv, kRows);
-      }
-    };
-    auto put_v = [&](uint4 (&src)[v_it], const VMeta& mt) {
-      const int st = v_half % C::VS;
-      if (v_half >= C::VS)
-        ok = ok && warp_wait(v_empty + st, (v_half / C::VS - 1) & 1, s_abort);
-      if (!ok) return;
-      unsigned char* dst = smem + C::o_v + st * C::v_stage;
-      // Where the tile's rows do not see the same keys, a weight of zero must not
-      // meet a NaN (0 x NaN is NaN): a NaN of V is written as zero and kept as
-      // the first key whose column has one.
-      const bool mixed = mt.key0 > mt.nan_base;
-      unsigned short* first_nan = s_nan + mt.seg * D;
-      if (mt.opens) {
-        for (int i = dt; i < D; i += C::loaders) first_nan[i] = 0xffff;
-        tc::mbar_arrive(nan_sync);
-        ok = warp_wait(nan_sync, nan_phase & 1, s_abort);
-        ++nan_phase;
-        if (!ok) return;
-      }
-#pragma unroll
-      for (int it = 0; it < v_it; ++it) {
-        const int idx = it * C::loaders + dt;
-        const int r = (idx & 7) + ((idx / (8 * chunks)) << 3), c = (idx >> 3) % chunks;
-        uint32_t w[4] = {src[it].x, src[it].y, src[it].z, src[it].w};
-        if (mixed) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if ((((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0) {
-              for (int b = 0; b < 4; ++b)
-                if (((w[k] >> (8 * b)) & 0x7fu) == 0x7fu) {
-                  unsigned short* at = first_nan + c * 16 + k * 4 + b;
-                  const unsigned short key = (unsigned short)(mt.key0 + r - mt.nan_base);
-                  unsigned short old = *reinterpret_cast<volatile unsigned short*>(at);
-                  while (key < old) {
-                    const unsigned short was = atomicCAS(at, old, key);
-                    if (was == old) break;
-                    old = was;
-                  }
-                  *s_any_nan = 1;
-                  w[k] &= ~(0xffu << (8 * b));
-                }
-            }
-          }
-        }
-        unsigned char* at = dst + (r >> 3) * (D * 16) + c * 256 + (r & 7) * 16;
-        *reinterpret_cast<uint4*>(at) = make_uint4(e4m3x2_half2(w[0]), e4m3x2_half2(w[0] >> 16),
-                                                   e4m3x2_half2(w[1]), e4m3x2_half2(w[1] >> 16));
-        *reinterpret_cast<uint4*>(at + 128) = make_uint4(e4m3x2_half2(w[2]), e4m3x2_half2(w[2] >> 16),
-                                                         e4m3x2_half2(w[3]), e4m3x2_half2(w[3] >> 16));
-      }
-      tc::fence_smem_to_async();
-      tc::mbar_arrive(v_full + st);
-      ++v_half;
-    };
-    long long left = max(0LL, l.u_end - l.u);         // units of this CTA
-#pragma unroll
-    for (int i = 0; i < C::KS; ++i) issue_k();
-    load_v(raw[0], meta[0]);
-    load_v(raw[1], meta[1]);
-    // K of unit `n` has landed: hand it over.
-    auto give_k = [&](int n) {
-      tc::fence_smem_to_async();
-      tc::mbar_arrive(k_full + n % C::KS);
-    };
-    if (left > 0 && ok) {
-      tc::cp_async_wait_group<C::KS - 1>();
-      give_k(0);
+      l.pass(g);
+      ++seg;
     }
-    for (int n = 0; ok && n < left; ++n) {
-      tc::cp_async_wait_group<C::KS - 2>();
-      if (n + 1 < left) give_k(n + 1);
-      put_v(raw[0], meta[0]);
-      load_v(raw[0], meta[0]);
-      if (ok) {
-        put_v(raw[1], meta[1]);
-        load_v(raw[1], meta[1]);
-      }
-      issue_k();
-    }
-    tc::cp_async_wait_group<0>();
   } else {
     // ======================= softmax of 128 rows ================================
     regs_up<C::soft_regs>();
@@ -562,53 +594,73 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const Args p) {
       return warp_wait(wg_sync + m, n_sync++ & 1, s_abort);
     };
     bool ok = true;
-    for (; ok && l.u < l.u_end;) {
+    while (ok && l.more()) {
       const Seg g = seg_at(p, l, kRows);
       const int row = g.row0 + m * 128 + r;
       const bool live = m * 128 + r < g.n_rows;
-      const int tok = row / G, hq = g.head * G + row - tok * G;
-      // ---- Q: hi and lo codes of this thread's row ------------------------------
+      const int tok = row / G, hq = l.head * G + row - tok * G;
+      // ---- Q: hi and lo codes, one power-of-two scale per row ---------------------
+      // A warp takes its 32 rows 8 at a time, 4 lanes to 64 bytes of a row, so that
+      // loads use whole sectors and the stores fill the core matrices in order.
       float rs = 0.f;
       {
-        const __nv_bfloat16* src = p.q + (int64_t)(g.s.first + tok) * p.q_stride + (int64_t)hq * D;
-        uint32_t top_bits = 0;                         // largest magnitude, as bits
-        if (live) {
-#pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 u = ldg16(src + c * 8);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        constexpr int passes = D / 32, at_once = 256 / D;   // 8 loads in flight
+        const int rr = lane & 7, cq = lane >> 3;
+        const float neg = p.scale_log2 < 0.f ? -1.f : 1.f;
+#pragma unroll 1
+        for (int g0 = 0; g0 < 4; g0 += at_once) {
+          uint4 w[at_once][passes];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              top_bits = max(top_bits, max((w[k] & 0x7fffu) << 16, w[k] & 0x7fff0000u));
+          for (int a = 0; a < at_once; ++a) {
+            const int local = m * 128 + (warp & 3) * 32 + (g0 + a) * 8 + rr;
+            const int qrow = g.row0 + local, qt = qrow / G;
+            const __nv_bfloat16* src = p.q + (int64_t)(g.s.first + qt) * p.q_stride +
+                                       (int64_t)(l.head * G + qrow - qt * G) * D + cq * 8;
+#pragma unroll
+            for (int k = 0; k < passes; ++k)
+              w[a][k] = local < g.n_rows ? ldg16(src + k * 32) : make_uint4(0, 0, 0, 0);
           }
-        }
-        const bool bad = top_bits >= 0x7f800000u;      // an infinity or NaN in the row
-        const int ex = max((int)(top_bits >> 23) - 127 - 7, -126);
-        const float inv = __int_as_float((127 - min(ex, 126)) << 23);
-        rs = bad ? __int_as_float(0x7fffffff) : __int_as_float((min(ex, 126) + 127) << 23);
-        rs *= fabsf(p.scale_log2);
-        const float sgn = p.scale_log2 < 0.f ? -inv : inv;
-        unsigned char* hi = smem + C::o_q + (m * 2) * C::q_part + (r >> 3) * (D * 8) + (r & 7) * 16;
-#pragma unroll 2
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t h4[4] = {0, 0, 0, 0}, l4[4] = {0, 0, 0, 0};
-          if (live && !bad) {
-            const uint4 ua = ldg16(src + c * 16), ub = ldg16(src + c * 16 + 8);
-            const uint32_t w[8] = {ua.x, ua.y, ua.z, ua.w, ub.x, ub.y, ub.z, ub.w};
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float a = bf16lo(w[k]) * sgn, b = bf16hi(w[k]) * sgn;
-              const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-              const uint32_t f = e4m3x2_half2(h2);
-              const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&f));
-              const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(a - hf.x, b - hf.y),
-                                                           __NV_SATFINITE, __NV_E4M3);
-              h4[k >> 1] |= h2 << (16 * (k & 1));
-              l4[k >> 1] |= l2 << (16 * (k & 1));
+          for (int a = 0; a < at_once; ++a) {
+            uint32_t top = 0;                          // largest magnitude, as bits
+#pragma unroll
+            for (int k = 0; k < passes; ++k) {
+              const uint32_t v[4] = {w[a][k].x, w[a][k].y, w[a][k].z, w[a][k].w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                top = max(top, max((v[i] & 0x7fffu) << 16, v[i] & 0x7fff0000u));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const bool bad = top >= 0x7f800000u;       // an infinity or NaN in the row
+            const int ex = min(max((int)(top >> 23) - 127 - 7, -126), 126);
+            const float inv = bad ? 0.f : neg * __int_as_float((127 - ex) << 23);
+            const float back = bad ? __int_as_float(0x7fffffff) : __int_as_float((ex + 127) << 23);
+            const float mine = __shfl_sync(0xffffffffu, back, lane & 7);
+            if ((lane >> 3) == g0 + a) rs = mine * fabsf(p.scale_log2);
+            unsigned char* hi = smem + C::o_q + m * 2 * C::q_part +
+                                ((warp & 3) * 4 + g0 + a) * (D * 8) + rr * 16 + (cq & 1) * 8 +
+                                (cq >> 1) * 128;
+#pragma unroll
+            for (int k = 0; k < passes; ++k) {
+              const uint32_t v[4] = {w[a][k].x, w[a][k].y, w[a][k].z, w[a][k].w};
+              uint32_t h4[2] = {0, 0}, l4[2] = {0, 0};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                // A row that is not finite is zeros here; its factor is NaN.
+                const float x0 = bad ? 0.f : bf16lo(v[i]) * inv, x1 = bad ? 0.f : bf16hi(v[i]) * inv;
+                const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t f = e4m3x2_half2(h2);
+                const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&f));
+                const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(x0 - hf.x, x1 - hf.y),
+                                                             __NV_SATFINITE, __NV_E4M3);
+                h4[i >> 1] |= h2 << (16 * (i & 1));
+                l4[i >> 1] |= l2 << (16 * (i & 1));
+              }
+              *reinterpret_cast<uint2*>(hi + k * 256) = make_uint2(h4[0], h4[1]);
+              *reinterpret_cast<uint2*>(hi + C::q_part + k * 256) = make_uint2(l4[0], l4[1]);
             }
           }
-          *reinterpret_cast<uint4*>(hi + c * 128) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
-          *reinterpret_cast<uint4*>(hi + C::q_part + c * 128) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
         }
         tc::fence_smem_to_async();
         tc::mbar_arrive(q_full + m);
@@ -741,10 +793,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const Args p) {
         __threadfence();
         ok = wg_barrier();
         if (!ok) break;
-        const long long at0 = (long long)g.head * l.units1 + g.cum;
+        const long long at0 = (long long)l.head * l.units1 + g.cum;
         const int c0 = (int)(at0 / l.per_cta), c1 = (int)((at0 + g.n_units - 1) / l.per_cta);
         if (r == 0) {
-          int* counter = p.tile_counters + ((size_t)g.lo * p.Hk + g.head) * kM + m;
+          int* counter = p.tile_counters + ((size_t)l.lo * p.Hk + l.head) * kM + m;
           const int seen = atomicAdd(counter, 1);
           s_flag[m] = seen == c1 - c0;
           if (seen == c1 - c0) *counter = 0;           // ready for the next call on this plan
@@ -787,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const Args p) {
         if (!ok) break;
       }
       tc::fence_before_sync();
-      l.u += g.count;
+      l.pass(g);
       ++seg;
     }
   }
@@ -798,13 +850,48 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const Args p) {
   if (warp == 12) tc::tmem_dealloc(tmem, 512);
 }
 
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The cache as (d, token of the block, block x head), boxes of `rows` tokens.
+bool cache_map(CUtensorMap* map, const void* cache, int d, int B, int64_t pages, int row, int rows) {
+  static const EncodeTiled encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<EncodeTiled>(fn);
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)B, (cuuint64_t)(pages > 0 ? pages : 1)};
+  const cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)d * B};
+  const cuuint32_t box[3] = {(cuuint32_t)row, (cuuint32_t)rows, 1}, step[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(cache), dims, strides, box,
+                step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D>
 gdn_status_t launch_tile(const Args& a, cudaStream_t st) {
   static const cudaError_t set = cudaFuncSetAttribute(
       attn_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TC<D>::total);
   if (set != cudaSuccess) return check_launch(set);
+  const int B = 1 << a.log_b;
+  const int64_t pages = (int64_t)a.num_blocks * a.Hk;
+  CUtensorMap k_map, v_map;
+  if (!cache_map(&k_map, a.kc, D, B, pages, TC<D>::row, std::min(B, kKeys)) ||
+      !cache_map(&v_map, a.vc, D, B, pages, TC<D>::row, std::min(B, kHalf))) {
+    set_cuda_error(cudaErrorInvalidValue);
+    return GDN_ERR_CUDA;
+  }
   return check_launch(launch_pdl(attn_tile_kernel<D>, dim3(a.tile_grid), dim3(kThreads),
-                                 TC<D>::total, st, a));
+                                 TC<D>::total, st, a, k_map, v_map));
 }
 
 }  // namespace
