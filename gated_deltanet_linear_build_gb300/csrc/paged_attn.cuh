@@ -30,7 +30,7 @@ struct Header {
 static_assert(sizeof(Header) == 256, "header is 256 bytes");
 
 constexpr int kUnit = 32;              // keys per unit of the split kernel
-constexpr int kTileKeys = 128;         // keys per unit of the tensor-core kernel
+constexpr int kTileKeys = 64;         // keys per unit of the tensor-core kernel
 
 // Where a CTA's piece of the work line begins.
 struct Start {

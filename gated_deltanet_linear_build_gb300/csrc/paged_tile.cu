@@ -5,8 +5,9 @@
 // long as the softmax (one exponential a pair) and the widening of V keep up.
 // One CTA per SM; a tile is 256 rows (d <= 128: two 128-row halves that take
 // turns on the tensor core) or 128 rows (d = 256, whose float32 output fills
-// half of the tensor memory; two score buffers take turns instead). Per 128
-// keys:
+// half of the tensor memory). Scores are kept two units of 64 keys ahead of the
+// softmax, so that neither it nor the tensor core waits for the other's
+// latency. Per unit:
 //
 // * S = Q K^T as e4m3 MMAs (kind::f8f6f4): K as it lies in the cache, Q as the
 //   sum of two e4m3 parts hi + lo, which hold BF16's 8 significand bits. Two
@@ -20,13 +21,13 @@
 //   - m), with P' / vs in the sum, per 16 keys (the smallest block). O is
 //   rescaled only when a row's maximum grows by more than 2^8.
 //
-// Work split: as in the split kernel, all (tile, kv head, 128 keys) units form
+// Work split: as in the split kernel, all (tile, kv head, 64 keys) units form
 // one line cut into equal pieces, one per SM; a tile cut by the end of a piece
 // leaves float32 partial results, joined in a fixed order by the warps that
 // arrive last.
 //
 // Roles (four warpgroups): 0 .. kM - 1: softmax of one 128-row tile each; the
-// others up to 2: widening of V; warp 12: MMAs; warp 13: TMA copies of K, and
+// others up to 2: Q, widening of V; warp 12: MMAs; warp 13: TMA copies of K, and
 // the blocks' scales; warp 14: TMA copies of V's codes.
 // K and V's codes lie as TMA leaves them, rows of 128 (64 for d = 64) bytes
 // with their 16-byte chunks XOR-swizzled; Q and the widened V as 8 x 16-byte
@@ -46,7 +47,6 @@ using namespace attn;
 
 constexpr int kThreads = 512;
 constexpr int kKeys = kTileKeys;         // keys per unit
-constexpr int kHalf = 64;                // keys per V stage
 // Registers: four warpgroups are launched with 128 a thread; their shares add
 // up to no more than 4 x 128.
 constexpr int kLaunchRegs = 128;
@@ -54,37 +54,40 @@ constexpr int kLaunchRegs = 128;
 template <int D>
 struct TC {
   static constexpr int M = D == 256 ? 1 : 2;            // 128-row tiles
-  static constexpr int KS = D == 256 ? 2 : 3;           // K stages of 128 keys
-  static constexpr int VR = D == 256 ? 2 : 4;           // stages of 64 keys of V's codes
+  static constexpr int KS = D == 256 ? 4 : 6;           // K stages
+  static constexpr int VR = D == 256 ? 2 : 4;           // stages of V's codes
   static constexpr int VS = D == 256 ? 2 : 4;           // and of V widened
   static constexpr int loaders = (3 - M) * 128;
   static constexpr int row = D == 64 ? 64 : 128;        // bytes of a row in a TMA box
   static constexpr int boxes = D / row;                 // boxes across a cache row
   static constexpr int q_part = 128 * D;                // one part (hi or lo) of one tile
-  static constexpr int k_stage = kKeys * D;
-  static constexpr int vr_stage = kHalf * D;
-  static constexpr int v_stage = kHalf * D * 2;
+  static constexpr int c_stage = kKeys * D;             // a unit's codes of K or V
+  static constexpr int v_stage = kKeys * D * 2;
   static constexpr int o_q = 0;
   static constexpr int o_k = o_q + M * 2 * q_part;
-  static constexpr int o_vr = o_k + KS * k_stage;
-  static constexpr int o_v = o_vr + VR * vr_stage;
-  // Scales of a unit's 8 groups of 16 keys, float [4 units][ks | log2 vs | 1 / vs][8].
-  // A unit is copied at most 3 units ahead of the softmax that reads its scales.
+  static constexpr int o_vr = o_k + KS * c_stage;
+  static constexpr int o_v = o_vr + VR * c_stage;
+  // Scales of a unit's 4 groups of 16 keys, float [8 units][ks | log2 vs | 1 / vs][4].
+  // Unit n + KS is copied once the scores of n are done, so once the softmax of
+  // n - 2 is: KS + 2 units are alive.
   static constexpr int o_sc = o_v + VS * v_stage;
-  // First key of a segment whose V is NaN in a column, uint16 [4 segments][D]. V
-  // is widened at most 3 units, hence segments, ahead of the results.
-  static constexpr int o_nan = o_sc + 4 * 24 * 4;
-  static constexpr int o_bar = o_nan + 4 * D * 2;
-  static constexpr int n_bar = 2 * KS + 2 * VR + 2 * VS + 4 + 2 + 2 + 2 + 2 + 2 + 2;
+  static_assert(KS + 2 <= 8, "ring of scales");
+  // First key of a segment whose V is NaN in a column, uint16 [NR segments][D]. V
+  // is widened at most VS units, hence segments, ahead of the results.
+  static constexpr int NR = D == 256 ? 3 : 8;
+  static_assert(VS < NR, "ring of NaN marks");
+  static constexpr int o_nan = o_sc + 8 * 12 * 4;
+  // Exponents of the rows' scales, int8 [2 segments][rows].
+  static constexpr int o_ex = o_nan + NR * D * 2;
+  static constexpr int o_bar = o_ex + 2 * M * 128;
+  static constexpr int n_bar = 2 * KS + 2 * VR + 2 * VS + 8 + 4 + 4 + 4 + 2 + 2 + 2;
   static constexpr int o_misc = o_bar + n_bar * 8;      // tmem base, abort, flags
   static constexpr int total = o_misc + 32;
   static_assert(total <= 232448, "shared memory of one CTA");
-  static constexpr int soft_regs = M == 2 ? 184 : 216, load_regs = M == 2 ? 88 : 120,
-                       mma_regs = 56;
-  static_assert(M * soft_regs + (3 - M) * load_regs + mma_regs <= 4 * kLaunchRegs,
-                "registers of the launch");
-  // Tensor-memory columns.
-  static constexpr int c_s(int i) { return i * 128; }
+  static constexpr int regs = 152, mma_regs = 56;
+  static_assert(3 * regs + mma_regs <= 4 * kLaunchRegs, "registers of the launch");
+  // Tensor-memory columns: two score buffers of 64 keys per tile, then O.
+  static constexpr int c_s(int m, int b) { return m * 128 + b * 64; }
   static constexpr int c_o(int m) { return 256 + m * D; }
 };
 
@@ -251,19 +254,23 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
   uint64_t* vr_empty = vr_full + C::VR;
   uint64_t* v_full = vr_empty + C::VR;
   uint64_t* v_empty = v_full + C::VS;
-  uint64_t* sc_full = v_empty + C::VS;       // [4]
-  uint64_t* s_full = sc_full + 4;            // [2] score buffers
-  uint64_t* p_full = s_full + 2;             // [2]
-  uint64_t* o_done = p_full + 2;             // [kM]
-  uint64_t* q_full = o_done + 2;             // [kM]
+  uint64_t* sc_full = v_empty + C::VS;       // [8]
+  uint64_t* s_full = sc_full + 8;            // [kM][2] score buffers
+  uint64_t* p_full = s_full + 4;             // [kM][2]
+  // Products done, [kM][2] by the unit's parity, and Q, [2] by the segment's: the
+  // softmax does not wait for every one of them, and with two barriers none is
+  // more than one phase away from what it waits for.
+  uint64_t* o_done = p_full + 4;
+  uint64_t* q_full = o_done + 4;
   uint64_t* wg_sync = q_full + 2;            // [kM] a softmax warpgroup among itself
-  uint64_t* nan_sync = wg_sync + 2;          // the loaders among themselves
+  uint64_t* nan_sync = wg_sync + 2;          // the widening threads among themselves
   uint64_t* drained = nan_sync + 1;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::o_misc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::o_misc + 4);
   int* s_flag = reinterpret_cast<int*>(smem + C::o_misc + 8);     // [2] this warpgroup joins
   volatile int* s_any_nan = reinterpret_cast<volatile int*>(smem + C::o_misc + 16);
   float* s_sc = reinterpret_cast<float*>(smem + C::o_sc);
+  signed char* s_ex = reinterpret_cast<signed char*>(smem + C::o_ex);
   unsigned short* s_nan = reinterpret_cast<unsigned short*>(smem + C::o_nan);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = tid >> 7;
   const int G = p.Hq / p.Hk, B = 1 << p.log_b;
@@ -281,14 +288,14 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       tc::mbar_init(v_full + i, C::loaders);
       tc::mbar_init(v_empty + i, 1);
     }
-    for (int i = 0; i < 4; ++i) tc::mbar_init(sc_full + i, 8);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 8; ++i) tc::mbar_init(sc_full + i, 4);
+    for (int i = 0; i < 4; ++i) {
       tc::mbar_init(s_full + i, 1);
       tc::mbar_init(p_full + i, 128);
       tc::mbar_init(o_done + i, 1);
-      tc::mbar_init(q_full + i, 128);
-      tc::mbar_init(wg_sync + i, 128);
     }
+    for (int i = 0; i < 2; ++i) tc::mbar_init(wg_sync + i, 128);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(q_full + i, C::loaders);
     tc::mbar_init(nan_sync, C::loaders);
     tc::mbar_init(drained, 1);
     *s_abort = 0;
@@ -318,12 +325,18 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       const uint32_t id_pv = idesc_f32(128, D) | tc::kTransB;
       const uint32_t sq = tc::smem_u32(smem + C::o_q), sk = tc::smem_u32(smem + C::o_k),
                      sv = tc::smem_u32(smem + C::o_v);
-      int unit = 0, halves = 0, segs = 0;      // running counts: stages and phases
-      int n_p[2] = {0, 0};
+      int unit = 0, segs = 0;                  // running counts: stages and phases
       bool ok = true;
-      auto qk = [&](int m, int buf, int stage) {
-        const uint32_t d = tmem + C::c_s(buf);
-        const uint64_t b = desc_swizzled<C::row>(sk + stage * C::k_stage);
+      // S of unit u for every tile, two units ahead of the softmax.
+      auto qk = [&](int u, int m) {
+        const int st = u % C::KS;
+        if (m == 0) {
+          ok = ok && warp_wait(k_full + st, (u / C::KS) & 1, s_abort);
+          tc::fence_after_sync();
+        }
+        if (!ok) return;
+        const uint32_t d = tmem + m * 128 + (u & 1) * 64;
+        const uint64_t b = desc_swizzled<C::row>(sk + st * C::c_stage);
         const uint64_t a = tc::tile_desc(sq + m * 2 * C::q_part, D / 2, 0);
         if (one) {
 #pragma unroll
@@ -333,84 +346,35 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
               mma_f8(d, a + part * (C::q_part / 16) + k * 16,
                      b + (k * 32 / C::row) * (kKeys * C::row / 16) + (k * 32 % C::row) / 16, id_qk,
                      part | k);
-          tc::mma_commit(s_full + buf);
-        }
-      };
-      auto wait_k = [&](int u) {
-        ok = ok && warp_wait(k_full + u % C::KS, (u / C::KS) & 1, s_abort);
-        tc::fence_after_sync();
-      };
-      auto pv = [&](int m, int buf, int h0, bool first, bool wait_v, bool free_v) {
-        const uint32_t d = tmem + C::c_o(m), a = tmem + C::c_s(buf);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int h = h0 + half, st = h % C::VS;
-          if (wait_v) {
-            ok = ok && warp_wait(v_full + st, (h / C::VS) & 1, s_abort);
-            tc::fence_after_sync();
-          }
-          if (!ok) return;
-          const uint64_t b = tc::mn_desc(sv + st * C::v_stage, D, 0);
-          if (one) {
-#pragma unroll
-            for (int k = 0; k < kHalf / 16; ++k)
-              tc::mma_bf16_tmem_a(d, a + half * 32 + k * 8, b + k * 2 * D, id_pv,
-                                  !(first && half == 0 && k == 0));
-            if (free_v) tc::mma_commit(v_empty + st);
-            if (half == 1) tc::mma_commit(o_done + m);
-          }
+          tc::mma_commit(s_full + m * 2 + (u & 1));
+          if (m == kM - 1) tc::mma_commit(k_empty + st);
         }
       };
       while (ok && l.more()) {
         const Seg g = seg_at(p, l, kRows);
-#pragma unroll
-        for (int m = 0; m < kM; ++m)
-          ok = ok && warp_wait(q_full + m, segs & 1, s_abort);
+        ok = ok && warp_wait(q_full + (segs & 1), (segs >> 1) & 1, s_abort);
         tc::fence_after_sync();
-        if constexpr (kM == 2) {
-          wait_k(unit);
-          if (!ok) break;
-          qk(0, 0, unit % C::KS);
-          qk(1, 1, unit % C::KS);
-          if (one) tc::mma_commit(k_empty + unit % C::KS);
-          for (int j = 0; ok && j < g.count; ++j) {
+        for (int u = 0; ok && u < min(2, g.count); ++u)
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              ok = ok && warp_wait(p_full + m, n_p[m] & 1, s_abort);
-              ++n_p[m];
-              tc::fence_after_sync();
-              if (!ok) break;
-              pv(m, m, halves, j == 0, m == 0, m == 1);
-              if (j + 1 < g.count) {
-                if (m == 0) wait_k(unit + 1);
-                if (!ok) break;
-                qk(m, m, (unit + 1) % C::KS);
-                if (m == 1 && one) tc::mma_commit(k_empty + (unit + 1) % C::KS);
-              }
-            }
-            ++unit;
-            halves += 2;
-          }
-        } else {
-          wait_k(unit);
-          if (!ok) break;
-          qk(0, unit & 1, unit % C::KS);
-          if (one) tc::mma_commit(k_empty + unit % C::KS);
-          for (int j = 0; ok && j < g.count; ++j) {
-            if (j + 1 < g.count) {
-              wait_k(unit + 1);
-              if (!ok) break;
-              qk(0, (unit + 1) & 1, (unit + 1) % C::KS);
-              if (one) tc::mma_commit(k_empty + (unit + 1) % C::KS);
-            }
-            const int b = unit & 1;
-            ok = ok && warp_wait(p_full + b, n_p[b] & 1, s_abort);
-            ++n_p[b];
+          for (int m = 0; m < kM; ++m) qk(unit + u, m);
+        for (int j = 0; ok && j < g.count; ++j, ++unit) {
+#pragma unroll
+          for (int m = 0; m < kM; ++m) {
+            ok = ok && warp_wait(p_full + m * 2 + (unit & 1), (unit >> 1) & 1, s_abort);
+            const int st = unit % C::VS;
+            if (m == 0) ok = ok && warp_wait(v_full + st, (unit / C::VS) & 1, s_abort);
             tc::fence_after_sync();
             if (!ok) break;
-            pv(0, b, halves, j == 0, true, true);
-            ++unit;
-            halves += 2;
+            const uint32_t d = tmem + C::c_o(m), a = tmem + m * 128 + (unit & 1) * 64;
+            const uint64_t b = tc::mn_desc(sv + st * C::v_stage, D, 0);
+            if (one) {
+#pragma unroll
+              for (int k = 0; k < kKeys / 16; ++k)
+                tc::mma_bf16_tmem_a(d, a + k * 8, b + k * 2 * D, id_pv, j > 0 || k > 0);
+              tc::mma_commit(o_done + m * 2 + (unit & 1));
+              if (m == kM - 1) tc::mma_commit(v_empty + st);
+            }
+            if (j + 2 < g.count) qk(unit + 2, m);
           }
         }
         ++segs;
@@ -422,18 +386,18 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       __syncwarp();
     } else if (warp == 13 || warp == 14) {
       // ===================== TMA copies ==========================================
-      // Warp 13: K units and their scales; warp 14: halves of V. Lane i posts box
-      // i: one page (or its part in the unit) times one of the boxes across a row.
+      // Warp 13: K and the units' scales; warp 14: V's codes. Lane i posts box i:
+      // one page (or its part in the unit) times one of the boxes across a row.
       const bool is_k = warp == 13;
-      const int keys = is_k ? kKeys : kHalf;
-      const int box_keys = min(B, keys), log_box = p.log_b < (is_k ? 7 : 6) ? p.log_b : (is_k ? 7 : 6);
-      const int pages = keys >> log_box;
+      const int log_box = min(p.log_b, 6), box_keys = 1 << log_box;
+      static_assert(kKeys == 64, "log_box");
+      const int pages = kKeys >> log_box;
       const int page = lane % pages, bx = lane / pages;
       const bool posts = lane < pages * C::boxes;
       const CUtensorMap* map = is_k ? &k_map : &v_map;
       uint64_t* full = is_k ? k_full : vr_full;
       uint64_t* empty = is_k ? k_empty : vr_empty;
-      const int stages = is_k ? C::KS : C::VR, stage_bytes = is_k ? C::k_stage : C::vr_stage;
+      const int stages = is_k ? C::KS : C::VR;
       unsigned char* base = smem + (is_k ? C::o_k : C::o_vr);
       const int absent = max(p.num_blocks * p.Hk, 1);   // a box past the end reads zeros
       int st = 0, round = 0, unit = 0;
@@ -442,9 +406,9 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         const Seg g = seg_at(p, l, kRows);
         const int32_t* table = p.table + (int64_t)g.seq * p.table_stride;
         const int key_first = g.first_unit * kKeys;
-        const int n = is_k ? g.count : 2 * g.count;
+        const int n = g.count;
         auto id_at = [&](int i) {
-          const int key = key_first + i * keys + page * box_keys;
+          const int key = key_first + i * kKeys + page * box_keys;
           return i < n && key < g.key_end ? __ldg(table + (key >> p.log_b)) : -1;
         };
         int next = id_at(0);
@@ -453,31 +417,31 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
           next = id_at(i + 1);
           if (round > 0) ok = ok && warp_wait(empty + st, (round - 1) & 1, s_abort);
           if (!ok) break;
-          const int key0 = key_first + i * keys;
+          const int key0 = key_first + i * kKeys;
           const int key = key0 + page * box_keys;
-          if (lane == 0) tc::mbar_arrive_expect_tx(full + st, stage_bytes);
+          if (lane == 0) tc::mbar_arrive_expect_tx(full + st, C::c_stage);
           __syncwarp();
           if (posts) {
             const bool in = (unsigned)id < (unsigned)p.num_blocks;
             if (!in && is_k && key < g.key_end) record_device_status(GDN_ERR_INVALID_ARG);
-            tma_box(base + st * stage_bytes + (bx * keys + page * box_keys) * C::row, map, bx * C::row,
+            tma_box(base + st * C::c_stage + (bx * kKeys + page * box_keys) * C::row, map, bx * C::row,
                     key & (B - 1), in ? id * p.Hk + l.head : absent, full + st);
           }
           if (is_k) {
-            // Scales of the unit's 8 groups of 16 keys.
-            const int blk = __shfl_sync(0xffffffffu, id, ((lane & 7) * 16) >> log_box);
-            if (lane < 8) {
+            // Scales of the unit's 4 groups of 16 keys.
+            const int blk = __shfl_sync(0xffffffffu, id, ((lane & 3) * 16) >> log_box);
+            if (lane < 4) {
               float a = 1.f, v = 1.f;
               if (key0 + lane * 16 < g.key_end && (unsigned)blk < (unsigned)p.num_blocks) {
                 a = __ldg(p.ks + (size_t)blk * p.Hk + l.head);
                 v = __ldg(p.vs + (size_t)blk * p.Hk + l.head);
               }
               v = fmaxf(v, 7.888609052210118e-31f);     // 2^-100
-              float* sc = s_sc + (unit & 3) * 24;
+              float* sc = s_sc + (unit & 7) * 12;
               sc[lane] = a;
-              sc[8 + lane] = lg2_approx(v);
-              sc[16 + lane] = __fdividef(1.f, v);
-              tc::mbar_arrive(sc_full + (unit & 3));
+              sc[4 + lane] = lg2_approx(v);
+              sc[8 + lane] = __fdividef(1.f, v);
+              tc::mbar_arrive(sc_full + (unit & 7));
             }
             __syncwarp();
             ++unit;
@@ -498,26 +462,99 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       }
     }
   } else if (wg >= kM) {
-    // ======================= widening of V ======================================
-    regs_down<C::load_regs>();
+    // ======================= Q, widening of V ====================================
+    regs_up<C::regs>();
     const int dt = tid - kM * 128;                    // 0 .. loaders - 1
     constexpr int chunks = D / 16;
-    constexpr int v_it = kHalf * chunks / C::loaders;
+    constexpr int v_it = kKeys * chunks / C::loaders;
     const int r_in = dt & 7, c = (dt >> 3) % chunks;  // this thread's row of 8, its chunk
     const int rg_in = dt / (8 * chunks);              // and its group of 8 rows in a pass
     constexpr int rg_per = C::loaders / (8 * chunks); // groups of 8 rows per pass
-    int half = 0, nan_phase = 0, seg = 0;             // running counts
+    int unit = 0, nan_phase = 0, seg = 0;             // running counts
     bool ok = true;
     while (ok && l.more()) {
       const Seg g = seg_at(p, l, kRows);
-      const int nan_base = visible(g.s, g.row0 / G) - kHalf;   // every row sees the 64 keys behind it
-      unsigned short* first_nan = s_nan + (seg & 3) * D;
-      for (int i = 0; ok && i < 2 * g.count; ++i, ++half) {
-        const int key0 = g.first_unit * kKeys + i * kHalf;
-        const int sr = half % C::VR, st = half % C::VS;
-        ok = ok && warp_wait(vr_full + sr, (half / C::VR) & 1, s_abort);
-        if (half >= C::VS)
-          ok = ok && warp_wait(v_empty + st, (half / C::VS - 1) & 1, s_abort);
+      // ---- Q: hi and lo codes, one power-of-two scale per row ---------------------
+      // 8 rows at a time, 4 lanes to 64 bytes of a row, so that loads use whole
+      // sectors and the stores fill the core matrices in order.
+      {
+        constexpr int passes = D / 32, at_once = 64 / passes / 4;   // 16 loads in flight
+        constexpr int groups = kRows / 8 / (C::loaders / 32);       // of 8 rows, per warp
+        static_assert(groups % at_once == 0, "groups of rows");
+        const int rr = lane & 7, cq = lane >> 3;
+        const float neg = p.scale_log2 < 0.f ? -1.f : 1.f;
+#pragma unroll 1
+        for (int g0 = 0; g0 < groups; g0 += at_once) {
+          uint4 w[at_once][passes];
+#pragma unroll
+          for (int a = 0; a < at_once; ++a) {
+            const int local = ((dt >> 5) * groups + g0 + a) * 8 + rr;
+            const int qrow = g.row0 + local, qt = qrow / G;
+            const __nv_bfloat16* src = p.q + (int64_t)(g.s.first + qt) * p.q_stride +
+                                       (int64_t)(l.head * G + qrow - qt * G) * D + cq * 8;
+#pragma unroll
+            for (int k = 0; k < passes; ++k)
+              w[a][k] = local < g.n_rows ? ldg16(src + k * 32) : make_uint4(0, 0, 0, 0);
+          }
+          if (g0 == 0 && unit > 0) {
+            // The last scores of the segment before are done with Q's place.
+            ok = ok && warp_wait(k_empty + (unit - 1) % C::KS, ((unit - 1) / C::KS) & 1, s_abort);
+            if (!ok) break;
+          }
+#pragma unroll
+          for (int a = 0; a < at_once; ++a) {
+            const int local = ((dt >> 5) * groups + g0 + a) * 8 + rr;
+            uint32_t top = 0;                          // largest magnitude, as bits
+#pragma unroll
+            for (int k = 0; k < passes; ++k) {
+              const uint32_t v[4] = {w[a][k].x, w[a][k].y, w[a][k].z, w[a][k].w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                top = max(top, max((v[i] & 0x7fffu) << 16, v[i] & 0x7fff0000u));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            // The row's largest magnitude goes to [128, 256). A row with an infinity
+            // or NaN is zeros here, and marked by the exponent -128.
+            const bool bad = top >= 0x7f800000u;
+            const int ex = min(max((int)(top >> 23) - 127 - 7, -126), 126);
+            const float inv = bad ? 0.f : neg * __int_as_float((127 - ex) << 23);
+            if (cq == 0) s_ex[(seg & 1) * kRows + local] = (signed char)(bad ? -128 : ex);
+            unsigned char* hi = smem + C::o_q + (local >> 7) * 2 * C::q_part +
+                                ((local & 127) >> 3) * (D * 8) + rr * 16 + (cq & 1) * 8 +
+                                (cq >> 1) * 128;
+#pragma unroll
+            for (int k = 0; k < passes; ++k) {
+              const uint32_t v[4] = {w[a][k].x, w[a][k].y, w[a][k].z, w[a][k].w};
+              uint32_t h4[2] = {0, 0}, l4[2] = {0, 0};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float x0 = bad ? 0.f : bf16lo(v[i]) * inv, x1 = bad ? 0.f : bf16hi(v[i]) * inv;
+                const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t f = e4m3x2_half2(h2);
+                const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&f));
+                const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(x0 - hf.x, x1 - hf.y),
+                                                             __NV_SATFINITE, __NV_E4M3);
+                h4[i >> 1] |= h2 << (16 * (i & 1));
+                l4[i >> 1] |= l2 << (16 * (i & 1));
+              }
+              *reinterpret_cast<uint2*>(hi + k * 256) = make_uint2(h4[0], h4[1]);
+              *reinterpret_cast<uint2*>(hi + C::q_part + k * 256) = make_uint2(l4[0], l4[1]);
+            }
+          }
+        }
+        if (!ok) break;
+        tc::fence_smem_to_async();
+        tc::mbar_arrive(q_full + (seg & 1));
+      }
+      const int nan_base = visible(g.s, g.row0 / G) - kKeys;   // every row sees the unit behind it
+      unsigned short* first_nan = s_nan + (seg % C::NR) * D;
+      for (int i = 0; ok && i < g.count; ++i, ++unit) {
+        const int key0 = (g.first_unit + i) * kKeys;
+        const int sr = unit % C::VR, st = unit % C::VS;
+        ok = ok && warp_wait(vr_full + sr, (unit / C::VR) & 1, s_abort);
+        if (unit >= C::VS)
+          ok = ok && warp_wait(v_empty + st, (unit / C::VS - 1) & 1, s_abort);
         if (!ok) break;
         if (i == 0) {
           for (int k = dt; k < D; k += C::loaders) first_nan[k] = 0xffff;
@@ -526,8 +563,8 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
           ++nan_phase;
           if (!ok) break;
         }
-        const unsigned char* src = smem + C::o_vr + sr * C::vr_stage +
-                                   (c * 16 / C::row) * (kHalf * C::row);
+        const unsigned char* src = smem + C::o_vr + sr * C::c_stage +
+                                   (c * 16 / C::row) * (kKeys * C::row);
         uint4 raw[v_it];
 #pragma unroll
         for (int it = 0; it < v_it; ++it)
@@ -584,10 +621,10 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
     }
   } else {
     // ======================= softmax of 128 rows ================================
-    regs_up<C::soft_regs>();
+    regs_up<C::regs>();
     const int m = wg, r = tid & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    int n_o = 0, unit = 0, seg = 0, n_sync = 0;
+    int unit = 0, seg = 0, n_sync = 0;
     // All 128 threads of the warpgroup, or false when the CTA gave up.
     auto wg_barrier = [&]() {
       tc::mbar_arrive(wg_sync + m);
@@ -599,103 +636,50 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       const int row = g.row0 + m * 128 + r;
       const bool live = m * 128 + r < g.n_rows;
       const int tok = row / G, hq = l.head * G + row - tok * G;
-      // ---- Q: hi and lo codes, one power-of-two scale per row ---------------------
-      // A warp takes its 32 rows 8 at a time, 4 lanes to 64 bytes of a row, so that
-      // loads use whole sectors and the stores fill the core matrices in order.
-      float rs = 0.f;
-      {
-        constexpr int passes = D / 32, at_once = 256 / D;   // 8 loads in flight
-        const int rr = lane & 7, cq = lane >> 3;
-        const float neg = p.scale_log2 < 0.f ? -1.f : 1.f;
-#pragma unroll 1
-        for (int g0 = 0; g0 < 4; g0 += at_once) {
-          uint4 w[at_once][passes];
-#pragma unroll
-          for (int a = 0; a < at_once; ++a) {
-            const int local = m * 128 + (warp & 3) * 32 + (g0 + a) * 8 + rr;
-            const int qrow = g.row0 + local, qt = qrow / G;
-            const __nv_bfloat16* src = p.q + (int64_t)(g.s.first + qt) * p.q_stride +
-                                       (int64_t)(l.head * G + qrow - qt * G) * D + cq * 8;
-#pragma unroll
-            for (int k = 0; k < passes; ++k)
-              w[a][k] = local < g.n_rows ? ldg16(src + k * 32) : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int a = 0; a < at_once; ++a) {
-            uint32_t top = 0;                          // largest magnitude, as bits
-#pragma unroll
-            for (int k = 0; k < passes; ++k) {
-              const uint32_t v[4] = {w[a][k].x, w[a][k].y, w[a][k].z, w[a][k].w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                top = max(top, max((v[i] & 0x7fffu) << 16, v[i] & 0x7fff0000u));
-            }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const bool bad = top >= 0x7f800000u;       // an infinity or NaN in the row
-            const int ex = min(max((int)(top >> 23) - 127 - 7, -126), 126);
-            const float inv = bad ? 0.f : neg * __int_as_float((127 - ex) << 23);
-            const float back = bad ? __int_as_float(0x7fffffff) : __int_as_float((ex + 127) << 23);
-            const float mine = __shfl_sync(0xffffffffu, back, lane & 7);
-            if ((lane >> 3) == g0 + a) rs = mine * fabsf(p.scale_log2);
-            unsigned char* hi = smem + C::o_q + m * 2 * C::q_part +
-                                ((warp & 3) * 4 + g0 + a) * (D * 8) + rr * 16 + (cq & 1) * 8 +
-                                (cq >> 1) * 128;
-#pragma unroll
-            for (int k = 0; k < passes; ++k) {
-              const uint32_t v[4] = {w[a][k].x, w[a][k].y, w[a][k].z, w[a][k].w};
-              uint32_t h4[2] = {0, 0}, l4[2] = {0, 0};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                // A row that is not finite is zeros here; its factor is NaN.
-                const float x0 = bad ? 0.f : bf16lo(v[i]) * inv, x1 = bad ? 0.f : bf16hi(v[i]) * inv;
-                const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t f = e4m3x2_half2(h2);
-                const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&f));
-                const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(x0 - hf.x, x1 - hf.y),
-                                                             __NV_SATFINITE, __NV_E4M3);
-                h4[i >> 1] |= h2 << (16 * (i & 1));
-                l4[i >> 1] |= l2 << (16 * (i & 1));
-              }
-              *reinterpret_cast<uint2*>(hi + k * 256) = make_uint2(h4[0], h4[1]);
-              *reinterpret_cast<uint2*>(hi + C::q_part + k * 256) = make_uint2(l4[0], l4[1]);
-            }
-          }
-        }
-        tc::fence_smem_to_async();
-        tc::mbar_arrive(q_full + m);
-      }
+      ok = ok && warp_wait(q_full + (seg & 1), (seg >> 1) & 1, s_abort);
+      if (!ok) break;
+      const int ex = s_ex[(seg & 1) * kRows + m * 128 + r];
+      const float rs = fabsf(p.scale_log2) * (ex == -128 ? __int_as_float(0x7fffffff)
+                                                         : __int_as_float((ex + 127) << 23));
       const int lim = live ? visible(g.s, tok) : 0;
       const int min_lim = visible(g.s, (g.row0 + m * 128) / G);
-      const int nan_base = visible(g.s, g.row0 / G) - kHalf;
+      const int nan_base = visible(g.s, g.row0 / G) - kKeys;
       const bool part_tile = m * 128 + 128 > g.n_rows;
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < g.count; ++j, ++unit) {
-        const int buf = kM == 2 ? m : (unit & 1);
-        const int ph = kM == 2 ? (unit & 1) : ((unit >> 1) & 1);
-        ok = ok && warp_wait(s_full + buf, ph, s_abort);
-        ok = ok && warp_wait(sc_full + (unit & 3), (unit >> 2) & 1, s_abort);
+        const int buf = m * 2 + (unit & 1);
+        ok = ok && warp_wait(s_full + buf, (unit >> 1) & 1, s_abort);
+        ok = ok && warp_wait(sc_full + (unit & 7), (unit >> 3) & 1, s_abort);
         if (!ok) break;
         tc::fence_after_sync();
-        float x[128];
-        const uint32_t ts = tmem + lane_base + C::c_s(buf);
+        float x[64];
+        const uint32_t ts = tmem + lane_base + m * 128 + (unit & 1) * 64;
+        tmem_ld32_async(ts, x);
+        tmem_ld32_async(ts + 32, x + 32);
+        const float* sc = s_sc + (unit & 7) * 12;
+        float fa[4], fb[4], fi[4];
+        *reinterpret_cast<float4*>(fa) = *reinterpret_cast<const float4*>(sc);
+        *reinterpret_cast<float4*>(fb) = *reinterpret_cast<const float4*>(sc + 4);
+        *reinterpret_cast<float4*>(fi) = *reinterpret_cast<const float4*>(sc + 8);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_async(ts + c * 32, x + c * 32);
+        for (int gr = 0; gr < 4; ++gr) fa[gr] = factor(rs * fa[gr]);
         tmem_wait_ld();
-        const float* sc = s_sc + (unit & 3) * 24;
         const int key0 = (g.first_unit + j) * kKeys;
         if (part_tile || key0 + kKeys > min_lim) {
 #pragma unroll
-          for (int k = 0; k < 128; ++k)
+          for (int k = 0; k < 64; ++k)
             if (key0 + k >= lim) x[k] = -INFINITY;
         }
         float mx = -INFINITY;
 #pragma unroll
-        for (int gr = 0; gr < 8; ++gr) {
-          float gm = x[gr * 16];
+        for (int gr = 0; gr < 4; ++gr) {
+          float g0 = x[gr * 16], g1 = x[gr * 16 + 1];
 #pragma unroll
-          for (int k = 1; k < 16; ++k) gm = fmaxf(gm, x[gr * 16 + k]);
-          mx = fmaxf(mx, fmaf(gm, factor(rs * sc[gr]), sc[8 + gr]));
+          for (int k = 2; k < 16; k += 2) {
+            g0 = fmaxf(g0, x[gr * 16 + k]);
+            g1 = fmaxf(g1, x[gr * 16 + k + 1]);
+          }
+          mx = fmaxf(mx, fmaf(fmaxf(g0, g1), fa[gr], fb[gr]));
         }
         if (__any_sync(0xffffffffu, mx > m_run + 8.f)) {
           const float m_new = fmaxf(mx, m_run);
@@ -703,8 +687,8 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
           m_run = m_new;
           l_run *= al;
           if (j > 0) {
-            // The products of the previous unit are in O; this unit's wait for P.
-            ok = ok && warp_wait(o_done + m, (n_o - 1) & 1, s_abort);
+            // The products of the unit before are in O; this unit's wait for P.
+            ok = ok && warp_wait(o_done + m * 2 + ((unit - 1) & 1), ((unit - 1) >> 1) & 1, s_abort);
             if (!ok) break;
             tc::fence_after_sync();
             const uint32_t to = tmem + lane_base + C::c_o(m);
@@ -721,39 +705,32 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
           }
         }
         const float ref = (m_run == -INFINITY ? 0.f : m_run) - 7.f;
-        uint32_t pk[64];
+        uint32_t pk[32];
         float lsum = 0.f;
 #pragma unroll
-        for (int gr = 0; gr < 8; ++gr) {
-          const float a = factor(rs * sc[gr]), b = sc[8 + gr] - ref;
-          const float2 a2 = make_float2(a, a), b2 = make_float2(b, b);
+        for (int gr = 0; gr < 4; ++gr) {
+          const float2 a2 = make_float2(fa[gr], fa[gr]), b2 = make_float2(fb[gr] - ref, fb[gr] - ref);
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            float2 v = make_float2(x[gr * 16 + 2 * k], x[gr * 16 + 2 * k + 1]);
-            v = fma2(v, a2, b2);
+            float2 v = fma2(make_float2(x[gr * 16 + 2 * k], x[gr * 16 + 2 * k + 1]), a2, b2);
             v.x = ex2_approx(v.x);
             v.y = ex2_approx(v.y);
             sum = add2(sum, v);
             const __half2 h = __floats2half2_rn(v.x, v.y);
             pk[gr * 8 + k] = *reinterpret_cast<const uint32_t*>(&h);
           }
-          lsum = fmaf(sum.x + sum.y, sc[16 + gr], lsum);
+          lsum = fmaf(sum.x + sum.y, fi[gr], lsum);
         }
         l_run += lsum;
         tmem_st32_async(ts, pk);
-        tmem_st32_async(ts + 32, pk + 32);
         tmem_wait_st();
         tc::fence_before_sync();
         tc::mbar_arrive(p_full + buf);
-        ++n_o;
       }
       if (!ok) break;
       // ---- results -------------------------------------------------------------
-      // With two score buffers the last scores do not imply that the products
-      // before them are done, and a parity wait cannot see two phases ahead.
-      if (kM == 1 && n_o > 1) ok = warp_wait(o_done + m, (n_o - 2) & 1, s_abort);
-      ok = ok && warp_wait(o_done + m, (n_o - 1) & 1, s_abort);
+      ok = warp_wait(o_done + m * 2 + ((unit - 1) & 1), ((unit - 1) >> 1) & 1, s_abort);
       if (!ok) break;
       tc::fence_after_sync();
       const uint32_t to = tmem + lane_base + C::c_o(m);
@@ -771,7 +748,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         if (*s_any_nan) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            const int first = s_nan[(seg & 3) * D + c + k];
+            const int first = s_nan[(seg % C::NR) * D + c + k];
             if (first != 0xffff && lim > nan_base + first) v[k] = NAN;
           }
         }
@@ -886,7 +863,7 @@ gdn_status_t launch_tile(const Args& a, cudaStream_t st) {
   const int64_t pages = (int64_t)a.num_blocks * a.Hk;
   CUtensorMap k_map, v_map;
   if (!cache_map(&k_map, a.kc, D, B, pages, TC<D>::row, std::min(B, kKeys)) ||
-      !cache_map(&v_map, a.vc, D, B, pages, TC<D>::row, std::min(B, kHalf))) {
+      !cache_map(&v_map, a.vc, D, B, pages, TC<D>::row, std::min(B, kKeys))) {
     set_cuda_error(cudaErrorInvalidValue);
     return GDN_ERR_CUDA;
   }
