@@ -260,7 +260,6 @@ gdn_status_t gdn_paged_attention(const void* q, int64_t q_stride, const void* k_
   a.num_blocks = num_blocks;
   a.max_blocks = max_blocks;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
-  a.hdr = reinterpret_cast<attn::Header*>(ws);
   a.items = reinterpret_cast<attn::Item*>(ws + l.items);
   a.counters = reinterpret_cast<int*>(ws + l.counters);
   a.partials = reinterpret_cast<float*>(ws + l.partials);
@@ -270,7 +269,6 @@ gdn_status_t gdn_paged_attention(const void* q, int64_t q_stride, const void* k_
   a.split_rows = l.split_rows;
   a.split_grid = attn::split_grid(d);
   a.tile_grid = attn::tile_grid();
-  a.tile_counters = reinterpret_cast<int*>(ws + l.tile_counters);
   a.tile_partials = reinterpret_cast<float*>(ws + l.tile_partials);
   // The two kernels share a step's sequences by their rows; a step whose
   // lengths rule one of them out launches the other alone. One sequence is

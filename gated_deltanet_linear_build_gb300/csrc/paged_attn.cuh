@@ -18,27 +18,20 @@ struct Item {
   int cum;       // units of the tiles before it
 };
 
-struct Header {
-  int num_items;         // row tiles of the split kernel
-  int units;             // their kv units, one head's
-  int per_cta;           // units per CTA, over all heads
-  int num_tiles;         // row tiles of the tensor-core kernel,
-  int tile_units;        // their kv units, one head's,
-  int tile_per_cta;      // units per CTA
-  int pad[58];
-};
-static_assert(sizeof(Header) == 256, "header is 256 bytes");
-
 constexpr int kUnit = 32;              // keys per unit of the split kernel
 constexpr int kTileKeys = 64;         // keys per unit of the tensor-core kernel
 
-// Where a CTA's piece of the work line begins.
-struct Start {
-  int item, head;
+// A CTA's piece [u, u_end) of the work line (units of all heads), with all that
+// its first segment needs: one 64-byte line instead of a chain of loads.
+struct alignas(64) Start {
+  int item, head, num_items, units;   // of unit u; of the list: tiles, one head's units
+  Item it;
+  int first, len, kv, per_cta;        // the item's sequence; units per CTA
+  long long u, u_end;
 };
 
 struct Layout {
-  size_t starts, tile_starts, items, counters, partials, tiles, tile_counters, tile_partials, total;
+  size_t starts, tile_starts, items, counters, partials, tiles, tile_partials, total;
   int item_cap, tile_cap, split_rows, tile_rows;
 };
 
@@ -72,14 +65,12 @@ struct Args {
   __nv_bfloat16* o;
   int N, T, Hq, Hk, d, log_b, num_blocks, max_blocks;
   float scale_log2;                    // softmax scale x log2 e
-  Header* hdr;
   Item* items;
-  int* counters;                       // [item][head]: partial results that have arrived
+  int* counters;                       // arrivals, see the split kernel
   float* partials;
   Item* tiles;
   int split_rows, split_grid, tile_grid;
   const Start *starts, *tile_starts;
-  int* tile_counters;                  // [tile][head][128-row half]
   float* tile_partials;
 };
 
@@ -96,6 +87,15 @@ __device__ __forceinline__ Seq seq_of(const int32_t* cu, const int32_t* kv, int 
   const int64_t k = __ldg(kv + n);
   s.kv = (int)(k < 0 ? 0 : k > kv_max ? kv_max : k);
   return s;
+}
+__device__ __forceinline__ Start read_start(const Start* at) {
+  union {
+    int4 v[4];
+    Start s;
+  } x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x.v[i] = reinterpret_cast<const int4*>(at)[i];
+  return x.s;
 }
 // Keys that row r of the sequence sees: [0, visible).
 __device__ __forceinline__ int visible(const Seq& s, int token) {

@@ -48,7 +48,7 @@ Layout layout(int T, int N, int Hq, int Hk, int d) {
   l.tile_rows = tile_rows(d);
   l.tile_cap = (int)std::min<int64_t>((int64_t)T * G / l.tile_rows + N, 0x7fffffff / 16);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  size_t at = sizeof(Header);
+  size_t at = 0;
   l.starts = at;
   at += kSplitGridMax * sizeof(Start);
   l.tile_starts = at;
@@ -56,11 +56,9 @@ Layout layout(int T, int N, int Hq, int Hk, int d) {
   l.items = at;
   at = up(at + (size_t)l.item_cap * sizeof(Item));
   l.counters = at;
-  at = up(at + (size_t)l.item_cap * Hk * sizeof(int));
+  at = up(at + ((size_t)l.item_cap * Hk + 2 * kSplitGridMax) * sizeof(int));
   l.tiles = at;
   at = up(at + (size_t)l.tile_cap * sizeof(Item));
-  l.tile_counters = at;
-  at = up(at + (size_t)l.tile_cap * Hk * 2 * sizeof(int));
   l.partials = at;
   at = up(at + (size_t)kSplitGridMax * 2 * (size_t)l.split_rows * (d + 2) * sizeof(float));
   l.tile_partials = at;
@@ -86,9 +84,8 @@ struct PlanArgs {
   int64_t kv_max;
   int rows, item_cap, grid;            // split kernel
   int tile_rows, tile_cap, tile_grid;  // tensor-core kernel
-  Header* hdr;
   Item *items, *tiles;
-  int *counters, *tile_counters;
+  int* counters;
   Start *starts, *tile_starts;
 };
 
@@ -119,9 +116,8 @@ __device__ __forceinline__ int block_scan(int v, int* sums, int& tot) {
 // Row tiles of `rows` rows, with units of `keys` keys, of the sequences with
 // more than `above` and at most `upto` rows.
 struct ListArgs {
-  int rows, keys, above, upto, cap, per_item;   // per_item: counters of a tile
+  int rows, keys, above, upto, cap;
   Item* items;
-  int* counters;
 };
 
 __device__ void build_list(const PlanArgs& p, const ListArgs& a, int* sums, int* s_first,
@@ -160,10 +156,7 @@ __device__ void build_list(const PlanArgs& p, const ListArgs& a, int* sums, int*
       int tot_units;
       const int cum = block_scan(it.units, sums, tot_units);
       it.cum = units + cum - it.units;
-      if (i < tot && items + i < a.cap) {
-        a.items[items + i] = it;
-        for (int h = 0; h < a.per_item; ++h) a.counters[(int64_t)(items + i) * a.per_item + h] = 0;
-      }
+      if (i < tot && items + i < a.cap) a.items[items + i] = it;
       units += tot_units;
     }
     items += tot;
@@ -172,27 +165,39 @@ __device__ void build_list(const PlanArgs& p, const ListArgs& a, int* sums, int*
   items = min(items, a.cap);
 }
 
-// Units per CTA, and where each CTA's piece of the line begins.
-__device__ int cut_line(const Item* items, int num, int units, int Hk, int grid, Start* starts) {
-  const int64_t all = (int64_t)units * Hk;
-  const int per_cta = (int)max((int64_t)1, (all + grid - 1) / grid);
+// Every CTA's piece of the line, of at least `least` units.
+__device__ void cut_line(const PlanArgs& p, const Item* items, int num, int units, int grid, int least,
+                         Start* starts) {
+  const int64_t all = (int64_t)units * p.Hk;
+  const int per_cta = (int)max((int64_t)least, (all + grid - 1) / grid);
   __syncthreads();                              // the list is written
   for (int c = threadIdx.x; c < grid; c += kPlanThreads) {
-    const int64_t u = (int64_t)c * per_cta;
-    Start at = {0, 0};
-    if (u < all) {
-      at.head = (int)(u / units);
-      const int x = (int)(u - (int64_t)at.head * units);
+    Start at;
+    at.u = min((long long)all, (long long)c * per_cta);
+    at.u_end = min((long long)all, at.u + per_cta);
+    at.item = at.head = 0;
+    at.num_items = num;
+    at.units = units;
+    at.per_cta = per_cta;
+    at.it = {0, 0, 0, 0};
+    at.first = at.len = at.kv = 0;
+    if (at.u < all) {
+      at.head = (int)(at.u / units);
+      const int x = (int)(at.u - (int64_t)at.head * units);
       int lo = 0, hi = num - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (items[mid].cum <= x) lo = mid; else hi = mid - 1;
       }
       at.item = lo;
+      at.it = items[lo];
+      const Seq s = seq_of(p.cu, p.kv, at.it.seq, p.T, p.kv_max);
+      at.first = s.first;
+      at.len = s.len;
+      at.kv = s.kv;
     }
     starts[c] = at;
   }
-  return per_cta;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs p) {
@@ -201,20 +206,13 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
   pdl_wait();
   pdl_trigger();
   int items, units, tiles, tile_units;
-  build_list(p, {p.rows, kUnit, 0, p.limit, p.item_cap, p.Hk, p.items, p.counters}, sums, s_first,
-             items, units);
-  build_list(p, {p.tile_rows, kTileKeys, p.limit, 0x7fffffff, p.tile_cap, 2 * p.Hk, p.tiles,
-                 p.tile_counters}, sums, s_first, tiles, tile_units);
-  const int per_cta = cut_line(p.items, items, units, p.Hk, p.grid, p.starts);
-  const int tile_per_cta = cut_line(p.tiles, tiles, tile_units, p.Hk, p.tile_grid, p.tile_starts);
-  if (threadIdx.x == 0) {
-    p.hdr->num_items = items;
-    p.hdr->units = units;
-    p.hdr->per_cta = per_cta;
-    p.hdr->num_tiles = tiles;
-    p.hdr->tile_units = tile_units;
-    p.hdr->tile_per_cta = tile_per_cta;
-  }
+  build_list(p, {p.rows, kUnit, 0, p.limit, p.item_cap, p.items}, sums, s_first, items, units);
+  build_list(p, {p.tile_rows, kTileKeys, p.limit, 0x7fffffff, p.tile_cap, p.tiles}, sums, s_first,
+             tiles, tile_units);
+  for (int i = threadIdx.x; i < items * p.Hk + 2 * kSplitGridMax; i += kPlanThreads) p.counters[i] = 0;
+  // A piece of the split kernel gives each of its warps a unit at least.
+  cut_line(p, p.items, items, units, p.grid, 8, p.starts);
+  cut_line(p, p.tiles, tiles, tile_units, p.tile_grid, 1, p.tile_starts);
 }
 
 // ---------------------------------------------------------------------------
@@ -262,6 +260,8 @@ __device__ __forceinline__ void cp_async4(void* dst, const void* src, uint32_t b
 // Split kernel
 // ---------------------------------------------------------------------------
 constexpr int kWarps = 8;
+constexpr int kJoin = 16;                // partial results joined by one CTA
+constexpr int kJoinMax = (kSplitGridMax + kJoin - 1) / kJoin > kJoin ? (kSplitGridMax + kJoin - 1) / kJoin : kJoin;
 
 template <int D, int QM>
 struct Cfg {
@@ -310,22 +310,19 @@ attn_split_kernel(const Args p) {
 
   pdl_wait();
   pdl_trigger();
-  const int num_items = p.hdr->num_items, units1 = p.hdr->units, per_cta = p.hdr->per_cta;
-  const long long total = (long long)units1 * p.Hk;
-  long long u = (long long)blockIdx.x * per_cta;
-  const long long u_end = min(total, u + per_cta);
-
-  const int2 at = *reinterpret_cast<const int2*>(p.starts + blockIdx.x);
-  int lo = at.x, head = at.y;
+  const Start start = read_start(p.starts + blockIdx.x);
+  const int num_items = start.num_items, units1 = start.units, per_cta = start.per_cta;
+  long long u = start.u;
+  const long long u_end = start.u_end;
+  int lo = start.item, head = start.head;
+  Item it = start.it;
+  Seq s = {start.first, start.len, start.kv};
 
   while (u < u_end) {
-    // ---- the item that holds unit u ------------------------------------------
     const int x = (int)(u - (long long)head * units1);
-    const int4 raw = __ldg(reinterpret_cast<const int4*>(p.items) + lo);
-    const int seq = raw.x, row0 = raw.y, n_units = raw.z, cum = raw.w;
+    const int seq = it.seq, row0 = it.row0, n_units = it.units, cum = it.cum;
     const int first_unit = x - cum;
     const int seg = (int)min((long long)(n_units - first_unit), u_end - u);
-    const Seq s = seq_of(p.cu, p.kv, seq, p.T, (int64_t)p.max_blocks << p.log_b);
     const int n_rows = min(C::rows, s.len * G - row0);
     const int key_end = visible(s, (row0 + n_rows - 1) / G);      // keys of the last row
     const int32_t* table = p.table + (int64_t)seq * p.table_stride;
@@ -733,40 +730,85 @@ attn_split_kernel(const Args p) {
       }
     }
     if (!whole) {
-      __threadfence();
-      __syncthreads();
-      // CTAs of this item: those of its first and last unit and all between.
+      // The item's CTAs are those of its first and last unit and all between, in
+      // groups of kJoin: the last of a group joins it in place of its first
+      // member's partial, the last group's joins the groups.
       const long long at0 = (long long)head * units1 + cum;
       const int c0 = (int)(at0 / per_cta), c1 = (int)((at0 + n_units - 1) / per_cta);
-      if (tid == 0) {
-        int* counter = p.counters + (size_t)lo * p.Hk + head;
-        const int seen = atomicAdd(counter, 1);
-        *s_flag = seen == c1 - c0;
-        if (seen == c1 - c0) *counter = 0;       // ready for the next call on this plan
-      }
-      __syncthreads();
-      if (*s_flag) {
-        __threadfence();
-#pragma unroll 1
-        for (int i = 0; i < n_el; ++i) {
-          const int at = i * kWarps * 32 + tid, r = at / D, dd = at % D;
-          float top = -INFINITY;
-          for (int c = c0; c <= c1; ++c)
-            top = fmaxf(top, __ldcg(p.partials + ((size_t)c * 2 + (c == c0)) * C::rows * (D + 2) + r * 2));
-          float l = 0.f, o = 0.f;
-          for (int c = c0; c <= c1; ++c) {
-            const float* q = p.partials + ((size_t)c * 2 + (c == c0)) * C::rows * (D + 2);
-            const float mc = __ldcg(q + r * 2);
-            const float f = mc == -INFINITY ? 1.f : ex2_approx(mc - top);
-            l += __ldcg(q + r * 2 + 1) * f;
-            o += __ldcg(q + 2 * C::rows + r * D + dd) * f;
+      const int grp = ((int)blockIdx.x - c0) / kJoin, groups = (c1 - c0) / kJoin + 1;
+      const int ga = c0 + grp * kJoin, gb = min(c1, ga + kJoin - 1);
+      const size_t psz = C::rows * (D + 2);
+      float* fs = reinterpret_cast<float*>(smem);             // factors, [n][rows]
+      float* s_l = fs + kJoinMax * C::rows;
+      auto slot = [&](int c) { return p.partials + ((size_t)c * 2 + (c == c0)) * psz; };
+      // Joins the partials of CTAs a, a + step, ... (n of them); `out` or the output.
+      auto join = [&](int a, int step, int n, float* out) {
+        for (int r = w; r < C::rows; r += kWarps) {
+          float top = -INFINITY, l = 0.f;
+          for (int c = lane; c < n; c += 32) top = fmaxf(top, __ldcg(slot(a + c * step) + r * 2));
+#pragma unroll
+          for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+          for (int c = lane; c < n; c += 32) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot(a + c * step)) + r);
+            // NaN sums pass on: a NaN row has m = -inf and its l as it is.
+            const float f = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - top);
+            fs[c * C::rows + r] = f;
+            l += ml.y * f;
           }
-          if (r < n_rows) {
-            const int row = row0 + r;
-            p.o[((int64_t)(s.first + row / G) * p.Hq + head * G + row % G) * D + dd] =
-                __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+#pragma unroll
+          for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+          if (lane == 0) {
+            s_l[r * 2] = top;
+            s_l[r * 2 + 1] = l;
           }
         }
+        __syncthreads();
+#pragma unroll 1
+        for (int e = tid * 4; e < C::rows * D; e += kWarps * 32 * 4) {
+          const int r = e / D, dd = e % D;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int c = 0; c < n; ++c) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(slot(a + c * step) + 2 * C::rows + e));
+            const float f = fs[c * C::rows + r];
+            o.x = fmaf(v.x, f, o.x);
+            o.y = fmaf(v.y, f, o.y);
+            o.z = fmaf(v.z, f, o.z);
+            o.w = fmaf(v.w, f, o.w);
+          }
+          if (out) {
+            __stcg(reinterpret_cast<float4*>(out + 2 * C::rows + e), o);
+          } else if (r < n_rows) {
+            const int row = row0 + r;
+            const float l = s_l[r * 2 + 1], il = l == 0.f ? 0.f : 1.f / l;
+            uint2 b;
+            b.x = pack_bf16x2(o.x * il, o.y * il);
+            b.y = pack_bf16x2(o.z * il, o.w * il);
+            *reinterpret_cast<uint2*>(p.o + ((int64_t)(s.first + row / G) * p.Hq + head * G + row % G) * D + dd) = b;
+          }
+        }
+        if (out && tid < C::rows)
+          __stcg(reinterpret_cast<float2*>(out) + tid, make_float2(s_l[tid * 2], s_l[tid * 2 + 1]));
+      };
+      // One more arrival of `of` at the counter; true for the whole CTA at the last.
+      auto last = [&](int* counter, int of) {
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+          const int seen = atomicAdd(counter, 1);
+          s_flag[0] = seen == of - 1;
+          if (seen == of - 1) *counter = 0;        // ready for the next call on this plan
+        }
+        __syncthreads();
+        if (s_flag[0]) __threadfence();
+        return s_flag[0] != 0;
+      };
+      int* item_counter = p.counters + 2 * kSplitGridMax + (size_t)lo * p.Hk + head;
+      if (groups == 1) {
+        if (last(item_counter, gb - ga + 1)) join(ga, 1, gb - ga + 1, nullptr);
+      } else if (last(p.counters + ga * 2 + (ga == c0), gb - ga + 1)) {
+        join(ga, 1, gb - ga + 1, slot(ga));
+        if (last(item_counter, groups)) join(c0, kJoin, groups, nullptr);
       }
     }
     __syncthreads();                     // the ring, Q and s_ml are free again
@@ -774,6 +816,11 @@ attn_split_kernel(const Args p) {
     if (first_unit + seg == n_units && ++lo == num_items) {
       lo = 0;
       ++head;
+    }
+    if (u < u_end) {
+      const int4 raw = __ldg(reinterpret_cast<const int4*>(p.items) + lo);
+      it = {raw.x, raw.y, raw.z, raw.w};
+      s = seq_of(p.cu, p.kv, it.seq, p.T, (int64_t)p.max_blocks << p.log_b);
     }
   }
 }
@@ -804,7 +851,6 @@ gdn_status_t launch_attn_plan(const int32_t* cu, const int32_t* kv, int N, int T
   p.item_cap = l.item_cap;
   p.grid = split_grid(d);
   p.kv_max = kv_max;
-  p.hdr = reinterpret_cast<Header*>(ws);
   p.items = reinterpret_cast<Item*>(ws + l.items);
   p.counters = reinterpret_cast<int*>(ws + l.counters);
   p.limit = split_limit(p.G);
@@ -812,7 +858,6 @@ gdn_status_t launch_attn_plan(const int32_t* cu, const int32_t* kv, int N, int T
   p.tile_cap = l.tile_cap;
   p.tile_grid = tile_grid();
   p.tiles = reinterpret_cast<Item*>(ws + l.tiles);
-  p.tile_counters = reinterpret_cast<int*>(ws + l.tile_counters);
   p.starts = reinterpret_cast<Start*>(ws + l.starts);
   p.tile_starts = reinterpret_cast<Start*>(ws + l.tile_starts);
   return check_launch(launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p));

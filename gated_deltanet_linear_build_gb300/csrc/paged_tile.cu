@@ -23,8 +23,7 @@
 //
 // Work split: as in the split kernel, all (tile, kv head, 64 keys) units form
 // one line cut into equal pieces, one per SM; a tile cut by the end of a piece
-// leaves float32 partial results, joined in a fixed order by the warps that
-// arrive last.
+// leaves float32 partial results, which a second kernel joins in CTA order.
 //
 // Roles (four warpgroups): 0 .. kM - 1: softmax of one 128-row tile each; the
 // others up to 2: Q, widening of V; warp 12: MMAs; warp 13: TMA copies of K, and
@@ -80,11 +79,11 @@ struct TC {
   // Exponents of the rows' scales, int8 [2 segments][rows].
   static constexpr int o_ex = o_nan + NR * D * 2;
   static constexpr int o_bar = o_ex + 2 * M * 128;
-  static constexpr int n_bar = 2 * KS + 2 * VR + 2 * VS + 8 + 4 + 4 + 4 + 2 + 2 + 2;
+  static constexpr int n_bar = 2 * KS + 2 * VR + 2 * VS + 8 + 4 + 4 + 4 + 2 + 2;
   static constexpr int o_misc = o_bar + n_bar * 8;      // tmem base, abort, flags
   static constexpr int total = o_misc + 32;
   static_assert(total <= 232448, "shared memory of one CTA");
-  static constexpr int regs = 152, mma_regs = 56;
+  static constexpr int regs = 144, mma_regs = 80;
   static_assert(3 * regs + mma_regs <= 4 * kLaunchRegs, "registers of the launch");
   // Tensor-memory columns: two score buffers of 64 keys per tile, then O.
   static constexpr int c_s(int m, int b) { return m * 128 + b * 64; }
@@ -196,48 +195,55 @@ struct Seg {
   int n_rows, key_end;
 };
 
-// This CTA's piece of the work line; lo and head are those of its next unit.
+// This CTA's piece of the work line; lo, head, it and s are those of its next unit.
 struct Line {
-  int num, units1, per_cta, lo, head;
+  int num, units1, lo, head;
+  Item it;
+  Seq s;
   long long u, u_end;
   __device__ bool more() const { return u < u_end; }
-  __device__ void pass(const Seg& g) {
-    u += g.count;
-    if (g.first_unit + g.count == g.n_units && ++lo == num) {
-      lo = 0;
-      ++head;
-    }
-  }
 };
 
 __device__ __forceinline__ Line line_of(const Args& p) {
+  const Start at = read_start(p.tile_starts + blockIdx.x);
   Line l;
-  l.num = p.hdr->num_tiles;
-  l.units1 = p.hdr->tile_units;
-  l.per_cta = p.hdr->tile_per_cta;
-  const long long total = (long long)l.units1 * p.Hk;
-  l.u = (long long)blockIdx.x * l.per_cta;
-  l.u_end = min(total, l.u + l.per_cta);
-  const int2 at = *reinterpret_cast<const int2*>(p.tile_starts + blockIdx.x);
-  l.lo = at.x;
-  l.head = at.y;
+  l.num = at.num_items;
+  l.units1 = at.units;
+  l.lo = at.item;
+  l.head = at.head;
+  l.it = at.it;
+  l.s = {at.first, at.len, at.kv};
+  l.u = at.u;
+  l.u_end = at.u_end;
   return l;
 }
 
 __device__ __forceinline__ Seg seg_at(const Args& p, const Line& l, int tile_rows) {
   Seg g;
-  const int4 raw = __ldg(reinterpret_cast<const int4*>(p.tiles) + l.lo);
-  g.seq = raw.x;
-  g.row0 = raw.y;
-  g.n_units = raw.z;
-  g.cum = raw.w;
+  g.seq = l.it.seq;
+  g.row0 = l.it.row0;
+  g.n_units = l.it.units;
+  g.cum = l.it.cum;
   g.first_unit = (int)(l.u - (long long)l.head * l.units1) - g.cum;
   g.count = (int)min((long long)(g.n_units - g.first_unit), l.u_end - l.u);
-  g.s = seq_of(p.cu, p.kv, g.seq, p.T, (int64_t)p.max_blocks << p.log_b);
+  g.s = l.s;
   const int G = p.Hq / p.Hk;
   g.n_rows = min(tile_rows, g.s.len * G - g.row0);
   g.key_end = visible(g.s, (g.row0 + g.n_rows - 1) / G);
   return g;
+}
+
+__device__ __forceinline__ void pass(const Args& p, Line& l, const Seg& g) {
+  l.u += g.count;
+  if (g.first_unit + g.count == g.n_units && ++l.lo == l.num) {
+    l.lo = 0;
+    ++l.head;
+  }
+  if (l.more()) {
+    const int4 raw = __ldg(reinterpret_cast<const int4*>(p.tiles) + l.lo);
+    l.it = {raw.x, raw.y, raw.z, raw.w};
+    l.s = seq_of(p.cu, p.kv, l.it.seq, p.T, (int64_t)p.max_blocks << p.log_b);
+  }
 }
 
 template <int D>
@@ -262,12 +268,10 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
   // more than one phase away from what it waits for.
   uint64_t* o_done = p_full + 4;
   uint64_t* q_full = o_done + 4;
-  uint64_t* wg_sync = q_full + 2;            // [kM] a softmax warpgroup among itself
-  uint64_t* nan_sync = wg_sync + 2;          // the widening threads among themselves
+  uint64_t* nan_sync = q_full + 2;           // the widening threads among themselves
   uint64_t* drained = nan_sync + 1;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::o_misc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::o_misc + 4);
-  int* s_flag = reinterpret_cast<int*>(smem + C::o_misc + 8);     // [2] this warpgroup joins
   volatile int* s_any_nan = reinterpret_cast<volatile int*>(smem + C::o_misc + 16);
   float* s_sc = reinterpret_cast<float*>(smem + C::o_sc);
   signed char* s_ex = reinterpret_cast<signed char*>(smem + C::o_ex);
@@ -294,7 +298,6 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       tc::mbar_init(p_full + i, 128);
       tc::mbar_init(o_done + i, 1);
     }
-    for (int i = 0; i < 2; ++i) tc::mbar_init(wg_sync + i, 128);
     for (int i = 0; i < 2; ++i) tc::mbar_init(q_full + i, C::loaders);
     tc::mbar_init(nan_sync, C::loaders);
     tc::mbar_init(drained, 1);
@@ -378,7 +381,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
           }
         }
         ++segs;
-        l.pass(g);
+        pass(p, l, g);
       }
       // Nothing of this CTA's tensor work is in flight when TMEM is freed.
       if (one) tc::mma_commit(drained);
@@ -451,7 +454,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
             ++round;
           }
         }
-        l.pass(g);
+        pass(p, l, g);
       }
       // The copies in flight land before the CTA may end: a giving-up reader
       // would not have waited for them.
@@ -616,7 +619,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         tc::fence_smem_to_async();
         tc::mbar_arrive(v_full + st);
       }
-      l.pass(g);
+      pass(p, l, g);
       ++seg;
     }
   } else {
@@ -624,12 +627,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
     regs_up<C::regs>();
     const int m = wg, r = tid & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    int unit = 0, seg = 0, n_sync = 0;
-    // All 128 threads of the warpgroup, or false when the CTA gave up.
-    auto wg_barrier = [&]() {
-      tc::mbar_arrive(wg_sync + m);
-      return warp_wait(wg_sync + m, n_sync++ & 1, s_abort);
-    };
+    int unit = 0, seg = 0;
     bool ok = true;
     while (ok && l.more()) {
       const Seg g = seg_at(p, l, kRows);
@@ -738,8 +736,8 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       __nv_bfloat16* out = p.o + ((int64_t)(g.s.first + tok) * p.Hq + hq) * D;
       const float il = l_run == 0.f ? 0.f : 1.f / l_run;
       const size_t part_sz = (size_t)(D + 2) * 128;
-      float* parts = p.tile_partials + (size_t)m * part_sz;
-      float* part = parts + ((size_t)blockIdx.x * 2 + (g.first_unit == 0 ? 1 : 0)) * kM * part_sz;
+      float* part = p.tile_partials +
+                    (((size_t)blockIdx.x * 2 + (g.first_unit == 0 ? 1 : 0)) * kM + m) * part_sz;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float v[32];
@@ -767,56 +765,9 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       if (!whole) {
         __stcg(part + r, m_run);
         __stcg(part + 128 + r, l_run);
-        __threadfence();
-        ok = wg_barrier();
-        if (!ok) break;
-        const long long at0 = (long long)l.head * l.units1 + g.cum;
-        const int c0 = (int)(at0 / l.per_cta), c1 = (int)((at0 + g.n_units - 1) / l.per_cta);
-        if (r == 0) {
-          int* counter = p.tile_counters + ((size_t)l.lo * p.Hk + l.head) * kM + m;
-          const int seen = atomicAdd(counter, 1);
-          s_flag[m] = seen == c1 - c0;
-          if (seen == c1 - c0) *counter = 0;           // ready for the next call on this plan
-        }
-        ok = wg_barrier();
-        if (!ok) break;
-        if (s_flag[m]) {
-          __threadfence();
-          float top = -INFINITY;
-          for (int c = c0; c <= c1; ++c)
-            top = fmaxf(top, __ldcg(parts + ((size_t)c * 2 + (c == c0)) * kM * part_sz + r));
-          float lt = 0.f;
-          for (int c = c0; c <= c1; ++c) {
-            const float* q = parts + ((size_t)c * 2 + (c == c0)) * kM * part_sz;
-            const float mc = __ldcg(q + r);
-            lt += __ldcg(q + 128 + r) * (mc == -INFINITY ? 1.f : ex2_approx(mc - top));
-          }
-          const float it = lt == 0.f ? 0.f : 1.f / lt;
-#pragma unroll 1
-          for (int cb = 0; cb < D; cb += 32) {
-            float v[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = 0.f;
-            for (int c = c0; c <= c1; ++c) {
-              const float* q = parts + ((size_t)c * 2 + (c == c0)) * kM * part_sz;
-              const float mc = __ldcg(q + r);
-              const float f = mc == -INFINITY ? 1.f : ex2_approx(mc - top);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = fmaf(__ldcg(q + (size_t)(2 + cb + k) * 128 + r), f, v[k]);
-            }
-            if (live) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] *= it;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(out + cb + 8 * k) = pack8(v + 8 * k);
-            }
-          }
-        }
-        ok = wg_barrier();                             // s_flag is free again
-        if (!ok) break;
       }
       tc::fence_before_sync();
-      l.pass(g);
+      pass(p, l, g);
       ++seg;
     }
   }
@@ -825,6 +776,54 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
   __syncthreads();
   tc::fence_after_sync();
   if (warp == 12) tc::tmem_dealloc(tmem, 512);
+}
+
+// Joins the partial results of tiles that were cut. Tile (c0, ...) of the grid:
+// the item that begins in CTA c0's piece and goes on past its end, 32 of its
+// rows; warp w takes an eighth of the columns, lane i row i (the layout
+// [column][128 rows] of the partials keeps its loads whole).
+template <int D>
+__global__ void __launch_bounds__(256) attn_tile_join_kernel(const Args p) {
+  constexpr int kM = TC<D>::M, kCols = D / 8;
+  pdl_wait();
+  pdl_trigger();
+  const int c0 = blockIdx.x, m = blockIdx.y >> 2, r = (blockIdx.y & 3) * 32 + (threadIdx.x & 31);
+  const int col0 = (threadIdx.x >> 5) * kCols;
+  if (c0 + 1 >= (int)gridDim.x) return;
+  const Start next = read_start(p.tile_starts + c0 + 1);
+  if (next.u >= next.u_end) return;
+  const long long at0 = (long long)next.head * next.units + next.it.cum;
+  if (at0 == next.u || at0 / next.per_cta != c0) return;    // not cut here, or begun earlier
+  const int c1 = (int)((at0 + next.it.units - 1) / next.per_cta);
+  const int G = p.Hq / p.Hk;
+  const int row = next.it.row0 + m * 128 + r, tok = row / G;
+  if (row >= next.len * G) return;
+  constexpr size_t part_sz = (size_t)(D + 2) * 128;
+  auto part = [&](int c) {
+    return p.tile_partials + (((size_t)c * 2 + (c == c0)) * kM + m) * part_sz;
+  };
+  float top = -INFINITY;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(part(c) + r));
+  float l = 0.f, v[kCols];
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) v[k] = 0.f;
+#pragma unroll 2
+  for (int c = c0; c <= c1; ++c) {
+    const float* q = part(c);
+    const float mc = __ldcg(q + r);
+    // NaN sums pass on: a NaN row has m = -inf and its l as it is.
+    const float f = mc == -INFINITY ? 1.f : ex2_approx(mc - top);
+    l += __ldcg(q + 128 + r) * f;
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) v[k] = fmaf(__ldcg(q + (size_t)(2 + col0 + k) * 128 + r), f, v[k]);
+  }
+  const float il = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) v[k] *= il;
+  __nv_bfloat16* out = p.o + ((int64_t)(next.first + tok) * p.Hq + next.head * G + row - tok * G) * D + col0;
+#pragma unroll
+  for (int k = 0; k < kCols; k += 8) *reinterpret_cast<uint4*>(out + k) = pack8(v + k);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -867,8 +866,11 @@ gdn_status_t launch_tile(const Args& a, cudaStream_t st) {
     set_cuda_error(cudaErrorInvalidValue);
     return GDN_ERR_CUDA;
   }
-  return check_launch(launch_pdl(attn_tile_kernel<D>, dim3(a.tile_grid), dim3(kThreads),
-                                 TC<D>::total, st, a, k_map, v_map));
+  const gdn_status_t rc = check_launch(launch_pdl(attn_tile_kernel<D>, dim3(a.tile_grid),
+                                                  dim3(kThreads), TC<D>::total, st, a, k_map, v_map));
+  if (rc != GDN_OK) return rc;
+  return check_launch(launch_pdl(attn_tile_join_kernel<D>, dim3(a.tile_grid, TC<D>::M * 4),
+                                 dim3(256), 0, st, a));
 }
 
 }  // namespace
