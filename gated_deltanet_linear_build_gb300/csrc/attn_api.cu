@@ -204,7 +204,7 @@ gdn_status_t gdn_paged_attention_plan(const int32_t* cu_seqlens, const int32_t* 
                                      &nothing);
   if (rc != GDN_OK || nothing) return rc;
   return launch_attn_plan(cu_seqlens, kv_lens, N, T, Hq, Hk, d,
-                          (int64_t)max_blocks * block_tokens, workspace,
+                          (int64_t)max_blocks * block_tokens, max_new_tokens, workspace,
                           static_cast<cudaStream_t>(stream));
 }
 
@@ -234,7 +234,7 @@ gdn_status_t gdn_paged_attention(const void* q, int64_t q_stride, const void* k_
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if ((flags & GDN_FLAG_PLANNED) == 0) {
     rc = launch_attn_plan(cu_seqlens, kv_lens, N, T, Hq, Hk, d,
-                          (int64_t)max_blocks * block_tokens, workspace, st);
+                          (int64_t)max_blocks * block_tokens, max_new_tokens, workspace, st);
     if (rc != GDN_OK) return rc;
   }
   const attn::Layout l = attn::layout(T, N, Hq, Hk, d);
@@ -271,12 +271,10 @@ gdn_status_t gdn_paged_attention(const void* q, int64_t q_stride, const void* k_
   a.tile_grid = attn::tile_grid();
   a.tile_partials = reinterpret_cast<float*>(ws + l.tile_partials);
   // The two kernels share a step's sequences by their rows; a step whose
-  // lengths rule one of them out launches the other alone. One sequence is
-  // exactly as long as the step.
-  const int64_t G = Hq / Hk, limit = attn::split_limit((int)G);
-  const int64_t longest = N == 1 ? T : max_new_tokens;
-  if (!(N == 1 && T * G > limit)) rc = launch_attn_split(a, st);
-  if (rc == GDN_OK && longest * G > limit) rc = launch_attn_tile(a, st);
+  // lengths rule one of them out launches the other alone.
+  const attn::Kernels use = attn::kernels_of(N, T, Hq / Hk, max_new_tokens);
+  if (use.split) rc = launch_attn_split(a, st);
+  if (rc == GDN_OK && use.tile) rc = launch_attn_tile(a, st);
   return rc;
 }
 

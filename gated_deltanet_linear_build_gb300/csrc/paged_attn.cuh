@@ -2,6 +2,8 @@
 // the step's lengths and the others read, and its layout in the workspace.
 #pragma once
 
+#include <cuda.h>
+
 #include "gdn_internal.cuh"
 
 namespace gdn {
@@ -42,6 +44,16 @@ inline int tile_grid() { return num_sms() < 160 ? num_sms() : 160; }
 // Sequences of at most this many rows (new tokens x G) go to the split kernel.
 inline int split_limit(int G) { return 64; }
 
+// Which kernels a step's lengths leave work for. One sequence is exactly as
+// long as the step.
+struct Kernels {
+  bool split, tile;
+};
+inline Kernels kernels_of(int N, int T, int G, int max_new_tokens) {
+  const int64_t longest = N == 1 ? T : max_new_tokens, limit = split_limit(G);
+  return {!(N == 1 && longest * G > limit), longest * G > limit};
+}
+
 // Rows of a split tile: 16 where the query heads of a token need more than 8.
 inline int split_rows(int G) { return G > 8 ? 16 : 8; }
 
@@ -53,6 +65,33 @@ inline int split_grid(int d) {
 }
 
 Layout layout(int T, int N, int Hq, int Hk, int d);
+
+// Bytes of a cache row in one TMA box: the widest swizzle.
+__host__ __device__ constexpr int box_row(int d) { return d == 64 ? 64 : 128; }
+// The cache as (d, token of the block, block x head), boxes of `rows` tokens.
+bool cache_map(CUtensorMap* map, const void* cache, int d, int B, int64_t pages, int rows);
+
+// TMA box: rows of one (block, head) to shared memory.
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                        uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];"
+      :: "r"(tc::smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+// K-major operand of 128-byte (64-byte) swizzled rows: 8-row groups 8 rows apart.
+template <int kRow>
+__device__ __forceinline__ uint64_t desc_swizzled(uint32_t addr) {
+  return tc::smem_desc(addr, 16, 8 * kRow) | ((uint64_t)(kRow == 128 ? 2 : 4) << 61);
+}
+// Byte of chunk c of row r under that swizzle.
+template <int kRow>
+__device__ __forceinline__ int swizzled(int r, int c) {
+  if constexpr (kRow == 128) return r * 128 + ((c ^ (r & 7)) << 4);
+  return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
 
 struct Args {
   const __nv_bfloat16* q;
@@ -105,7 +144,8 @@ __device__ __forceinline__ int visible(const Seq& s, int token) {
 }  // namespace attn
 
 gdn_status_t launch_attn_plan(const int32_t* cu, const int32_t* kv, int N, int T, int Hq, int Hk,
-                              int d, int64_t kv_max, void* workspace, cudaStream_t st);
+                              int d, int64_t kv_max, int max_new_tokens, void* workspace,
+                              cudaStream_t st);
 gdn_status_t launch_attn_split(const attn::Args& a, cudaStream_t st);
 gdn_status_t launch_attn_tile(const attn::Args& a, cudaStream_t st);
 

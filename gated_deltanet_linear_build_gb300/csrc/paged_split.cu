@@ -7,7 +7,7 @@
 //
 // * One unit = 32 keys. A warp owns whole units (running maximum, sum and
 //   output of its own; no block barrier in the loop) and streams them through
-//   a private ring of cp.async slots, K and V alternating.
+//   a private ring of TMA slots, K and V alternating.
 // * S = Q K^T on e4m3 MMAs (m16n8k32): K goes to the tensor core as it lies in
 //   the cache. Q is split into two e4m3 parts, hi + lo, which together hold
 //   BF16's 8 significand bits; hi is rows 0-7 of the A tile and lo rows 8-15,
@@ -74,104 +74,122 @@ using namespace attn;
 
 // ---------------------------------------------------------------------------
 // Plan: the row tiles of the step, in sequence order, with the running sum of
-// their kv units. One CTA; a few thousand tiles at most.
+// their kv units, and the pieces that the line of units is cut into. One CTA:
+// latency bounds it (two rounds of dependent loads and a scan each), so a list
+// that fits (up to 1,024 tiles, every decode step) stays in shared memory.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 
+struct ListArgs {
+  int rows, keys, above, upto, cap, grid, least;   // tiles of the sequences with above < rows <= upto
+  Item* items;
+  Start* starts;
+};
 struct PlanArgs {
   const int32_t *cu, *kv;
-  int N, T, G, Hk, limit;
+  int N, T, G, Hk;
   int64_t kv_max;
-  int rows, item_cap, grid;            // split kernel
-  int tile_rows, tile_cap, tile_grid;  // tensor-core kernel
-  Item *items, *tiles;
+  ListArgs list[2];                    // split kernel, tensor-core kernel
   int* counters;
-  Start *starts, *tile_starts;
 };
 
-__device__ __forceinline__ int block_scan(int v, int* sums, int& tot) {
+// Inclusive scan of a pair over the block; the total in tot.
+__device__ __forceinline__ int2 block_scan(int2 v, int2* sums, int2& tot) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int a = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += a;
+    const int a = __shfl_up_sync(0xffffffffu, v.x, d), b = __shfl_up_sync(0xffffffffu, v.y, d);
+    if (lane >= d) { v.x += a; v.y += b; }
   }
-  __syncthreads();
+  __syncthreads();                     // earlier readers of sums are done
   if (lane == 31) sums[w] = v;
   __syncthreads();
-  if (w == 0) {
-    int s = sums[lane];
+  int2 s = sums[lane];                 // every warp scans the warps' sums itself
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, s, d);
-      if (lane >= d) s += a;
-    }
-    sums[lane] = s;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, s.x, d), b = __shfl_up_sync(0xffffffffu, s.y, d);
+    if (lane >= d) { s.x += a; s.y += b; }
   }
-  __syncthreads();
-  tot = sums[31];
-  return v + (w > 0 ? sums[w - 1] : 0);
+  tot.x = __shfl_sync(0xffffffffu, s.x, 31);
+  tot.y = __shfl_sync(0xffffffffu, s.y, 31);
+  const int bx = __shfl_sync(0xffffffffu, s.x, (w + 31) & 31), by = __shfl_sync(0xffffffffu, s.y, (w + 31) & 31);
+  if (w > 0) { v.x += bx; v.y += by; }
+  return v;
 }
 
-// Row tiles of `rows` rows, with units of `keys` keys, of the sequences with
-// more than `above` and at most `upto` rows.
-struct ListArgs {
-  int rows, keys, above, upto, cap;
-  Item* items;
-};
+__device__ __forceinline__ Item item_of(const PlanArgs& p, const ListArgs& a, const Seq& s, int seq,
+                                        int tile) {
+  Item it = {seq, tile * a.rows, 0, 0};
+  const int last = min(s.len - 1, (it.row0 + a.rows - 1) / p.G);
+  // An item without keys still has one unit, which writes its zeros.
+  it.units = max(1, (visible(s, last) + a.keys - 1) / a.keys);
+  return it;
+}
 
-__device__ void build_list(const PlanArgs& p, const ListArgs& a, int* sums, int* s_first,
-                           int& items, int& units) {
+__device__ void build_list(const PlanArgs& p, const ListArgs& a, int2* sums, int* s_first,
+                           int* s_cum, int& items, int& units) {
   const int tid = threadIdx.x;
   items = units = 0;
   for (int n0 = 0; n0 < p.N; n0 += kPlanThreads) {
-    // Tiles of this thread's sequence, then one thread per tile.
     int tiles = 0;
+    Seq s = {0, 0, 0};
     if (n0 + tid < p.N) {
-      const Seq s = seq_of(p.cu, p.kv, n0 + tid, p.T, p.kv_max);
+      s = seq_of(p.cu, p.kv, n0 + tid, p.T, p.kv_max);
       const int64_t r = (int64_t)s.len * p.G;
       if (r > a.above && r <= a.upto) tiles = (int)((r + a.rows - 1) / a.rows);
     }
-    int tot;
-    const int inc = block_scan(tiles, sums, tot);
-    s_first[tid] = inc - tiles;
+    if (!__syncthreads_or(tiles > 1)) {
+      // One tile a sequence: one scan gives its place and its units.
+      Item it = {0, 0, 0, 0};
+      if (tiles) it = item_of(p, a, s, n0 + tid, 0);
+      int2 tot;
+      const int2 inc = block_scan(make_int2(tiles, it.units), sums, tot);
+      it.cum = units + inc.y - it.units;
+      const int at = items + inc.x - 1;
+      if (tiles && at < a.cap) {
+        a.items[at] = it;
+        if (at < kPlanThreads) s_cum[at] = it.cum;
+      }
+      items += tot.x;
+      units += tot.y;
+      continue;
+    }
+    int2 tot;
+    const int2 inc = block_scan(make_int2(tiles, 0), sums, tot);
+    s_first[tid] = inc.x - tiles;
     __syncthreads();
-    for (int i0 = 0; i0 < tot; i0 += kPlanThreads) {
+    for (int i0 = 0; i0 < tot.x; i0 += kPlanThreads) {
       const int i = i0 + tid;
       Item it = {0, 0, 0, 0};
-      if (i < tot) {
-        int lo = 0, hi = kPlanThreads - 1;    // last sequence whose first tile is <= i
+      if (i < tot.x && items + i < a.cap) {    // beyond: malformed offsets only
+        int lo = 0, hi = kPlanThreads - 1;     // last sequence whose first tile is <= i
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
           if (s_first[mid] <= i) lo = mid; else hi = mid - 1;
         }
-        it.seq = n0 + lo;
-        it.row0 = (i - s_first[lo]) * a.rows;
-        const Seq s = seq_of(p.cu, p.kv, it.seq, p.T, p.kv_max);
-        const int last = min(s.len - 1, (it.row0 + a.rows - 1) / p.G);
-        // An item without keys still has one unit, which writes its zeros.
-        it.units = max(1, (visible(s, last) + a.keys - 1) / a.keys);
-        if (items + i >= a.cap) it.units = 0;      // malformed offsets only
+        it = item_of(p, a, seq_of(p.cu, p.kv, n0 + lo, p.T, p.kv_max), n0 + lo, i - s_first[lo]);
       }
-      int tot_units;
-      const int cum = block_scan(it.units, sums, tot_units);
-      it.cum = units + cum - it.units;
-      if (i < tot && items + i < a.cap) a.items[items + i] = it;
-      units += tot_units;
+      int2 tot_units;
+      const int2 cum = block_scan(make_int2(0, it.units), sums, tot_units);
+      it.cum = units + cum.y - it.units;
+      if (i < tot.x && items + i < a.cap) {
+        a.items[items + i] = it;
+        if (items + i < kPlanThreads) s_cum[items + i] = it.cum;
+      }
+      units += tot_units.y;
     }
-    items += tot;
-    __syncthreads();
+    items += tot.x;
+    __syncthreads();                           // s_first is free again
   }
   items = min(items, a.cap);
 }
 
 // Every CTA's piece of the line, of at least `least` units.
-__device__ void cut_line(const PlanArgs& p, const Item* items, int num, int units, int grid, int least,
-                         Start* starts) {
+__device__ void cut_line(const PlanArgs& p, const ListArgs& a, const int* s_cum, int num, int units) {
   const int64_t all = (int64_t)units * p.Hk;
-  const int per_cta = (int)max((int64_t)least, (all + grid - 1) / grid);
+  const int per_cta = (int)max((int64_t)a.least, (all + a.grid - 1) / a.grid);
   __syncthreads();                              // the list is written
-  for (int c = threadIdx.x; c < grid; c += kPlanThreads) {
+  for (int c = threadIdx.x; c < a.grid; c += kPlanThreads) {
     Start at;
     at.u = min((long long)all, (long long)c * per_cta);
     at.u_end = min((long long)all, at.u + per_cta);
@@ -182,37 +200,40 @@ __device__ void cut_line(const PlanArgs& p, const Item* items, int num, int unit
     at.it = {0, 0, 0, 0};
     at.first = at.len = at.kv = 0;
     if (at.u < all) {
-      at.head = (int)(at.u / units);
+      at.head = (int)((unsigned long long)at.u / (unsigned)units);
       const int x = (int)(at.u - (int64_t)at.head * units);
       int lo = 0, hi = num - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (items[mid].cum <= x) lo = mid; else hi = mid - 1;
+        if ((num <= kPlanThreads ? s_cum[mid] : a.items[mid].cum) <= x) lo = mid; else hi = mid - 1;
       }
       at.item = lo;
-      at.it = items[lo];
+      at.it = a.items[lo];
       const Seq s = seq_of(p.cu, p.kv, at.it.seq, p.T, p.kv_max);
       at.first = s.first;
       at.len = s.len;
       at.kv = s.kv;
     }
-    starts[c] = at;
+    a.starts[c] = at;
   }
 }
 
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs p) {
-  __shared__ int sums[32];
-  __shared__ int s_first[kPlanThreads];
+  __shared__ int2 sums[32];
+  __shared__ int s_first[kPlanThreads], s_cum[kPlanThreads];
   pdl_wait();
   pdl_trigger();
-  int items, units, tiles, tile_units;
-  build_list(p, {p.rows, kUnit, 0, p.limit, p.item_cap, p.items}, sums, s_first, items, units);
-  build_list(p, {p.tile_rows, kTileKeys, p.limit, 0x7fffffff, p.tile_cap, p.tiles}, sums, s_first,
-             tiles, tile_units);
-  for (int i = threadIdx.x; i < items * p.Hk + 2 * kSplitGridMax; i += kPlanThreads) p.counters[i] = 0;
-  // A piece of the split kernel gives each of its warps a unit at least.
-  cut_line(p, p.items, items, units, p.grid, 8, p.starts);
-  cut_line(p, p.tiles, tiles, tile_units, p.tile_grid, 1, p.tile_starts);
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    const ListArgs& a = p.list[k];
+    if (a.grid == 0) continue;                  // that kernel has no sequence in this step
+    int items, units;
+    build_list(p, a, sums, s_first, s_cum, items, units);
+    if (k == 0)
+      for (int i = threadIdx.x; i < items * p.Hk + 2 * kSplitGridMax; i += kPlanThreads) p.counters[i] = 0;
+    cut_line(p, a, s_cum, items, units);
+    __syncthreads();                            // s_cum is free again
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -251,11 +272,6 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void cp_async4(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
-               :: "r"(tc::smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
-}
-
 // ---------------------------------------------------------------------------
 // Split kernel
 // ---------------------------------------------------------------------------
@@ -266,48 +282,73 @@ constexpr int kJoinMax = (kSplitGridMax + kJoin - 1) / kJoin > kJoin ? (kSplitGr
 template <int D, int QM>
 struct Cfg {
   static constexpr int rows = 8 * QM;
-  static constexpr int slots = 3;                      // half units in a warp's ring
+  static constexpr int slots = 3;                      // half units (K or V) in a warp's ring
   static constexpr int slot_bytes = kUnit * D;
-  static constexpr int chunks = D / 16;                // 16-byte chunks of a cache row
+  static constexpr int row = box_row(D), boxes = D / row;
   static constexpr int ring = kWarps * slots * slot_bytes;
   static constexpr int q_bytes = rows * 2 * D;         // hi | lo codes of each row
-  // ring | Q | Q row scales | scales of the ring's units | per-warp m, l | abort flag
+  static constexpr int o_pitch = D + 4;                // of a row of O while the warps join
+  static_assert(kWarps * rows * o_pitch * 4 <= ring, "the warps' O fits the rings");
+  // ring | Q | Q row scales | m, l and factor of each warp's rows | joined m, l |
+  // first key whose V is NaN in a column | barriers | flags
   static constexpr int o_q = ring;
   static constexpr int o_qs = o_q + q_bytes;
-  static constexpr int o_sc = o_qs + rows * 4;
-  static constexpr int o_ml = o_sc + kWarps * slots * 2 * 4;
-  static constexpr int o_flag = o_ml + kWarps * rows * 2 * 4;
-  static constexpr int o_nan = o_flag + 16;            // [D]: first key whose V is NaN there
-  static constexpr int total = o_nan + D * 4;
+  static constexpr int o_ml = o_qs + rows * 4;
+  static constexpr int o_l = o_ml + kWarps * rows * 3 * 4;
+  static constexpr int o_nan = o_l + rows * 2 * 4;
+  static constexpr int o_bar = o_nan + D * 4;
+  static constexpr int o_flag = o_bar + kWarps * slots * 8;
+  static constexpr int total = o_flag + 16;
 };
 
-// Chunk swizzle of a row inside a slot: the K reads (8 lanes: 2 neighbouring
-// rows x 4 chunks) and the V reads (4 rows two apart x 2 chunks) both touch all
-// 32 banks once. 64-byte rows pair up in a 128-byte line, so their K reads need
-// none and their V reads settle for two passes.
+// The K rows of an MMA's 8 columns and the V rows of its k index are free to
+// choose, as long as both agree. Column n is key 8 j + n / 2 + 4 (n % 2) where
+// rows are 128 bytes: with TMA's swizzle (chunk XOR row) the 8 lanes of a K read
+// (2 rows x 4 chunks) and of a V read (4 rows x 2 chunks) then touch all banks
+// once. 64-byte rows take key 8 j + n (their V reads take two passes).
 template <int D>
-__device__ __forceinline__ int swz(int row, int chunk) {
-  if constexpr (D == 64) return chunk ^ (2 * ((row >> 1) & 1));
-  return chunk ^ ((2 * ((row >> 1) & 3)) ^ (4 * (row & 1)));
+__device__ __forceinline__ int key_of(int n) {
+  if constexpr (D == 64) return n;
+  return (n >> 1) + 4 * (n & 1);
+}
+// V's chunk of lane group g.
+__device__ __forceinline__ int v_chunk(int g) { return (g >> 1) | ((g & 1) << 2); }
+// d of element `pos` of a row of O as the warps leave it: [m-tile k][g][2].
+template <int D>
+__device__ __forceinline__ int d_of(int pos) {
+  const int k = pos >> 4, g = (pos >> 1) & 7, b = pos & 1;
+  if constexpr (D == 64) return g * 8 + 2 * k + b;
+  return 128 * (k >> 3) + 16 * v_chunk(g) + 2 * (k & 7) + b;
 }
 
 template <int D, int QM>
 __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
-attn_split_kernel(const Args p) {
+attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
+                  const __grid_constant__ CUtensorMap v_map) {
   using C = Cfg<D, QM>;
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* s_q = smem + C::o_q;
   float* s_qs = reinterpret_cast<float*>(smem + C::o_qs);
   float* s_ml = reinterpret_cast<float*>(smem + C::o_ml);
-  int* s_flag = reinterpret_cast<int*>(smem + C::o_flag);   // [0] last to arrive, [1] a NaN in V
+  float* s_l = reinterpret_cast<float*>(smem + C::o_l);
   int* s_nan = reinterpret_cast<int*>(smem + C::o_nan);
+  int* s_flag = reinterpret_cast<int*>(smem + C::o_flag);   // last to arrive | a NaN in V | gave up
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   unsigned char* ring = smem + w * (C::slots * C::slot_bytes);
-  float* ring_sc = reinterpret_cast<float*>(smem + C::o_sc) + w * C::slots * 2;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::o_bar) + w * C::slots;
   const int G = p.Hq / p.Hk, B = 1 << p.log_b;
-  const size_t block_bytes = (size_t)B * D;
+  const int log_box = min(p.log_b, 5);                 // tokens of a TMA box, and boxes of a half unit
+  const int pages = kUnit >> log_box;
+  const int page = lane & (pages - 1), bx = lane >> (5 - log_box);
+  const bool posts = bx < C::boxes;
+  const int absent = max(p.num_blocks * p.Hk, 1);      // a box past the end reads zeros
 
+  if (lane < C::slots) tc::mbar_init(full + lane, 1);
+  if (tid == 0) s_flag[2] = 0;
+  __syncwarp();
+  bool dead = false;                                   // a wait of this warp ran out
+  int posted = 0, taken = 0;                           // half units, over all segments
   pdl_wait();
   pdl_trigger();
   const Start start = read_start(p.starts + blockIdx.x);
@@ -329,54 +370,50 @@ attn_split_kernel(const Args p) {
 
     // ---- this warp's units: first_unit + w, + 8, ... --------------------------
     const int mine = seg > w ? (seg - w + kWarps - 1) / kWarps : 0;
-    const int halves = 2 * mine;
-    // Blocks of the two 16-token halves of the next unit to be copied.
-    auto block_at = [&](int unit, int half) {
-      const int tok = unit * kUnit + half * 16;
-      return tok < key_end ? __ldg(table + (tok >> p.log_b)) : 0;
+    // Block of this lane's box of unit i; read a unit before it is needed.
+    auto block_of = [&](int i) {
+      const int key = (first_unit + w + i * kWarps) * kUnit + (page << log_box);
+      return i < mine && key < key_end ? __ldg(table + (key >> p.log_b)) : -1;
     };
-    int cur0 = 0, cur1 = 0, nxt0 = 0, nxt1 = 0;
-    if (mine > 0) {
-      nxt0 = block_at(first_unit + w, 0);
-      nxt1 = block_at(first_unit + w, 1);
-    }
+    int blk = -1, blk_next = block_of(0);
+    // Lane l & 3 of the unit being copied: K's scale of its halves, V's.
+    float sc_next = 0.f;
     auto issue = [&](int h) {
-      if (h < halves) {
-        const int i = h >> 1, is_v = h & 1;
-        const int unit = first_unit + w + i * kWarps;
-        if (!is_v) {
-          cur0 = nxt0;
-          cur1 = nxt1;
-          if (i + 1 < mine) {
-            nxt0 = block_at(unit + kWarps, 0);
-            nxt1 = block_at(unit + kWarps, 1);
-          }
-          if ((unsigned)cur0 >= (unsigned)p.num_blocks || (unsigned)cur1 >= (unsigned)p.num_blocks)
+      const int i = h >> 1, is_v = h & 1;
+      if (i >= mine || dead) return;
+      const int key0 = (first_unit + w + i * kWarps) * kUnit;
+      if (!is_v) {
+        blk = blk_next;
+        blk_next = block_of(i + 1);
+        const int half = lane & 1;
+        const int b = __shfl_sync(0xffffffffu, blk, pages == 2 ? half : 0);
+        sc_next = 1.f;
+        if (key0 + half * 16 < key_end) {
+          if ((unsigned)b < (unsigned)p.num_blocks)
+            sc_next = __ldg(((lane & 2) ? p.vs : p.ks) + (size_t)b * p.Hk + head);
+          else
             record_device_status(GDN_ERR_INVALID_ARG);
         }
-        const uint8_t* base = is_v ? p.vc : p.kc;
-        unsigned char* slot = ring + (h % C::slots) * C::slot_bytes;
-        constexpr int rows_per = 32 / C::chunks;                 // rows per warp-wide copy
-        const int c = lane % C::chunks, r_in = lane / C::chunks;
-#pragma unroll
-        for (int k = 0; k < kUnit / rows_per; ++k) {
-          const int r = k * rows_per + r_in;
-          const int tok = unit * kUnit + r;
-          const int blk = r < 16 ? cur0 : cur1;
-          const bool ok = tok < key_end && (unsigned)blk < (unsigned)p.num_blocks;
-          const uint8_t* src = base;
-          if (ok) src += ((size_t)blk * p.Hk + head) * block_bytes + (size_t)(tok & (B - 1)) * D + c * 16;
-          tc::cp_async16(slot + r * D + swz<D>(r, c) * 16, src, ok ? 16u : 0u);
-        }
-        if (lane < 2) {
-          const int blk = lane ? cur1 : cur0;
-          const bool ok = unit * kUnit + lane * 16 < key_end && (unsigned)blk < (unsigned)p.num_blocks;
-          const float* sc = is_v ? p.vs : p.ks;
-          cp_async4(ring_sc + (h % C::slots) * 2 + lane, ok ? sc + (size_t)blk * p.Hk + head : sc,
-                    ok ? 4u : 0u);
-        }
       }
-      tc::cp_async_commit();
+      const int st = posted % C::slots;
+      if (lane == 0) tc::mbar_arrive_expect_tx(full + st, C::slot_bytes);
+      __syncwarp();
+      if (posts)
+        tma_box(ring + st * C::slot_bytes + (bx * kUnit + (page << log_box)) * C::row,
+                is_v ? &v_map : &k_map, bx * C::row, (key0 + (page << log_box)) & (B - 1),
+                (unsigned)blk < (unsigned)p.num_blocks ? blk * p.Hk + head : absent, full + st);
+      ++posted;
+    };
+    // The next half unit in order; its slot.
+    auto take = [&]() {
+      const int st = taken % C::slots;
+      if (!dead && !__all_sync(0xffffffffu, tc::mbar_wait(full + st, (taken / C::slots) & 1))) {
+        dead = true;
+        s_flag[2] = 1;
+        record_device_status(GDN_ERR_TIMEOUT);
+      }
+      ++taken;
+      return ring + st * C::slot_bytes;
     };
 #pragma unroll
     for (int h = 0; h < C::slots - 1; ++h) issue(h);
@@ -469,19 +506,22 @@ attn_split_kernel(const Args p) {
         for (int c = 0; c < 4; ++c) acc[m][i][c] = 0.f;
     }
 
-    for (int i = 0; i < mine; ++i) {
+    for (int i = 0; i < mine && !dead; ++i) {
       const int unit = first_unit + w + i * kWarps;
-      // K of unit i has landed; its slot's predecessor is free again.
-      tc::cp_async_wait_group<C::slots - 2>();
-      __syncwarp();
-      issue(2 * i + C::slots - 1);
+      // The unit's scales, before those of the next one replace them.
+      float ksc[2], lvs[2], ivs[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        ksc[k] = __shfl_sync(0xffffffffu, sc_next, k);
+        const float v = fmaxf(__shfl_sync(0xffffffffu, sc_next, 2 + k), 7.888609052210118e-31f);   // 2^-100
+        lvs[k] = lg2_approx(v);
+        ivs[k] = __fdividef(1.f, v);
+      }
+      // K of unit i has landed, and the slot before it is free again.
       float sc[QM][4][2];
-      float ksc[2];
       {
-        const int sl = (2 * i) % C::slots;
-        const unsigned char* slot = ring + sl * C::slot_bytes;
-        ksc[0] = ring_sc[sl * 2];
-        ksc[1] = ring_sc[sl * 2 + 1];
+        const unsigned char* slot = take();
+        issue(2 * i + C::slots - 1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float c4[QM][4];
@@ -489,10 +529,11 @@ attn_split_kernel(const Args p) {
           for (int m = 0; m < QM; ++m)
 #pragma unroll
             for (int c = 0; c < 4; ++c) c4[m][c] = 0.f;
-          const int r = 8 * j + g;
+          const int r = 8 * j + key_of<D>(g);
 #pragma unroll
           for (int c = 0; c < D / 64; ++c) {
-            const uint4 kk = *reinterpret_cast<const uint4*>(slot + r * D + swz<D>(r, t4 + 4 * c) * 16);
+            const uint4 kk = *reinterpret_cast<const uint4*>(
+                slot + (c >> 1) * (kUnit * C::row) + swizzled<C::row>(r, t4 + 4 * (c & 1)));
 #pragma unroll
             for (int m = 0; m < QM; ++m) {
               mma_e4m3(c4[m], qf[m][2 * c][0], qf[m][2 * c][1], qf[m][2 * c][2], qf[m][2 * c][3],
@@ -508,41 +549,34 @@ attn_split_kernel(const Args p) {
           }
         }
       }
-      // V of unit i has landed.
-      tc::cp_async_wait_group<C::slots - 2>();
       __syncwarp();
+      unsigned char* slot = take();                      // V of unit i
       issue(2 * i + C::slots);
-      const int sl = (2 * i + 1) % C::slots;
-      const unsigned char* slot = ring + sl * C::slot_bytes;
-      float lvs[2], ivs[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float vsc = fmaxf(ring_sc[sl * 2 + k], 7.888609052210118e-31f);   // 2^-100
-        lvs[k] = lg2_approx(vsc);
-        ivs[k] = __fdividef(1.f, vsc);
-      }
       const bool cut = unit * kUnit + kUnit > min_lim;
-      // Where the rows of the tile do not see the same keys, a weight of zero
-      // must not meet a NaN (0 x NaN is NaN): a NaN of V is taken out of the
-      // slot and kept as the first key whose column has one.
-      if (cut && min_lim < key_end) {
-        unsigned char* vs_ = ring + sl * C::slot_bytes;
+      // Keys past the end hold stale bytes: zeros instead. And where the rows of the
+      // tile do not see the same keys, a weight of zero must not meet a NaN (0 x NaN
+      // is NaN): a NaN of V is taken out of the slot and kept as the first key whose
+      // column has one.
+      if (cut && (min_lim < key_end || unit * kUnit + kUnit > key_end)) {
         for (int k = lane; k < C::slot_bytes / 4; k += 32) {
-          const uint32_t word = *reinterpret_cast<const uint32_t*>(vs_ + 4 * k);
-          if ((((word & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0) {
-            const int r = 4 * k / D, at = 4 * k % D;
-            const int col = swz<D>(r, at / 16) * 16 + at % 16;      // the swizzle is its own inverse
-            uint32_t clean = word;
+          uint32_t* at = reinterpret_cast<uint32_t*>(slot) + k;
+          const int box = 4 * k / (kUnit * C::row), r = 4 * k / C::row % kUnit;
+          // The swizzle is its own inverse.
+          const int col = box * C::row + (swizzled<C::row>(r, 4 * k % C::row / 16) - r * C::row) + 4 * k % 16;
+          const uint32_t word = *at;
+          uint32_t clean = unit * kUnit + r >= key_end ? 0u : word;
+          if ((((clean & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0) {
             for (int c = 0; c < 4; ++c) {
-              if (((word >> (8 * c)) & 0x7fu) == 0x7fu) {
+              if (((clean >> (8 * c)) & 0x7fu) == 0x7fu) {
                 atomicMin(s_nan + col + c, unit * kUnit + r);
                 clean &= ~(0xffu << (8 * c));
               }
             }
-            *reinterpret_cast<uint32_t*>(vs_ + 4 * k) = clean;
             s_flag[1] = 1;
           }
+          if (clean != word) *at = clean;
         }
+        tc::fence_smem_to_async();                       // before the next copy into the slot
         __syncwarp();
       }
       uint32_t pf[QM][4];
@@ -554,7 +588,7 @@ attn_split_kernel(const Args p) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float xx = fmaf(sc[m][j][e], rs[m] * ksc[j >> 1], lvs[j >> 1]);
-            if (cut && unit * kUnit + 8 * j + 2 * t4 + e >= lim[m]) xx = -INFINITY;
+            if (cut && unit * kUnit + 8 * j + key_of<D>(2 * t4 + e) >= lim[m]) xx = -INFINITY;
             sc[m][j][e] = xx;
             mx = fmaxf(mx, xx);
           }
@@ -585,17 +619,16 @@ attn_split_kernel(const Args p) {
         }
         l_run[m] += lsum;
       }
-      // O^T += V^T P^T: lane (g, t4) holds d = 16 chunk + byte, 16 chunk(g): the
-      // two rows of m-tile b are bytes 2b and 2b + 1 of the lane's own chunk.
+      // O^T += V^T P^T: the two rows of m-tile k are bytes 2k and 2k + 1 of the
+      // lane's own 16-byte chunk (8-byte one for d = 64) of the V rows.
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        const int r0 = 16 * ks + 2 * t4;
         if constexpr (D == 64) {
           uint2 va[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int r = r0 + (k & 1) + 8 * (k >> 1);
-            va[k] = *reinterpret_cast<const uint2*>(slot + r * D + swz<D>(r, g >> 1) * 16 + (g & 1) * 8);
+            const int r = 16 * ks + 8 * (k >> 1) + key_of<D>(2 * t4 + (k & 1));
+            va[k] = *reinterpret_cast<const uint2*>(slot + swizzled<C::row>(r, g >> 1) + (g & 1) * 8);
           }
           const uint32_t wv[4][2] = {{va[0].x, va[0].y}, {va[1].x, va[1].y},
                                      {va[2].x, va[2].y}, {va[3].x, va[3].y}};
@@ -619,8 +652,9 @@ attn_split_kernel(const Args p) {
             uint4 va[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const int r = r0 + (k & 1) + 8 * (k >> 1);
-              va[k] = *reinterpret_cast<const uint4*>(slot + r * D + swz<D>(r, g + 8 * cc) * 16);
+              const int r = 16 * ks + 8 * (k >> 1) + key_of<D>(2 * t4 + (k & 1));
+              va[k] = *reinterpret_cast<const uint4*>(slot + cc * (kUnit * C::row) +
+                                                      swizzled<C::row>(r, v_chunk(g)));
             }
             const uint32_t wv[4][4] = {{va[0].x, va[0].y, va[0].z, va[0].w},
                                        {va[1].x, va[1].y, va[1].z, va[1].w},
@@ -645,90 +679,83 @@ attn_split_kernel(const Args p) {
       }
       __syncwarp();
     }
-    tc::cp_async_wait_group<0>();
 
     // ---- join the warps ------------------------------------------------------
 #pragma unroll
     for (int m = 0; m < QM; ++m) {
       l_run[m] += __shfl_xor_sync(0xffffffffu, l_run[m], 1);
       l_run[m] += __shfl_xor_sync(0xffffffffu, l_run[m], 2);
-      if (t4 == 0) {
-        s_ml[(w * C::rows + m * 8 + g) * 2] = m_run[m];
-        s_ml[(w * C::rows + m * 8 + g) * 2 + 1] = l_run[m];
-      }
+      if (t4 == 0)
+        *reinterpret_cast<float2*>(s_ml + (w * C::rows + m * 8 + g) * 2) = make_float2(m_run[m], l_run[m]);
     }
     __syncthreads();                     // also: every warp is done with its ring
-    // Warp w leaves its rows of O, on the common maximum, in its ring:
-    // float32 [rows][D], 16-byte chunks XOR-ed by the row.
-    float* s_o = reinterpret_cast<float*>(smem);
-    static_assert(kWarps * C::rows * D * 4 <= C::ring, "the warps' O fits the rings");
-    constexpr int n_el = C::rows * D / (kWarps * 32);
+    float* s_f = s_ml + kWarps * C::rows * 2;            // factors to the common maximum
+    if (tid < C::rows) {
+      float top = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int m = 0; m < QM; ++m) {
+      for (int k = 0; k < kWarps; ++k) top = fmaxf(top, s_ml[(k * C::rows + tid) * 2]);
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const float2 ml = *reinterpret_cast<const float2*>(s_ml + (k * C::rows + tid) * 2);
+        // A warp without keys has zeros; a NaN row keeps m = -inf and its l, a NaN.
+        const float f = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - top);
+        s_f[k * C::rows + tid] = f;
+        l += ml.y * f;
+      }
+      s_l[tid * 2] = top;
+      s_l[tid * 2 + 1] = l;
+    }
+    __syncthreads();
+    // Each warp leaves its O, on the common maximum, as [row][m-tile][g][2]: rows
+    // D + 4 floats apart, so that a store's 16 lanes touch all banks.
+    float* s_o = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int m = 0; m < QM; ++m)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = m * 8 + 2 * t4 + e;
-        float top = -INFINITY;
+        const float f = s_f[w * C::rows + r];
+        float* dst = s_o + (w * C::rows + r) * C::o_pitch + 2 * g;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) top = fmaxf(top, s_ml[(k * C::rows + r) * 2]);
-        const float mw = s_ml[(w * C::rows + r) * 2];
-        // A warp without keys has f = 0; its accumulator is zero as well.
-        const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - top);
-        float* dst = s_o + (w * C::rows + r) * D;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          // m-tile k: d of its rows g and g + 8.
-          int d0;
-          if constexpr (D == 64) d0 = g * 8 + 2 * k;
-          else d0 = 128 * (k >> 3) + g * 16 + 2 * (k & 7);
-          *reinterpret_cast<float2*>(dst + (d0 ^ (8 * (r & 3)))) =
-              make_float2(acc[m][k][e] * f, acc[m][k][2 + e] * f);
-        }
+        for (int k = 0; k < D / 16; ++k)
+          *reinterpret_cast<float2*>(dst + 16 * k) = make_float2(acc[m][k][e] * f, acc[m][k][2 + e] * f);
       }
-    }
     __syncthreads();
-    float sum_o[n_el];
+    const bool whole = seg == n_units, gave_up = s_flag[2] != 0;
+    float* part = p.partials + ((size_t)blockIdx.x * 2 + (first_unit == 0 ? 1 : 0)) * C::rows * (D + 2);
+    // Four elements of row r, from position pos, to the output.
+    auto put = [&](int r, int pos, float4 o, float l) {
+      if (r >= n_rows || gave_up) return;
+      const int row = row0 + r;
+      const float il = l == 0.f ? 0.f : 1.f / l;
+      __nv_bfloat16* at = p.o + ((int64_t)(s.first + row / G) * p.Hq + head * G + row % G) * D;
+      *reinterpret_cast<uint32_t*>(at + d_of<D>(pos)) = pack_bf16x2(o.x * il, o.y * il);
+      *reinterpret_cast<uint32_t*>(at + d_of<D>(pos + 2)) = pack_bf16x2(o.z * il, o.w * il);
+    };
 #pragma unroll
-    for (int i = 0; i < n_el; ++i) {
-      const int at = i * kWarps * 32 + tid, r = at / D, dd = at % D;
-      sum_o[i] = 0.f;
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) sum_o[i] += s_o[(k * C::rows + r) * D + (dd ^ (8 * (r & 3)))];
-      if (s_flag[1] && r < n_rows && visible(s, (row0 + r) / G) > s_nan[dd]) sum_o[i] = NAN;
-    }
-    // Row r's joined maximum and sum (each thread for the rows that it holds).
-    const bool whole = seg == n_units;
-    float* part = nullptr;
-    if (!whole)
-      part = p.partials + ((size_t)blockIdx.x * 2 + (first_unit == 0 ? 1 : 0)) * C::rows * (D + 2);
-#pragma unroll
-    for (int i = 0; i < n_el; ++i) {
-      const int at = i * kWarps * 32 + tid, r = at / D, dd = at % D;
-      float top = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) top = fmaxf(top, s_ml[(k * C::rows + r) * 2]);
-      float l = 0.f;
+    for (int e = tid * 4; e < C::rows * D; e += kWarps * 32 * 4) {
+      const int r = e / D, pos = e % D;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
-        const float mw = s_ml[(k * C::rows + r) * 2];
-        // NaN sums pass on: a NaN row keeps m = -inf, so its l is added as it is.
-        const float lw = s_ml[(k * C::rows + r) * 2 + 1];
-        l += mw == -INFINITY ? lw : lw * ex2_approx(mw - top);
+        const float4 v = *reinterpret_cast<const float4*>(s_o + (k * C::rows + r) * C::o_pitch + pos);
+        o.x += v.x;
+        o.y += v.y;
+        o.z += v.z;
+        o.w += v.w;
       }
-      if (whole) {
-        if (r < n_rows) {
-          const int row = row0 + r;
-          const float o = l == 0.f ? 0.f : sum_o[i] / l;
-          p.o[((int64_t)(s.first + row / G) * p.Hq + head * G + row % G) * D + dd] = __float2bfloat16_rn(o);
-        }
-      } else {
-        __stcg(part + 2 * C::rows + r * D + dd, sum_o[i]);
-        if (dd == 0) {
-          __stcg(part + r * 2, top);
-          __stcg(part + r * 2 + 1, l);
-        }
+      if (s_flag[1] && r < n_rows) {
+        const int lim_r = visible(s, (row0 + r) / G);
+        if (lim_r > s_nan[d_of<D>(pos)]) o.x = NAN;
+        if (lim_r > s_nan[d_of<D>(pos + 1)]) o.y = NAN;
+        if (lim_r > s_nan[d_of<D>(pos + 2)]) o.z = NAN;
+        if (lim_r > s_nan[d_of<D>(pos + 3)]) o.w = NAN;
       }
+      if (whole) put(r, pos, o, s_l[r * 2 + 1]);
+      else __stcg(reinterpret_cast<float4*>(part + 2 * C::rows + e), o);
     }
+    if (!whole && tid < C::rows)
+      __stcg(reinterpret_cast<float2*>(part) + tid, *reinterpret_cast<const float2*>(s_l + tid * 2));
     if (!whole) {
       // The item's CTAs are those of its first and last unit and all between, in
       // groups of kJoin: the last of a group joins it in place of its first
@@ -739,7 +766,6 @@ attn_split_kernel(const Args p) {
       const int ga = c0 + grp * kJoin, gb = min(c1, ga + kJoin - 1);
       const size_t psz = C::rows * (D + 2);
       float* fs = reinterpret_cast<float*>(smem);             // factors, [n][rows]
-      float* s_l = fs + kJoinMax * C::rows;
       auto slot = [&](int c) { return p.partials + ((size_t)c * 2 + (c == c0)) * psz; };
       // Joins the partials of CTAs a, a + step, ... (n of them); `out` or the output.
       auto join = [&](int a, int step, int n, float* out) {
@@ -765,7 +791,7 @@ attn_split_kernel(const Args p) {
         __syncthreads();
 #pragma unroll 1
         for (int e = tid * 4; e < C::rows * D; e += kWarps * 32 * 4) {
-          const int r = e / D, dd = e % D;
+          const int r = e / D;
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
           for (int c = 0; c < n; ++c) {
@@ -776,16 +802,8 @@ attn_split_kernel(const Args p) {
             o.z = fmaf(v.z, f, o.z);
             o.w = fmaf(v.w, f, o.w);
           }
-          if (out) {
-            __stcg(reinterpret_cast<float4*>(out + 2 * C::rows + e), o);
-          } else if (r < n_rows) {
-            const int row = row0 + r;
-            const float l = s_l[r * 2 + 1], il = l == 0.f ? 0.f : 1.f / l;
-            uint2 b;
-            b.x = pack_bf16x2(o.x * il, o.y * il);
-            b.y = pack_bf16x2(o.z * il, o.w * il);
-            *reinterpret_cast<uint2*>(p.o + ((int64_t)(s.first + row / G) * p.Hq + head * G + row % G) * D + dd) = b;
-          }
+          if (out) __stcg(reinterpret_cast<float4*>(out + 2 * C::rows + e), o);
+          else put(r, e % D, o, s_l[r * 2 + 1]);
         }
         if (out && tid < C::rows)
           __stcg(reinterpret_cast<float2*>(out) + tid, make_float2(s_l[tid * 2], s_l[tid * 2 + 1]));
@@ -811,6 +829,7 @@ attn_split_kernel(const Args p) {
         if (last(item_counter, groups)) join(c0, kJoin, groups, nullptr);
       }
     }
+    tc::fence_smem_to_async();           // before the next copies into the ring
     __syncthreads();                     // the ring, Q and s_ml are free again
     u += seg;
     if (first_unit + seg == n_units && ++lo == num_items) {
@@ -823,6 +842,10 @@ attn_split_kernel(const Args p) {
       s = seq_of(p.cu, p.kv, it.seq, p.T, (int64_t)p.max_blocks << p.log_b);
     }
   }
+  // Copies of a warp that gave up land before its CTA may end.
+  if (dead)
+    for (int h = max(0, posted - C::slots); h < posted; ++h)
+      tc::mbar_wait(full + h % C::slots, (h / C::slots) & 1);
 }
 
 template <int D, int QM>
@@ -830,36 +853,41 @@ gdn_status_t launch_split(const Args& a, cudaStream_t st) {
   static const cudaError_t set = cudaFuncSetAttribute(
       attn_split_kernel<D, QM>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, QM>::total);
   if (set != cudaSuccess) return check_launch(set);
+  const int B = 1 << a.log_b;
+  const int64_t pages = (int64_t)a.num_blocks * a.Hk;
+  CUtensorMap k_map, v_map;
+  if (!cache_map(&k_map, a.kc, D, B, pages, std::min(B, kUnit)) ||
+      !cache_map(&v_map, a.vc, D, B, pages, std::min(B, kUnit))) {
+    set_cuda_error(cudaErrorInvalidValue);
+    return GDN_ERR_CUDA;
+  }
   return check_launch(launch_pdl(attn_split_kernel<D, QM>, dim3(a.split_grid), dim3(kWarps * 32),
-                                 Cfg<D, QM>::total, st, a));
+                                 Cfg<D, QM>::total, st, a, k_map, v_map));
 }
 
 }  // namespace
 
 gdn_status_t launch_attn_plan(const int32_t* cu, const int32_t* kv, int N, int T, int Hq, int Hk,
-                              int d, int64_t kv_max, void* workspace, cudaStream_t st) {
+                              int d, int64_t kv_max, int max_new_tokens, void* workspace,
+                              cudaStream_t st) {
   const Layout l = layout(T, N, Hq, Hk, d);
+  const int G = Hq / Hk, limit = split_limit(G);
+  const Kernels use = kernels_of(N, T, G, max_new_tokens);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   PlanArgs p;
   p.cu = cu;
   p.kv = kv;
   p.N = N;
   p.T = T;
-  p.G = Hq / Hk;
+  p.G = G;
   p.Hk = Hk;
-  p.rows = l.split_rows;
-  p.item_cap = l.item_cap;
-  p.grid = split_grid(d);
   p.kv_max = kv_max;
-  p.items = reinterpret_cast<Item*>(ws + l.items);
+  // A piece of the split kernel gives each of its 8 warps a unit at least.
+  p.list[0] = {l.split_rows, kUnit, 0, limit, l.item_cap, use.split ? split_grid(d) : 0, kWarps,
+               reinterpret_cast<Item*>(ws + l.items), reinterpret_cast<Start*>(ws + l.starts)};
+  p.list[1] = {l.tile_rows, kTileKeys, limit, 0x7fffffff, l.tile_cap, use.tile ? tile_grid() : 0, 1,
+               reinterpret_cast<Item*>(ws + l.tiles), reinterpret_cast<Start*>(ws + l.tile_starts)};
   p.counters = reinterpret_cast<int*>(ws + l.counters);
-  p.limit = split_limit(p.G);
-  p.tile_rows = l.tile_rows;
-  p.tile_cap = l.tile_cap;
-  p.tile_grid = tile_grid();
-  p.tiles = reinterpret_cast<Item*>(ws + l.tiles);
-  p.starts = reinterpret_cast<Start*>(ws + l.starts);
-  p.tile_starts = reinterpret_cast<Start*>(ws + l.tile_starts);
   return check_launch(launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p));
 }
 

@@ -34,7 +34,6 @@
 // prefetches of 16 bytes each) held the tensor cores to a fifth of their rate.
 #include <algorithm>
 
-#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -57,7 +56,7 @@ struct TC {
   static constexpr int VR = D == 256 ? 2 : 4;           // stages of V's codes
   static constexpr int VS = D == 256 ? 2 : 4;           // and of V widened
   static constexpr int loaders = (3 - M) * 128;
-  static constexpr int row = D == 64 ? 64 : 128;        // bytes of a row in a TMA box
+  static constexpr int row = box_row(D);                // bytes of a row in a TMA box
   static constexpr int boxes = D / row;                 // boxes across a cache row
   static constexpr int q_part = 128 * D;                // one part (hi or lo) of one tile
   static constexpr int c_stage = kKeys * D;             // a unit's codes of K or V
@@ -89,27 +88,6 @@ struct TC {
   static constexpr int c_s(int m, int b) { return m * 128 + b * 64; }
   static constexpr int c_o(int m) { return 256 + m * D; }
 };
-
-// TMA box: rows of one (block, head) to shared memory.
-__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int y, int z,
-                                        uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];"
-      :: "r"(tc::smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(bar))
-      : "memory");
-}
-// K-major operand of 128-byte (64-byte) swizzled rows: 8-row groups 8 rows apart.
-template <int kRow>
-__device__ __forceinline__ uint64_t desc_swizzled(uint32_t addr) {
-  return tc::smem_desc(addr, 16, 8 * kRow) | ((uint64_t)(kRow == 128 ? 2 : 4) << 61);
-}
-// Byte of chunk c of row r under that swizzle.
-template <int kRow>
-__device__ __forceinline__ int swizzled(int r, int c) {
-  if constexpr (kRow == 128) return r * 128 + ((c ^ (r & 7)) << 4);
-  return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-}
 
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -826,13 +804,40 @@ __global__ void __launch_bounds__(256) attn_tile_join_kernel(const Args p) {
   for (int k = 0; k < kCols; k += 8) *reinterpret_cast<uint4*>(out + k) = pack8(v + k);
 }
 
+template <int D>
+gdn_status_t launch_tile(const Args& a, cudaStream_t st) {
+  static const cudaError_t set = cudaFuncSetAttribute(
+      attn_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TC<D>::total);
+  if (set != cudaSuccess) return check_launch(set);
+  const int B = 1 << a.log_b;
+  const int64_t pages = (int64_t)a.num_blocks * a.Hk;
+  CUtensorMap k_map, v_map;
+  if (!cache_map(&k_map, a.kc, D, B, pages, std::min(B, kKeys)) ||
+      !cache_map(&v_map, a.vc, D, B, pages, std::min(B, kKeys))) {
+    set_cuda_error(cudaErrorInvalidValue);
+    return GDN_ERR_CUDA;
+  }
+  const gdn_status_t rc = check_launch(launch_pdl(attn_tile_kernel<D>, dim3(a.tile_grid),
+                                                  dim3(kThreads), TC<D>::total, st, a, k_map, v_map));
+  if (rc != GDN_OK) return rc;
+  return check_launch(launch_pdl(attn_tile_join_kernel<D>, dim3(a.tile_grid, TC<D>::M * 4),
+                                 dim3(256), 0, st, a));
+}
+
+}  // namespace
+
+namespace attn {
+
+namespace {
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+}  // namespace
 
 // The cache as (d, token of the block, block x head), boxes of `rows` tokens.
-bool cache_map(CUtensorMap* map, const void* cache, int d, int B, int64_t pages, int row, int rows) {
+bool cache_map(CUtensorMap* map, const void* cache, int d, int B, int64_t pages, int rows) {
+  const int row = box_row(d);
   static const EncodeTiled encode = [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
@@ -853,27 +858,7 @@ bool cache_map(CUtensorMap* map, const void* cache, int d, int B, int64_t pages,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
-gdn_status_t launch_tile(const Args& a, cudaStream_t st) {
-  static const cudaError_t set = cudaFuncSetAttribute(
-      attn_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TC<D>::total);
-  if (set != cudaSuccess) return check_launch(set);
-  const int B = 1 << a.log_b;
-  const int64_t pages = (int64_t)a.num_blocks * a.Hk;
-  CUtensorMap k_map, v_map;
-  if (!cache_map(&k_map, a.kc, D, B, pages, TC<D>::row, std::min(B, kKeys)) ||
-      !cache_map(&v_map, a.vc, D, B, pages, TC<D>::row, std::min(B, kKeys))) {
-    set_cuda_error(cudaErrorInvalidValue);
-    return GDN_ERR_CUDA;
-  }
-  const gdn_status_t rc = check_launch(launch_pdl(attn_tile_kernel<D>, dim3(a.tile_grid),
-                                                  dim3(kThreads), TC<D>::total, st, a, k_map, v_map));
-  if (rc != GDN_OK) return rc;
-  return check_launch(launch_pdl(attn_tile_join_kernel<D>, dim3(a.tile_grid, TC<D>::M * 4),
-                                 dim3(256), 0, st, a));
-}
-
-}  // namespace
+}  // namespace attn
 
 gdn_status_t launch_attn_tile(const Args& a, cudaStream_t st) {
   if (a.d == 64) return launch_tile<64>(a, st);
