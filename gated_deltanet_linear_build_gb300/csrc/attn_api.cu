@@ -261,7 +261,6 @@ gdn_status_t gdn_paged_attention(const void* q, int64_t q_stride, const void* k_
   a.max_blocks = max_blocks;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   a.items = reinterpret_cast<attn::Item*>(ws + l.items);
-  a.counters = reinterpret_cast<int*>(ws + l.counters);
   a.partials = reinterpret_cast<float*>(ws + l.partials);
   a.tiles = reinterpret_cast<attn::Item*>(ws + l.tiles);
   a.starts = reinterpret_cast<const attn::Start*>(ws + l.starts);

@@ -33,7 +33,7 @@ struct alignas(64) Start {
 };
 
 struct Layout {
-  size_t starts, tile_starts, items, counters, partials, tiles, tile_partials, total;
+  size_t starts, tile_starts, items, partials, tiles, tile_partials, total;
   int item_cap, tile_cap, split_rows, tile_rows;
 };
 
@@ -105,7 +105,6 @@ struct Args {
   int N, T, Hq, Hk, d, log_b, num_blocks, max_blocks;
   float scale_log2;                    // softmax scale x log2 e
   Item* items;
-  int* counters;                       // arrivals, see the split kernel
   float* partials;
   Item* tiles;
   int split_rows, split_grid, tile_grid;

@@ -25,10 +25,11 @@
 //   2^8 (the headroom of P's range): most units skip it.
 //
 // Work split: all units of all (tile, head) items form one line that is cut
-// into equal pieces, one per CTA; a piece may end inside an item. Such items
-// leave float32 partial results in the workspace, and the CTA that arrives
-// last at the item's counter joins them in CTA order (a fixed order, so that
-// equal inputs give equal bits).
+// cut into equal pieces, one per CTA; a piece may end inside an item. Such items
+// leave float32 partial results in the workspace, which a second kernel joins
+// in a fixed order (equal inputs give equal bits). Joining inside this kernel,
+// by the CTA that arrives last, took as long as that launch does, and its code
+// cost the stream its registers (48 requests of 3k-30k tokens: 232 -> 335 us).
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -55,8 +56,6 @@ Layout layout(int T, int N, int Hq, int Hk, int d) {
   at = up(at + tile_grid() * sizeof(Start));
   l.items = at;
   at = up(at + (size_t)l.item_cap * sizeof(Item));
-  l.counters = at;
-  at = up(at + ((size_t)l.item_cap * Hk + 2 * kSplitGridMax) * sizeof(int));
   l.tiles = at;
   at = up(at + (size_t)l.tile_cap * sizeof(Item));
   l.partials = at;
@@ -90,7 +89,6 @@ struct PlanArgs {
   int N, T, G, Hk;
   int64_t kv_max;
   ListArgs list[2];                    // split kernel, tensor-core kernel
-  int* counters;
 };
 
 // Inclusive scan of a pair over the block; the total in tot.
@@ -229,8 +227,6 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
     if (a.grid == 0) continue;                  // that kernel has no sequence in this step
     int items, units;
     build_list(p, a, sums, s_first, s_cum, items, units);
-    if (k == 0)
-      for (int i = threadIdx.x; i < items * p.Hk + 2 * kSplitGridMax; i += kPlanThreads) p.counters[i] = 0;
     cut_line(p, a, s_cum, items, units);
     __syncthreads();                            // s_cum is free again
   }
@@ -276,8 +272,7 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 // Split kernel
 // ---------------------------------------------------------------------------
 constexpr int kWarps = 8;
-constexpr int kJoin = 16;                // partial results joined by one CTA
-constexpr int kJoinMax = (kSplitGridMax + kJoin - 1) / kJoin > kJoin ? (kSplitGridMax + kJoin - 1) / kJoin : kJoin;
+constexpr int kJoinCols = 4;             // CTAs that share the elements of a joined item
 
 template <int D, int QM>
 struct Cfg {
@@ -321,6 +316,46 @@ __device__ __forceinline__ int d_of(int pos) {
   return 128 * (k >> 3) + 16 * v_chunk(g) + 2 * (k & 7) + b;
 }
 
+// Where the rows of a tile go.
+struct RowsOut {
+  __nv_bfloat16* o;
+  int first, row0, n_rows, G, Hq, head;
+};
+// Four elements of row r, from position pos, over their sum l.
+template <int D>
+__device__ __forceinline__ void put_row4(const RowsOut& t, int r, int pos, float4 o, float l) {
+  if (r >= t.n_rows) return;
+  const int row = t.row0 + r, tok = row / t.G;
+  const float il = l == 0.f ? 0.f : 1.f / l;
+  __nv_bfloat16* at = t.o + ((int64_t)(t.first + tok) * t.Hq + t.head * t.G + row - tok * t.G) * D;
+  *reinterpret_cast<uint32_t*>(at + d_of<D>(pos)) = pack_bf16x2(o.x * il, o.y * il);
+  *reinterpret_cast<uint32_t*>(at + d_of<D>(pos + 2)) = pack_bf16x2(o.z * il, o.w * il);
+}
+
+// Takes this lane's NaNs of V out of a slot and keeps the first key of each of
+// their columns; true if there were any. (Out of line: few units need it, and
+// its registers are not the stream's.)
+template <int D>
+__device__ __noinline__ bool take_nans(unsigned char* slot, int* first_nan, int key0) {
+  constexpr int row = box_row(D);
+  bool any = false;
+#pragma unroll 1
+  for (int at = (threadIdx.x & 31) * 4; at < kUnit * D; at += 128) {
+    const uint32_t word = *reinterpret_cast<const uint32_t*>(slot + at);
+    if ((((word & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) == 0) continue;
+    const int box = at / (kUnit * row), r = at / row % kUnit;
+    // The swizzle is its own inverse.
+    const int col = box * row + swizzled<row>(r, at % row / 16) - r * row + at % 16;
+    for (int c = 0; c < 4; ++c)
+      if (((word >> (8 * c)) & 0x7fu) == 0x7fu) {
+        atomicMin(first_nan + col + c, key0 + r);
+        slot[at + c] = 0;
+      }
+    any = true;
+  }
+  return any;
+}
+
 template <int D, int QM>
 __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
 attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
@@ -332,7 +367,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
   float* s_ml = reinterpret_cast<float*>(smem + C::o_ml);
   float* s_l = reinterpret_cast<float*>(smem + C::o_l);
   int* s_nan = reinterpret_cast<int*>(smem + C::o_nan);
-  int* s_flag = reinterpret_cast<int*>(smem + C::o_flag);   // last to arrive | a NaN in V | gave up
+  int* s_flag = reinterpret_cast<int*>(smem + C::o_flag);   // unused | a NaN in V | gave up
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   unsigned char* ring = smem + w * (C::slots * C::slot_bytes);
@@ -553,30 +588,23 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       unsigned char* slot = take();                      // V of unit i
       issue(2 * i + C::slots);
       const bool cut = unit * kUnit + kUnit > min_lim;
-      // Keys past the end hold stale bytes: zeros instead. And where the rows of the
-      // tile do not see the same keys, a weight of zero must not meet a NaN (0 x NaN
-      // is NaN): a NaN of V is taken out of the slot and kept as the first key whose
-      // column has one.
-      if (cut && (min_lim < key_end || unit * kUnit + kUnit > key_end)) {
-        for (int k = lane; k < C::slot_bytes / 4; k += 32) {
-          uint32_t* at = reinterpret_cast<uint32_t*>(slot) + k;
-          const int box = 4 * k / (kUnit * C::row), r = 4 * k / C::row % kUnit;
-          // The swizzle is its own inverse.
-          const int col = box * C::row + (swizzled<C::row>(r, 4 * k % C::row / 16) - r * C::row) + 4 * k % 16;
-          const uint32_t word = *at;
-          uint32_t clean = unit * kUnit + r >= key_end ? 0u : word;
-          if ((((clean & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0) {
-            for (int c = 0; c < 4; ++c) {
-              if (((clean >> (8 * c)) & 0x7fu) == 0x7fu) {
-                atomicMin(s_nan + col + c, unit * kUnit + r);
-                clean &= ~(0xffu << (8 * c));
-              }
-            }
-            s_flag[1] = 1;
-          }
-          if (clean != word) *at = clean;
-        }
+      // Keys past the end hold stale bytes: zeros instead.
+      if (unit * kUnit + kUnit > key_end) {
+        const int past = max(0, key_end - unit * kUnit) * C::row;       // bytes of the rows before
+#pragma unroll 1
+        for (int box = 0; box < C::boxes; ++box)
+#pragma unroll 1
+          for (int at = past + lane * 16; at < kUnit * C::row; at += 512)
+            *reinterpret_cast<uint4*>(slot + box * (kUnit * C::row) + at) = make_uint4(0, 0, 0, 0);
         tc::fence_smem_to_async();                       // before the next copy into the slot
+        __syncwarp();
+      }
+      // Where the rows of the tile do not see the same keys, a weight of zero must not
+      // meet a NaN (0 x NaN is NaN): a NaN of V is taken out of the slot and kept as
+      // the first key whose column has one.
+      if (cut && min_lim < key_end) {
+        if (take_nans<D>(slot, s_nan, unit * kUnit)) s_flag[1] = 1;
+        tc::fence_smem_to_async();
         __syncwarp();
       }
       uint32_t pf[QM][4];
@@ -723,15 +751,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
     __syncthreads();
     const bool whole = seg == n_units, gave_up = s_flag[2] != 0;
     float* part = p.partials + ((size_t)blockIdx.x * 2 + (first_unit == 0 ? 1 : 0)) * C::rows * (D + 2);
-    // Four elements of row r, from position pos, to the output.
-    auto put = [&](int r, int pos, float4 o, float l) {
-      if (r >= n_rows || gave_up) return;
-      const int row = row0 + r;
-      const float il = l == 0.f ? 0.f : 1.f / l;
-      __nv_bfloat16* at = p.o + ((int64_t)(s.first + row / G) * p.Hq + head * G + row % G) * D;
-      *reinterpret_cast<uint32_t*>(at + d_of<D>(pos)) = pack_bf16x2(o.x * il, o.y * il);
-      *reinterpret_cast<uint32_t*>(at + d_of<D>(pos + 2)) = pack_bf16x2(o.z * il, o.w * il);
-    };
+    const RowsOut out = {p.o, s.first, row0, gave_up ? 0 : n_rows, G, p.Hq, head};
 #pragma unroll
     for (int e = tid * 4; e < C::rows * D; e += kWarps * 32 * 4) {
       const int r = e / D, pos = e % D;
@@ -751,84 +771,11 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         if (lim_r > s_nan[d_of<D>(pos + 2)]) o.z = NAN;
         if (lim_r > s_nan[d_of<D>(pos + 3)]) o.w = NAN;
       }
-      if (whole) put(r, pos, o, s_l[r * 2 + 1]);
+      if (whole) put_row4<D>(out, r, pos, o, s_l[r * 2 + 1]);
       else __stcg(reinterpret_cast<float4*>(part + 2 * C::rows + e), o);
     }
     if (!whole && tid < C::rows)
       __stcg(reinterpret_cast<float2*>(part) + tid, *reinterpret_cast<const float2*>(s_l + tid * 2));
-    if (!whole) {
-      // The item's CTAs are those of its first and last unit and all between, in
-      // groups of kJoin: the last of a group joins it in place of its first
-      // member's partial, the last group's joins the groups.
-      const long long at0 = (long long)head * units1 + cum;
-      const int c0 = (int)(at0 / per_cta), c1 = (int)((at0 + n_units - 1) / per_cta);
-      const int grp = ((int)blockIdx.x - c0) / kJoin, groups = (c1 - c0) / kJoin + 1;
-      const int ga = c0 + grp * kJoin, gb = min(c1, ga + kJoin - 1);
-      const size_t psz = C::rows * (D + 2);
-      float* fs = reinterpret_cast<float*>(smem);             // factors, [n][rows]
-      auto slot = [&](int c) { return p.partials + ((size_t)c * 2 + (c == c0)) * psz; };
-      // Joins the partials of CTAs a, a + step, ... (n of them); `out` or the output.
-      auto join = [&](int a, int step, int n, float* out) {
-        for (int r = w; r < C::rows; r += kWarps) {
-          float top = -INFINITY, l = 0.f;
-          for (int c = lane; c < n; c += 32) top = fmaxf(top, __ldcg(slot(a + c * step) + r * 2));
-#pragma unroll
-          for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-          for (int c = lane; c < n; c += 32) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot(a + c * step)) + r);
-            // NaN sums pass on: a NaN row has m = -inf and its l as it is.
-            const float f = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - top);
-            fs[c * C::rows + r] = f;
-            l += ml.y * f;
-          }
-#pragma unroll
-          for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-          if (lane == 0) {
-            s_l[r * 2] = top;
-            s_l[r * 2 + 1] = l;
-          }
-        }
-        __syncthreads();
-#pragma unroll 1
-        for (int e = tid * 4; e < C::rows * D; e += kWarps * 32 * 4) {
-          const int r = e / D;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int c = 0; c < n; ++c) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(slot(a + c * step) + 2 * C::rows + e));
-            const float f = fs[c * C::rows + r];
-            o.x = fmaf(v.x, f, o.x);
-            o.y = fmaf(v.y, f, o.y);
-            o.z = fmaf(v.z, f, o.z);
-            o.w = fmaf(v.w, f, o.w);
-          }
-          if (out) __stcg(reinterpret_cast<float4*>(out + 2 * C::rows + e), o);
-          else put(r, e % D, o, s_l[r * 2 + 1]);
-        }
-        if (out && tid < C::rows)
-          __stcg(reinterpret_cast<float2*>(out) + tid, make_float2(s_l[tid * 2], s_l[tid * 2 + 1]));
-      };
-      // One more arrival of `of` at the counter; true for the whole CTA at the last.
-      auto last = [&](int* counter, int of) {
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) {
-          const int seen = atomicAdd(counter, 1);
-          s_flag[0] = seen == of - 1;
-          if (seen == of - 1) *counter = 0;        // ready for the next call on this plan
-        }
-        __syncthreads();
-        if (s_flag[0]) __threadfence();
-        return s_flag[0] != 0;
-      };
-      int* item_counter = p.counters + 2 * kSplitGridMax + (size_t)lo * p.Hk + head;
-      if (groups == 1) {
-        if (last(item_counter, gb - ga + 1)) join(ga, 1, gb - ga + 1, nullptr);
-      } else if (last(p.counters + ga * 2 + (ga == c0), gb - ga + 1)) {
-        join(ga, 1, gb - ga + 1, slot(ga));
-        if (last(item_counter, groups)) join(c0, kJoin, groups, nullptr);
-      }
-    }
     tc::fence_smem_to_async();           // before the next copies into the ring
     __syncthreads();                     // the ring, Q and s_ml are free again
     u += seg;
@@ -848,6 +795,85 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       tc::mbar_wait(full + h % C::slots, (h / C::slots) & 1);
 }
 
+// Joins the partial results of items that were cut: CTA (c0, y) takes the item
+// that begins in CTA c0's piece and goes on past its end, a quarter of its
+// elements. Thread groups share a long item's partials; each adds its own in CTA
+// order, and the groups are added in order: the order is fixed.
+template <int D, int QM>
+__global__ void __launch_bounds__(256) attn_split_join_kernel(const Args p) {
+  constexpr int rows = 8 * QM, elems = rows * D / 4 / kJoinCols;      // float4 of this CTA
+  constexpr int groups = 256 / elems < 1 ? 1 : 256 / elems;
+  static_assert(256 % elems == 0, "whole groups");
+  __shared__ float fs[kSplitGridMax * rows];                          // factors [partial][row]
+  __shared__ float s_l[rows];
+  __shared__ float4 s_o[groups][elems];
+  pdl_wait();
+  pdl_trigger();
+  const int c0 = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  if (c0 + 1 >= (int)gridDim.x) return;
+  const Start next = read_start(p.starts + c0 + 1);
+  if (next.u >= next.u_end) return;
+  const long long at0 = (long long)next.head * next.units + next.it.cum;
+  if (at0 == next.u || at0 / next.per_cta != c0) return;    // not cut here, or begun earlier
+  const int n = (int)((at0 + next.it.units - 1) / next.per_cta) - c0 + 1;
+  const float* base = p.partials + ((size_t)c0 * 2 + 1) * (rows * (D + 2));
+  auto part = [&](int c) { return base + (c == 0 ? 0 : (size_t)(2 * c - 1) * (rows * (D + 2))); };
+  for (int r = tid >> 5; r < rows; r += 8) {
+    float top = -INFINITY, l = 0.f;
+    for (int c = lane; c < n; c += 32) {
+      const float m = __ldcg(part(c) + r * 2);
+      fs[c * rows + r] = m;
+      top = fmaxf(top, m);
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+    for (int c = lane; c < n; c += 32) {
+      const float m = fs[c * rows + r];
+      // NaN sums pass on: a NaN row has m = -inf and its l as it is.
+      const float f = m == -INFINITY ? 1.f : ex2_approx(m - top);
+      fs[c * rows + r] = f;
+      l += __ldcg(part(c) + r * 2 + 1) * f;
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+    if (lane == 0) s_l[r] = l;
+  }
+  __syncthreads();
+  const int group = tid / elems, e = (blockIdx.y * elems + tid % elems) * 4, r = e / D;
+  const int from = n * group / groups, to = n * (group + 1) / groups;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  // Eight loads at a time: a chain of single ones would take 0.5 us each.
+  for (int c = from; c < to; c += 8) {
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c + k < to) v[k] = __ldcg(reinterpret_cast<const float4*>(part(c + k) + 2 * rows + e));
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c + k < to) {
+        const float f = fs[(c + k) * rows + r];
+        o.x = fmaf(v[k].x, f, o.x);
+        o.y = fmaf(v[k].y, f, o.y);
+        o.z = fmaf(v[k].z, f, o.z);
+        o.w = fmaf(v[k].w, f, o.w);
+      }
+  }
+  s_o[group][tid % elems] = o;
+  __syncthreads();
+  if (group > 0) return;
+#pragma unroll
+  for (int k = 1; k < groups; ++k) {
+    const float4 v = s_o[k][tid];
+    o.x += v.x;
+    o.y += v.y;
+    o.z += v.z;
+    o.w += v.w;
+  }
+  const int G = p.Hq / p.Hk;
+  const RowsOut out = {p.o, next.first, next.it.row0, min(rows, next.len * G - next.it.row0), G, p.Hq, next.head};
+  put_row4<D>(out, r, e % D, o, s_l[r]);
+}
+
 template <int D, int QM>
 gdn_status_t launch_split(const Args& a, cudaStream_t st) {
   static const cudaError_t set = cudaFuncSetAttribute(
@@ -861,8 +887,12 @@ gdn_status_t launch_split(const Args& a, cudaStream_t st) {
     set_cuda_error(cudaErrorInvalidValue);
     return GDN_ERR_CUDA;
   }
-  return check_launch(launch_pdl(attn_split_kernel<D, QM>, dim3(a.split_grid), dim3(kWarps * 32),
-                                 Cfg<D, QM>::total, st, a, k_map, v_map));
+  const gdn_status_t rc = check_launch(launch_pdl(attn_split_kernel<D, QM>, dim3(a.split_grid),
+                                                  dim3(kWarps * 32), Cfg<D, QM>::total, st, a, k_map,
+                                                  v_map));
+  if (rc != GDN_OK) return rc;
+  return check_launch(launch_pdl(attn_split_join_kernel<D, QM>, dim3(a.split_grid, kJoinCols),
+                                 dim3(256), 0, st, a));
 }
 
 }  // namespace
@@ -887,7 +917,6 @@ gdn_status_t launch_attn_plan(const int32_t* cu, const int32_t* kv, int N, int T
                reinterpret_cast<Item*>(ws + l.items), reinterpret_cast<Start*>(ws + l.starts)};
   p.list[1] = {l.tile_rows, kTileKeys, limit, 0x7fffffff, l.tile_cap, use.tile ? tile_grid() : 0, 1,
                reinterpret_cast<Item*>(ws + l.tiles), reinterpret_cast<Start*>(ws + l.tile_starts)};
-  p.counters = reinterpret_cast<int*>(ws + l.counters);
   return check_launch(launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p));
 }
 
