@@ -266,7 +266,7 @@ gdn_status_t gdn_paged_attention(const void* q, int64_t q_stride, const void* k_
   a.starts = reinterpret_cast<const attn::Start*>(ws + l.starts);
   a.tile_starts = reinterpret_cast<const attn::Start*>(ws + l.tile_starts);
   a.split_rows = l.split_rows;
-  a.split_grid = attn::split_grid(d);
+  a.split_grid = attn::split_grid(d, l.split_rows);
   a.tile_grid = attn::tile_grid();
   a.tile_partials = reinterpret_cast<float*>(ws + l.tile_partials);
   // The two kernels share a step's sequences by their rows; a step whose

@@ -57,10 +57,10 @@ inline Kernels kernels_of(int N, int T, int G, int max_new_tokens) {
 // Rows of a split tile: 16 where the query heads of a token need more than 8.
 inline int split_rows(int G) { return G > 8 ? 16 : 8; }
 
-// CTAs of the split kernel: one wave, by the shared memory of its rings.
+// CTAs of the split kernel: one wave.
 constexpr int kSplitGridMax = 320;
-inline int split_grid(int d) {
-  const int n = num_sms() * (d == 256 ? 1 : 2);
+inline int split_grid(int d, int rows) {
+  const int n = num_sms() * (d * rows <= 8 * 128 ? 2 : 1);
   return n < kSplitGridMax ? n : kSplitGridMax;
 }
 

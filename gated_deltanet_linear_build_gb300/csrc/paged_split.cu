@@ -277,11 +277,18 @@ constexpr int kJoinCols = 4;             // CTAs that share the elements of a jo
 template <int D, int QM>
 struct Cfg {
   static constexpr int rows = 8 * QM;
-  static constexpr int slots = 3;                      // half units (K or V) in a warp's ring
+  // CTAs per SM, by registers: 128 a thread hold O of 8 rows up to d = 128 and of
+  // 16 up to d = 64; the others have the SM to themselves.
+  static constexpr int ctas = D * QM <= 128 ? 2 : 1;
+  static constexpr int slots = D == 128 && QM == 2 ? 6 : 3;   // half units (K or V) in a warp's ring
+  // Q's fragments, 64 registers at d x rows = 256 x 16, are read from shared
+  // memory there (rows 64 bytes off a bank line: two rows x four chunks at once).
+  static constexpr bool q_in_regs = D * QM <= 256;
+  static constexpr int q_pitch = 2 * D + 64;
   static constexpr int slot_bytes = kUnit * D;
   static constexpr int row = box_row(D), boxes = D / row;
   static constexpr int ring = kWarps * slots * slot_bytes;
-  static constexpr int q_bytes = rows * 2 * D;         // hi | lo codes of each row
+  static constexpr int q_bytes = rows * q_pitch;       // hi | lo codes of each row
   static constexpr int o_pitch = D + 4;                // of a row of O while the warps join
   static_assert(kWarps * rows * o_pitch * 4 <= ring, "the warps' O fits the rings");
   // ring | Q | Q row scales | m, l and factor of each warp's rows | joined m, l |
@@ -357,7 +364,7 @@ __device__ __noinline__ bool take_nans(unsigned char* slot, int* first_nan, int 
 }
 
 template <int D, int QM>
-__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
+__global__ void __launch_bounds__(kWarps * 32, Cfg<D, QM>::ctas)
 attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map) {
   using C = Cfg<D, QM>;
@@ -387,7 +394,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
   pdl_wait();
   pdl_trigger();
   const Start start = read_start(p.starts + blockIdx.x);
-  const int num_items = start.num_items, units1 = start.units, per_cta = start.per_cta;
+  const int num_items = start.num_items, units1 = start.units;
   long long u = start.u;
   const long long u_end = start.u_end;
   int lo = start.item, head = start.head;
@@ -411,9 +418,11 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       return i < mine && key < key_end ? __ldg(table + (key >> p.log_b)) : -1;
     };
     int blk = -1, blk_next = block_of(0);
-    // Lane l & 3 of the unit being copied: K's scale of its halves, V's.
-    float sc_next = 0.f;
-    auto issue = [&](int h) {
+    // Scales of the units being copied, in order: lane l & 3 holds K's of the unit's
+    // two halves and V's.
+    constexpr int kAhead = C::slots / 2;
+    float sc_q[kAhead];
+    auto issue = [&](int h, int q) {
       const int i = h >> 1, is_v = h & 1;
       if (i >= mine || dead) return;
       const int key0 = (first_unit + w + i * kWarps) * kUnit;
@@ -422,10 +431,10 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         blk_next = block_of(i + 1);
         const int half = lane & 1;
         const int b = __shfl_sync(0xffffffffu, blk, pages == 2 ? half : 0);
-        sc_next = 1.f;
+        sc_q[q] = 1.f;
         if (key0 + half * 16 < key_end) {
           if ((unsigned)b < (unsigned)p.num_blocks)
-            sc_next = __ldg(((lane & 2) ? p.vs : p.ks) + (size_t)b * p.Hk + head);
+            sc_q[q] = __ldg(((lane & 2) ? p.vs : p.ks) + (size_t)b * p.Hk + head);
           else
             record_device_status(GDN_ERR_INVALID_ARG);
         }
@@ -451,7 +460,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       return ring + st * C::slot_bytes;
     };
 #pragma unroll
-    for (int h = 0; h < C::slots - 1; ++h) issue(h);
+    for (int h = 0; h < C::slots - 1; ++h) issue(h, h >> 1);
 
     for (int i = tid; i < D; i += kWarps * 32) s_nan[i] = 0x7fffffff;
     if (tid == 0) s_flag[1] = 0;
@@ -495,8 +504,8 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&f));
         const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(a - hf.x, b - hf.y),
                                                      __NV_SATFINITE, __NV_E4M3);
-        *reinterpret_cast<uint16_t*>(s_q + r * 2 * D + lane * per + i) = (uint16_t)h2;
-        *reinterpret_cast<uint16_t*>(s_q + r * 2 * D + D + lane * per + i) = (uint16_t)l2;
+        *reinterpret_cast<uint16_t*>(s_q + r * C::q_pitch + lane * per + i) = (uint16_t)h2;
+        *reinterpret_cast<uint16_t*>(s_q + r * C::q_pitch + D + lane * per + i) = (uint16_t)l2;
       }
       // A row with an infinity or NaN has no finite softmax: its scores are NaN.
       if (lane == 0)
@@ -504,22 +513,20 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
     }
     __syncthreads();
 
-    // ---- Q fragments: k index (t4, i) of step s <-> the K chunk layout below ---
-    uint32_t qf[QM][D / 32][4];
+    // ---- Q fragments: chunk t4 + 4 c of a row, hi and lo, as K's chunks below -----
+    uint4 qf[C::q_in_regs ? QM : 1][C::q_in_regs ? D / 64 : 1][2];
     float rs[QM];
     int lim[QM];
     int min_lim = 0x7fffffff;
 #pragma unroll
     for (int m = 0; m < QM; ++m) {
+      if constexpr (C::q_in_regs) {
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        const unsigned char* at = s_q + (m * 8 + g) * 2 * D + 16 * (t4 + 4 * (k >> 1)) + 8 * (k & 1);
-        const uint2 h2 = *reinterpret_cast<const uint2*>(at);
-        const uint2 l2 = *reinterpret_cast<const uint2*>(at + D);
-        qf[m][k][0] = h2.x;
-        qf[m][k][1] = l2.x;
-        qf[m][k][2] = h2.y;
-        qf[m][k][3] = l2.y;
+        for (int c = 0; c < D / 64; ++c) {
+          const unsigned char* at = s_q + (m * 8 + g) * C::q_pitch + 16 * (t4 + 4 * c);
+          qf[m][c][0] = *reinterpret_cast<const uint4*>(at);
+          qf[m][c][1] = *reinterpret_cast<const uint4*>(at + D);
+        }
       }
       rs[m] = s_qs[m * 8 + g] * p.scale_log2;
       const int r = m * 8 + g;
@@ -547,46 +554,64 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       float ksc[2], lvs[2], ivs[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        ksc[k] = __shfl_sync(0xffffffffu, sc_next, k);
-        const float v = fmaxf(__shfl_sync(0xffffffffu, sc_next, 2 + k), 7.888609052210118e-31f);   // 2^-100
+        ksc[k] = __shfl_sync(0xffffffffu, sc_q[0], k);
+        const float v = fmaxf(__shfl_sync(0xffffffffu, sc_q[0], 2 + k), 7.888609052210118e-31f);   // 2^-100
         lvs[k] = lg2_approx(v);
         ivs[k] = __fdividef(1.f, v);
       }
+#pragma unroll
+      for (int k = 0; k + 1 < kAhead; ++k) sc_q[k] = sc_q[k + 1];
       // K of unit i has landed, and the slot before it is free again.
       float sc[QM][4][2];
       {
         const unsigned char* slot = take();
-        issue(2 * i + C::slots - 1);
+        issue(2 * i + C::slots - 1, kAhead - 1);
+        float c4[QM][4][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float c4[QM][4];
+        for (int m = 0; m < QM; ++m)
 #pragma unroll
-          for (int m = 0; m < QM; ++m)
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) c4[m][c] = 0.f;
-          const int r = 8 * j + key_of<D>(g);
+            for (int c = 0; c < 4; ++c) c4[m][j][c] = 0.f;
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
+        for (int c = 0; c < D / 64; ++c) {
+          uint4 qh[QM], ql[QM];
+          if constexpr (!C::q_in_regs) {
+#pragma unroll
+            for (int m = 0; m < QM; ++m) {
+              const unsigned char* at = s_q + (m * 8 + g) * C::q_pitch + 16 * (t4 + 4 * c);
+              qh[m] = *reinterpret_cast<const uint4*>(at);
+              ql[m] = *reinterpret_cast<const uint4*>(at + D);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = 8 * j + key_of<D>(g);
             const uint4 kk = *reinterpret_cast<const uint4*>(
                 slot + (c >> 1) * (kUnit * C::row) + swizzled<C::row>(r, t4 + 4 * (c & 1)));
 #pragma unroll
             for (int m = 0; m < QM; ++m) {
-              mma_e4m3(c4[m], qf[m][2 * c][0], qf[m][2 * c][1], qf[m][2 * c][2], qf[m][2 * c][3],
-                       kk.x, kk.y);
-              mma_e4m3(c4[m], qf[m][2 * c + 1][0], qf[m][2 * c + 1][1], qf[m][2 * c + 1][2],
-                       qf[m][2 * c + 1][3], kk.z, kk.w);
+              if constexpr (C::q_in_regs) {
+                mma_e4m3(c4[m][j], qf[m][c][0].x, qf[m][c][1].x, qf[m][c][0].y, qf[m][c][1].y, kk.x, kk.y);
+                mma_e4m3(c4[m][j], qf[m][c][0].z, qf[m][c][1].z, qf[m][c][0].w, qf[m][c][1].w, kk.z, kk.w);
+              } else {
+                mma_e4m3(c4[m][j], qh[m].x, ql[m].x, qh[m].y, ql[m].y, kk.x, kk.y);
+                mma_e4m3(c4[m][j], qh[m].z, ql[m].z, qh[m].w, ql[m].w, kk.z, kk.w);
+              }
             }
           }
-#pragma unroll
-          for (int m = 0; m < QM; ++m) {
-            sc[m][j][0] = c4[m][0] + c4[m][2];
-            sc[m][j][1] = c4[m][1] + c4[m][3];
-          }
         }
+#pragma unroll
+        for (int m = 0; m < QM; ++m)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sc[m][j][0] = c4[m][j][0] + c4[m][j][2];
+            sc[m][j][1] = c4[m][j][1] + c4[m][j][3];
+          }
       }
       __syncwarp();
       unsigned char* slot = take();                      // V of unit i
-      issue(2 * i + C::slots);
+      issue(2 * i + C::slots, kAhead - 1);
       const bool cut = unit * kUnit + kUnit > min_lim;
       // Keys past the end hold stale bytes: zeros instead.
       if (unit * kUnit + kUnit > key_end) {
@@ -913,7 +938,7 @@ gdn_status_t launch_attn_plan(const int32_t* cu, const int32_t* kv, int N, int T
   p.Hk = Hk;
   p.kv_max = kv_max;
   // A piece of the split kernel gives each of its 8 warps a unit at least.
-  p.list[0] = {l.split_rows, kUnit, 0, limit, l.item_cap, use.split ? split_grid(d) : 0, kWarps,
+  p.list[0] = {l.split_rows, kUnit, 0, limit, l.item_cap, use.split ? split_grid(d, l.split_rows) : 0, kWarps,
                reinterpret_cast<Item*>(ws + l.items), reinterpret_cast<Start*>(ws + l.starts)};
   p.list[1] = {l.tile_rows, kTileKeys, limit, 0x7fffffff, l.tile_cap, use.tile ? tile_grid() : 0, 1,
                reinterpret_cast<Item*>(ws + l.tiles), reinterpret_cast<Start*>(ws + l.tile_starts)};
