@@ -263,6 +263,7 @@ gdn_status_t gdn_paged_attention(const void* q, int64_t q_stride, const void* k_
   a.items = reinterpret_cast<attn::Item*>(ws + l.items);
   a.partials = reinterpret_cast<float*>(ws + l.partials);
   a.tiles = reinterpret_cast<attn::Item*>(ws + l.tiles);
+  a.sorted_tiles = reinterpret_cast<attn::Item*>(ws + l.sorted_tiles);
   a.starts = reinterpret_cast<const attn::Start*>(ws + l.starts);
   a.tile_starts = reinterpret_cast<const attn::Start*>(ws + l.tile_starts);
   a.split_rows = l.split_rows;

@@ -28,12 +28,12 @@ constexpr int kTileKeys = 64;         // keys per unit of the tensor-core kernel
 struct alignas(64) Start {
   int item, head, num_items, units;   // of unit u; of the list: tiles, one head's units
   Item it;
-  int first, len, kv, per_cta;        // the item's sequence; units per CTA
+  int first, len, kv, per_cta;        // the item's sequence; units per CTA (0: whole items)
   long long u, u_end;
 };
 
 struct Layout {
-  size_t starts, tile_starts, items, partials, tiles, tile_partials, total;
+  size_t starts, tile_starts, items, partials, tiles, sorted_tiles, tile_partials, total;
   int item_cap, tile_cap, split_rows, tile_rows;
 };
 
@@ -106,7 +106,7 @@ struct Args {
   float scale_log2;                    // softmax scale x log2 e
   Item* items;
   float* partials;
-  Item* tiles;
+  Item *tiles, *sorted_tiles;          // in sequence order; by length
   int split_rows, split_grid, tile_grid;
   const Start *starts, *tile_starts;
   float* tile_partials;

@@ -21,7 +21,8 @@
 //   - m), with P' / vs in the sum, per 16 keys (the smallest block). O is
 //   rescaled only when a row's maximum grows by more than 2^8.
 //
-// Work split: as in the split kernel, all (tile, kv head, 64 keys) units form
+// Work split: where items are many or alike enough, whole items are dealt out by
+// length (the plan compares the two). Otherwise, as in the split kernel, all (tile, kv head, 64 keys) units form
 // one line cut into equal pieces, one per SM; a tile cut by the end of a piece
 // leaves float32 partial results, which a second kernel joins in CTA order.
 //
@@ -173,9 +174,10 @@ struct Seg {
   int n_rows, key_end;
 };
 
-// This CTA's piece of the work line; lo, head, it and s are those of its next unit.
+// This CTA's work: a piece of the line of units (lo, head, it and s are those of
+// its next unit), or whole items dealt out from the list sorted by length.
 struct Line {
-  int num, units1, lo, head;
+  int num, units1, lo, head, deal;     // deal: round of the dealing, -1 for a piece
   Item it;
   Seq s;
   long long u, u_end;
@@ -189,6 +191,7 @@ __device__ __forceinline__ Line line_of(const Args& p) {
   l.units1 = at.units;
   l.lo = at.item;
   l.head = at.head;
+  l.deal = at.per_cta == 0 ? 0 : -1;
   l.it = at.it;
   l.s = {at.first, at.len, at.kv};
   l.u = at.u;
@@ -202,8 +205,8 @@ __device__ __forceinline__ Seg seg_at(const Args& p, const Line& l, int tile_row
   g.row0 = l.it.row0;
   g.n_units = l.it.units;
   g.cum = l.it.cum;
-  g.first_unit = (int)(l.u - (long long)l.head * l.units1) - g.cum;
-  g.count = (int)min((long long)(g.n_units - g.first_unit), l.u_end - l.u);
+  g.first_unit = l.deal >= 0 ? 0 : (int)(l.u - (long long)l.head * l.units1) - g.cum;
+  g.count = l.deal >= 0 ? g.n_units : (int)min((long long)(g.n_units - g.first_unit), l.u_end - l.u);
   g.s = l.s;
   const int G = p.Hq / p.Hk;
   g.n_rows = min(tile_rows, g.s.len * G - g.row0);
@@ -212,16 +215,63 @@ __device__ __forceinline__ Seg seg_at(const Args& p, const Line& l, int tile_row
 }
 
 __device__ __forceinline__ void pass(const Args& p, Line& l, const Seg& g) {
-  l.u += g.count;
-  if (g.first_unit + g.count == g.n_units && ++l.lo == l.num) {
-    l.lo = 0;
-    ++l.head;
+  const Item* from = p.tiles;
+  if (l.deal >= 0) {
+    // Back and forth over the CTAs: the longest with the shortest.
+    ++l.deal;
+    ++l.u;
+    const int grid = gridDim.x, c = blockIdx.x;
+    const int at = l.deal * grid + ((l.deal & 1) ? grid - 1 - c : c);
+    l.lo = at / p.Hk;
+    l.head = at - l.lo * p.Hk;
+    from = p.sorted_tiles;
+  } else {
+    l.u += g.count;
+    if (g.first_unit + g.count == g.n_units && ++l.lo == l.num) {
+      l.lo = 0;
+      ++l.head;
+    }
   }
   if (l.more()) {
-    const int4 raw = __ldg(reinterpret_cast<const int4*>(p.tiles) + l.lo);
+    const int4 raw = __ldg(reinterpret_cast<const int4*>(from) + l.lo);
     l.it = {raw.x, raw.y, raw.z, raw.w};
     l.s = seq_of(p.cu, p.kv, l.it.seq, p.T, (int64_t)p.max_blocks << p.log_b);
   }
+}
+
+// One 32-byte store of 16 BF16 values (or two of 16 bytes where o is not aligned
+// for it): a row's sectors are written whole.
+__device__ __forceinline__ void store16(__nv_bfloat16* at, const float* v, bool wide) {
+  const uint4 a = pack8(v), b = pack8(v + 8);
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(at), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z),
+                    "r"(b.w) : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(at) = a;
+    *reinterpret_cast<uint4*>(at + 8) = b;
+  }
+}
+
+// The NaNs of 16 codes of V taken out, and the first key of each of their columns
+// kept. (Out of line: few units need it.)
+__device__ __noinline__ uint4 take_nans(uint4 v, unsigned short* first_nan, int key) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b)
+      if (((w[k] >> (8 * b)) & 0x7fu) == 0x7fu) {
+        unsigned short* at = first_nan + k * 4 + b;
+        unsigned short old = *reinterpret_cast<volatile unsigned short*>(at);
+        while ((unsigned short)key < old) {
+          const unsigned short was = atomicCAS(at, old, (unsigned short)key);
+          if (was == old) break;
+          old = was;
+        }
+        w[k] &= ~(0xffu << (8 * b));
+      }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <int D>
@@ -457,71 +507,70 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       const Seg g = seg_at(p, l, kRows);
       // ---- Q: hi and lo codes, one power-of-two scale per row ---------------------
       // 8 rows at a time, 4 lanes to 64 bytes of a row, so that loads use whole
-      // sectors and the stores fill the core matrices in order.
+      // sectors and the stores fill the core matrices in order. The next 8 rows are
+      // on their way meanwhile. (A loop of small body: straight code that runs once
+      // a segment is paid in instruction fetches.)
       {
-        constexpr int passes = D / 32, at_once = 64 / passes / 4;   // 16 loads in flight
+        constexpr int passes = D / 32;
         constexpr int groups = kRows / 8 / (C::loaders / 32);       // of 8 rows, per warp
-        static_assert(groups % at_once == 0, "groups of rows");
         const int rr = lane & 7, cq = lane >> 3;
         const float neg = p.scale_log2 < 0.f ? -1.f : 1.f;
+        auto fetch = [&](int a, uint4 (&w)[passes]) {
+          const int local = ((dt >> 5) * groups + a) * 8 + rr;
+          const int qrow = g.row0 + local, qt = qrow / G;
+          const __nv_bfloat16* src = p.q + (int64_t)(g.s.first + qt) * p.q_stride +
+                                     (int64_t)(l.head * G + qrow - qt * G) * D + cq * 8;
+#pragma unroll
+          for (int k = 0; k < passes; ++k)
+            w[k] = local < g.n_rows ? ldg16(src + k * 32) : make_uint4(0, 0, 0, 0);
+        };
+        uint4 w[passes], ahead[passes];
+        fetch(0, ahead);
+        // The last scores of the segment before are done with Q's place.
+        if (unit > 0) ok = ok && warp_wait(k_empty + (unit - 1) % C::KS, ((unit - 1) / C::KS) & 1, s_abort);
 #pragma unroll 1
-        for (int g0 = 0; g0 < groups; g0 += at_once) {
-          uint4 w[at_once][passes];
+        for (int a = 0; ok && a < groups; ++a) {
 #pragma unroll
-          for (int a = 0; a < at_once; ++a) {
-            const int local = ((dt >> 5) * groups + g0 + a) * 8 + rr;
-            const int qrow = g.row0 + local, qt = qrow / G;
-            const __nv_bfloat16* src = p.q + (int64_t)(g.s.first + qt) * p.q_stride +
-                                       (int64_t)(l.head * G + qrow - qt * G) * D + cq * 8;
+          for (int k = 0; k < passes; ++k) w[k] = ahead[k];
+          if (a + 1 < groups) fetch(a + 1, ahead);
+          const int local = ((dt >> 5) * groups + a) * 8 + rr;
+          uint32_t top = 0;                          // largest magnitude, as bits
 #pragma unroll
-            for (int k = 0; k < passes; ++k)
-              w[a][k] = local < g.n_rows ? ldg16(src + k * 32) : make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < passes; ++k) {
+            const uint32_t v[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              top = max(top, max((v[i] & 0x7fffu) << 16, v[i] & 0x7fff0000u));
           }
-          if (g0 == 0 && unit > 0) {
-            // The last scores of the segment before are done with Q's place.
-            ok = ok && warp_wait(k_empty + (unit - 1) % C::KS, ((unit - 1) / C::KS) & 1, s_abort);
-            if (!ok) break;
-          }
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          // The row's largest magnitude goes to [128, 256). A row with an infinity
+          // or NaN is zeros here, and marked by the exponent -128.
+          const bool bad = top >= 0x7f800000u;
+          const int ex = min(max((int)(top >> 23) - 127 - 7, -126), 126);
+          const float inv = neg * __int_as_float((127 - ex) << 23);
+          if (cq == 0) s_ex[(seg & 1) * kRows + local] = (signed char)(bad ? -128 : ex);
+          unsigned char* hi = smem + C::o_q + (local >> 7) * 2 * C::q_part +
+                              ((local & 127) >> 3) * (D * 8) + rr * 16 + (cq & 1) * 8 +
+                              (cq >> 1) * 128;
 #pragma unroll
-          for (int a = 0; a < at_once; ++a) {
-            const int local = ((dt >> 5) * groups + g0 + a) * 8 + rr;
-            uint32_t top = 0;                          // largest magnitude, as bits
+          for (int k = 0; k < passes; ++k) {
+            const uint32_t v[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+            uint32_t h4[2] = {0, 0}, l4[2] = {0, 0};
 #pragma unroll
-            for (int k = 0; k < passes; ++k) {
-              const uint32_t v[4] = {w[a][k].x, w[a][k].y, w[a][k].z, w[a][k].w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                top = max(top, max((v[i] & 0x7fffu) << 16, v[i] & 0x7fff0000u));
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t x = bad ? 0u : v[i];
+              const float x0 = bf16lo(x) * inv, x1 = bf16hi(x) * inv;
+              const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+              const uint32_t f = e4m3x2_half2(h2);
+              const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&f));
+              const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(x0 - hf.x, x1 - hf.y),
+                                                           __NV_SATFINITE, __NV_E4M3);
+              h4[i >> 1] |= h2 << (16 * (i & 1));
+              l4[i >> 1] |= l2 << (16 * (i & 1));
             }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            // The row's largest magnitude goes to [128, 256). A row with an infinity
-            // or NaN is zeros here, and marked by the exponent -128.
-            const bool bad = top >= 0x7f800000u;
-            const int ex = min(max((int)(top >> 23) - 127 - 7, -126), 126);
-            const float inv = bad ? 0.f : neg * __int_as_float((127 - ex) << 23);
-            if (cq == 0) s_ex[(seg & 1) * kRows + local] = (signed char)(bad ? -128 : ex);
-            unsigned char* hi = smem + C::o_q + (local >> 7) * 2 * C::q_part +
-                                ((local & 127) >> 3) * (D * 8) + rr * 16 + (cq & 1) * 8 +
-                                (cq >> 1) * 128;
-#pragma unroll
-            for (int k = 0; k < passes; ++k) {
-              const uint32_t v[4] = {w[a][k].x, w[a][k].y, w[a][k].z, w[a][k].w};
-              uint32_t h4[2] = {0, 0}, l4[2] = {0, 0};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float x0 = bad ? 0.f : bf16lo(v[i]) * inv, x1 = bad ? 0.f : bf16hi(v[i]) * inv;
-                const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t f = e4m3x2_half2(h2);
-                const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&f));
-                const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(x0 - hf.x, x1 - hf.y),
-                                                             __NV_SATFINITE, __NV_E4M3);
-                h4[i >> 1] |= h2 << (16 * (i & 1));
-                l4[i >> 1] |= l2 << (16 * (i & 1));
-              }
-              *reinterpret_cast<uint2*>(hi + k * 256) = make_uint2(h4[0], h4[1]);
-              *reinterpret_cast<uint2*>(hi + C::q_part + k * 256) = make_uint2(l4[0], l4[1]);
-            }
+            *reinterpret_cast<uint2*>(hi + k * 256) = make_uint2(h4[0], h4[1]);
+            *reinterpret_cast<uint2*>(hi + C::q_part + k * 256) = make_uint2(l4[0], l4[1]);
           }
         }
         if (!ok) break;
@@ -557,31 +606,19 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         // NaN is NaN): a NaN of V is written as zero and kept as the first key
         // whose column has one.
         if (key0 > nan_base) {
+          uint32_t any = 0;
 #pragma unroll
           for (int it = 0; it < v_it; ++it) {
-            const int r = (it * rg_per + rg_in) * 8 + r_in;
-            uint32_t w[4] = {raw[it].x, raw[it].y, raw[it].z, raw[it].w};
-            const bool past = key0 + r >= g.key_end;
+            if (key0 + (it * rg_per + rg_in) * 8 + r_in >= g.key_end) raw[it] = make_uint4(0, 0, 0, 0);
+            any |= ((raw[it].x & 0x7f7f7f7fu) + 0x01010101u) | ((raw[it].y & 0x7f7f7f7fu) + 0x01010101u) |
+                   ((raw[it].z & 0x7f7f7f7fu) + 0x01010101u) | ((raw[it].w & 0x7f7f7f7fu) + 0x01010101u);
+          }
+          if ((any & 0x80808080u) != 0) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (past) w[k] = 0;
-              if ((((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0) {
-                for (int b = 0; b < 4; ++b)
-                  if (((w[k] >> (8 * b)) & 0x7fu) == 0x7fu) {
-                    unsigned short* at = first_nan + c * 16 + k * 4 + b;
-                    const unsigned short key = (unsigned short)(key0 + r - nan_base);
-                    unsigned short old = *reinterpret_cast<volatile unsigned short*>(at);
-                    while (key < old) {
-                      const unsigned short was = atomicCAS(at, old, key);
-                      if (was == old) break;
-                      old = was;
-                    }
-                    *s_any_nan = 1;
-                    w[k] &= ~(0xffu << (8 * b));
-                  }
-              }
-            }
-            raw[it] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int it = 0; it < v_it; ++it)
+              raw[it] = take_nans(raw[it], first_nan + c * 16,
+                                  key0 + (it * rg_per + rg_in) * 8 + r_in - nan_base);
+            *s_any_nan = 1;
           }
         }
         tc::mbar_arrive(vr_empty + sr);
@@ -712,6 +749,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       const uint32_t to = tmem + lane_base + C::c_o(m);
       const bool whole = g.count == g.n_units;
       __nv_bfloat16* out = p.o + ((int64_t)(g.s.first + tok) * p.Hq + hq) * D;
+      const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
       const float il = l_run == 0.f ? 0.f : 1.f / l_run;
       const size_t part_sz = (size_t)(D + 2) * 128;
       float* part = p.tile_partials +
@@ -732,8 +770,8 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
           if (live) {
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] *= il;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(out + c + 8 * k) = pack8(v + 8 * k);
+            store16(out + c, v, wide);
+            store16(out + c + 16, v + 16, wide);
           }
         } else {
 #pragma unroll
@@ -769,7 +807,7 @@ __global__ void __launch_bounds__(256) attn_tile_join_kernel(const Args p) {
   const int col0 = (threadIdx.x >> 5) * kCols;
   if (c0 + 1 >= (int)gridDim.x) return;
   const Start next = read_start(p.tile_starts + c0 + 1);
-  if (next.u >= next.u_end) return;
+  if (next.per_cta == 0 || next.u >= next.u_end) return;    // whole items, or no work
   const long long at0 = (long long)next.head * next.units + next.it.cum;
   if (at0 == next.u || at0 / next.per_cta != c0) return;    // not cut here, or begun earlier
   const int c1 = (int)((at0 + next.it.units - 1) / next.per_cta);
