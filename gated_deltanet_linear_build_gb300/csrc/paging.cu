@@ -13,7 +13,8 @@
 // bandwidth. One launch: every CTA owns a contiguous slice of tokens and forms
 // the prefix sums it needs itself (one block-wide reduction over all earlier
 // sequences, which also gives the totals that decide whether the step fits),
-// instead of a scan kernel followed by a fill kernel.
+// instead of a scan kernel followed by a fill kernel. 4,000 sequences, 125,000
+// tokens: MEASURED_TABLES.
 #include <algorithm>
 
 #include "gdn_internal.cuh"
@@ -81,7 +82,7 @@ struct TabArgs {
 __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TabArgs p) {
   __shared__ int2 warp_sums[kTabThreads / 32];
   __shared__ int s_cu[kTabSeqs + 1], s_ctx[kTabSeqs], s_need[kTabSeqs], s_piece[kTabSeqs];
-  __shared__ int s_lo, s_bad;
+  __shared__ int s_sum[6];             // first sequence, needs and pieces before it, of all, errors
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
@@ -89,38 +90,39 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TabArgs
   const int per = (p.T + gridDim.x - 1) / gridDim.x;
   const int t0 = min(p.T, (int)blockIdx.x * per), t1 = min(p.T, t0 + per);
 
-  // First sequence with tokens past t0 (the slice's first one).
-  if (tid == 0) {
-    int lo = 0, hi = p.N;              // largest n with cu[n] <= t0 ends the search
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(p.cu + mid + 1) <= t0) lo = mid + 1; else hi = mid;
-    }
-    s_lo = lo;
-    s_bad = 0;
-  }
+  if (tid < 6) s_sum[tid] = 0;
   __syncthreads();
-  const int n0 = s_lo;
-
-  // Needs and pieces of the sequences before n0, and of all.
-  int2 before = make_int2(0, 0), all = make_int2(0, 0);
-  int bad = 0;
+  // Needs and pieces of the sequences that end at or before t0, and of all; the
+  // former are those before the slice's first sequence.
+  int first = 0, need_b = 0, pcs_b = 0, need_a = 0, pcs_a = 0, bad = 0;
+#pragma unroll 4
   for (int n = tid; n < p.N; n += kTabThreads) {
     const SeqLens s = seq_lens(p.cu, p.ctx, n, p.T, bad);
     const int have = (s.ctx + B - 1) >> p.log_b, want = (s.ctx + s.len + B - 1) >> p.log_b;
     const int need = want - have, pcs = s.len > 0 ? want - (s.ctx >> p.log_b) : 0;
     if (want > p.max_blocks && s.len > 0) bad |= 2;
-    all.x += need;
-    all.y += pcs;
-    if (n < n0) { before.x += need; before.y += pcs; }
+    need_a += need;
+    pcs_a += pcs;
+    if (s.first + s.len <= t0) {
+      ++first;
+      need_b += need;
+      pcs_b += pcs;
+    }
   }
   if (tid == 0 && (__ldg(p.cu) != 0 || __ldg(p.cu + p.N) != p.T)) bad |= 1;
-  if (bad) atomicOr(&s_bad, bad);
-  int2 tot_before, tot_all;
-  block_scan2(before, warp_sums, tot_before);
-  block_scan2(all, warp_sums, tot_all);
+  const int sums[6] = {first, need_b, pcs_b, need_a, pcs_a, bad};
+#pragma unroll
+  for (int k = 0; k < 6; ++k) {
+    const int v = k < 5 ? __reduce_add_sync(0xffffffffu, sums[k]) : __reduce_or_sync(0xffffffffu, sums[k]);
+    if ((tid & 31) == k) {
+      if (k < 5) atomicAdd(s_sum + k, v);
+      else atomicOr(s_sum + k, v);
+    }
+  }
   __syncthreads();
-  int err = s_bad;
+  const int n0 = s_sum[0];
+  const int2 tot_before = make_int2(s_sum[1], s_sum[2]), tot_all = make_int2(s_sum[3], s_sum[4]);
+  int err = s_sum[5];
   if (tot_all.x > p.num_free || tot_all.y > p.piece_cap) err |= 2;
   const int status = (err & 1) ? GDN_ERR_INVALID_ARG : err ? GDN_ERR_WORKSPACE : GDN_OK;
   if (blockIdx.x == 0 && tid == 0) {

@@ -152,9 +152,10 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotArgs p) {
 // ---------------------------------------------------------------------------
 // Append to the cache.
 //
-// One CTA per (page piece, head, K or V): a block of at most 128 tokens x 256
-// values is held in registers between the reduction that gives its scale and
-// the rounding, so k and v are read once. The scale is the smallest power of
+// One CTA per (page piece, heads, K or V): 32 KB of them (64 KB where one head of
+// a block is that much) are held in registers between the reduction that gives
+// the scales and the rounding, so k and v are read once, and enough bytes are
+// in flight per SM; a token's sines serve all heads of the unit. The scale is the smallest power of
 // two that brings the largest finite magnitude of the piece within 448 (for a
 // rotated k with the headroom of the rotation, so that it follows from the
 // inputs' exponents alone and no rounding can move it). Powers of two cost an
@@ -168,10 +169,10 @@ struct AppendArgs {
   int64_t k_stride, v_stride;
   const gdn_page_piece_t* pieces;
   const int32_t* num_pieces;
-  int piece_cap, Hk, log_b, num_blocks, k_grow;
+  int piece_cap, Hk, hg, head_groups, log_b, num_blocks, k_grow;
   uint8_t *kc, *vc;
   float *ks, *vs;
-  int q_ctas;
+  int kv_ctas;
 };
 
 constexpr int kMinExp = -100;           // smallest exponent of a scale
@@ -200,23 +201,33 @@ __device__ __forceinline__ float e4m3_value(uint32_t code) {
   return __half2float(__half(h));
 }
 
-// Largest finite magnitude of 8 BF16 values.
-__device__ __forceinline__ float finite_max8(const uint4& u, float m) {
-  float f[8];
-  unpack8(u, f);
+// Largest magnitude of 16 BF16 values, as float bits (NaN and infinities above
+// all); with `finite` they do not count.
+__device__ __forceinline__ uint32_t max_bits(const uint4& a, const uint4& b, uint32_t top, bool finite) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float x = fabsf(f[i]);
-    m = fmaxf(m, x <= 3.4e38f ? x : 0.f);          // NaN and infinities do not count
+    uint32_t lo = (w[i] << 16) & 0x7fff0000u, hi = w[i] & 0x7fff0000u;
+    if (finite) {
+      if (lo >= 0x7f800000u) lo = 0;
+      if (hi >= 0x7f800000u) hi = 0;
+    }
+    top = max(top, max(lo, hi));
   }
-  return m;
+  return top;
 }
 
+// One unit: a page piece, K or V, `hg` heads. Row r of the unit is token r % B of
+// head r / B; a thread's rows are 256 / J apart (J threads a row).
+constexpr int kMaxHeads = 64;           // of a unit: 4 passes of 256 threads, 16 tokens x 4 threads
 template <int kPasses>
-__device__ __forceinline__ void append_piece(const AppendArgs& p, int unit, float* red) {
+__device__ __forceinline__ void append_piece(const AppendArgs& p, int unit, uint32_t* s_top, float* s_old,
+                                             float* s_scale) {
   const int is_v = unit & 1;
   const int rest = unit >> 1;
-  const int head = rest % p.Hk, pi = rest / p.Hk;
+  const int grp = rest % p.head_groups, pi = rest / p.head_groups;
+  const int head0 = grp * p.hg, heads = min(p.hg, p.Hk - head0);
+  const int tid = threadIdx.x;
   if (pi >= __ldg(p.num_pieces)) return;
   const int4 pc = __ldg(reinterpret_cast<const int4*>(p.pieces) + pi);
   const int block = pc.x, first = pc.y, len = pc.z, off = pc.w;
@@ -225,84 +236,111 @@ __device__ __forceinline__ void append_piece(const AppendArgs& p, int unit, floa
       first + len > p.r.T)
     return;
   const int J = 1 << p.r.log_j, d = 16 << p.r.log_j;
-  const int j = threadIdx.x & (J - 1), row0 = threadIdx.x >> p.r.log_j;
+  const int j = tid & (J - 1), row0 = tid >> p.r.log_j;
   const int rows = kRotThreads >> p.r.log_j;
   const int rot = is_v ? 0 : p.r.rot;
   int oa, ob;
   unit_offsets(j, rot, p.r.interleaved, oa, ob);
   const __nv_bfloat16* src = (is_v ? p.v + (int64_t)first * p.v_stride
-                                   : p.k + (int64_t)first * p.k_stride) + head * d;
+                                   : p.k + (int64_t)first * p.k_stride) + head0 * d;
   const int64_t stride = is_v ? p.v_stride : p.k_stride;
+  float* scale_at = (is_v ? p.vs : p.ks) + (int64_t)block * p.Hk + head0;
   uint4 a[kPasses], b[kPasses];
-  float top = 0.f;
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
-    const int r = row0 + i * rows;
+    const int r = row0 + i * rows, t = r & (B - 1), h = r >> p.log_b;
     a[i] = b[i] = make_uint4(0, 0, 0, 0);
-    if (r < len) {
-      a[i] = ldg16(src + r * stride + oa);
-      b[i] = ldg16(src + r * stride + ob);
+    if (t < len && h < heads) {
+      const __nv_bfloat16* at = src + t * stride + h * d;
+      a[i] = ldg16(at + oa);
+      b[i] = ldg16(at + ob);
     }
   }
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) top = finite_max8(b[i], finite_max8(a[i], top));
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
-  float* scale_at = (is_v ? p.vs : p.ks) + (int64_t)block * p.Hk + head;
-  const float old = off > 0 ? *scale_at : 0.f;
+  if (tid < heads) {
+    s_top[tid] = 0;
+    s_old[tid] = off > 0 ? scale_at[tid] : 0.f;
+  }
   __syncthreads();
+  // A warp's rows of one pass lie in one head (at most 8 rows, 16 tokens).
+  auto reduce = [&](bool finite) {
 #pragma unroll
-  for (int i = 0; i < kRotThreads / 32; ++i) top = fmaxf(top, red[i]);
-  const int e = scale_exp(top, is_v ? 0 : p.k_grow);
-  const float scale = fmaxf(pow2i(min(e, 127)), old);
-  uint8_t* page = (is_v ? p.vc : p.kc) + ((int64_t)block * p.Hk + head) * ((int64_t)B * d);
-  if (off > 0 && scale != old) {
-    // The tokens that the block held, on the grown scale.
-    const float ratio = old / scale;
-    for (int i = threadIdx.x; i < off * d / 4; i += kRotThreads) {
-      uint32_t w = reinterpret_cast<uint32_t*>(page)[i], o = 0;
+    for (int i = 0; i < kPasses; ++i) {
+      const uint32_t top = __reduce_max_sync(0xffffffffu, max_bits(a[i], b[i], 0u, finite));
+      const int h = (row0 + i * rows) >> p.log_b;
+      if ((tid & 31) == 0 && h < heads) atomicMax(s_top + h, top);
+    }
+    __syncthreads();
+  };
+  reduce(false);
+  bool special = false;                  // an infinity or NaN: count the finite ones
+  for (int h = 0; h < heads; ++h) special |= s_top[h] >= 0x7f800000u;
+  if (special) {
+    __syncthreads();
+    if (tid < heads) s_top[tid] = 0;
+    __syncthreads();
+    reduce(true);
+  }
+  if (tid < heads) {
+    const int e = scale_exp(__uint_as_float(s_top[tid]), is_v ? 0 : p.k_grow);
+    const float scale = fmaxf(pow2i(min(e, 127)), s_old[tid]);
+    s_scale[tid] = scale;
+    scale_at[tid] = scale;
+  }
+  __syncthreads();
+  uint8_t* page = (is_v ? p.vc : p.kc) + ((int64_t)block * p.Hk + head0) * ((int64_t)B * d);
+  if (off > 0) {
+    // The tokens that the block held, on a scale that grew.
+    for (int h = 0; h < heads; ++h) {
+      if (s_scale[h] == s_old[h]) continue;
+      const float ratio = s_old[h] / s_scale[h];
+      uint32_t* held = reinterpret_cast<uint32_t*>(page + (int64_t)h * B * d);
+      for (int i = tid; i < off * d / 4; i += kRotThreads) {
+        uint32_t w = held[i], o = 0;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float x = e4m3_value((w >> (8 * c)) & 0xffu) * ratio;
-        o |= (uint32_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3) << (8 * c);
+        for (int c = 0; c < 4; ++c) {
+          const float x = e4m3_value((w >> (8 * c)) & 0xffu) * ratio;
+          o |= (uint32_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3) << (8 * c);
+        }
+        held[i] = o;
       }
-      reinterpret_cast<uint32_t*>(page)[i] = o;
     }
   }
-  if (threadIdx.x == 0) *scale_at = scale;
-  const float inv = 1.f / scale;
   const bool turn = j * 16 < rot;
   uint64_t ph[8];
+  float co[8], si[8];
+  int t_of = -1;                         // token that the sines are for
   if (turn) load_phases(p.r.phases, j, ph);
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
-    const int r = row0 + i * rows;
-    if (r < len) {
+    const int r = row0 + i * rows, t = r & (B - 1), h = r >> p.log_b;
+    if (t < len && h < heads) {
       float x[16];
       unpack16(a[i], b[i], x);
       if (turn) {
-        float co[8], si[8];
-        angles(ph, __ldg(p.r.positions + first + r), p.r.scale, p.r.inverse, co, si);
+        if (t != t_of) angles(ph, __ldg(p.r.positions + first + t), p.r.scale, p.r.inverse, co, si);
+        t_of = t;
         rotate16(x, co, si, p.r.interleaved);
       }
-      uint8_t* dst = page + (int64_t)(off + r) * d;
+      const float inv = 1.f / s_scale[h];
+      uint8_t* dst = page + ((int64_t)h * B + off + t) * d;
       *reinterpret_cast<uint2*>(dst + oa) = to_codes8(x, inv);
       *reinterpret_cast<uint2*>(dst + ob) = to_codes8(x + 8, inv);
     }
   }
 }
 
-// CTAs [0, q_ctas): rotation of q; the others: one unit of the append each.
+// CTAs [0, kv_ctas): one unit of the append each, the longer work first; the
+// others: rotation of q.
 template <int kPasses>
-__global__ void __launch_bounds__(kRotThreads) rotary_append_kernel(const AppendArgs p) {
-  __shared__ float red[kRotThreads / 32];
+__global__ void __launch_bounds__(kRotThreads, kPasses <= 4 ? 3 : 2) rotary_append_kernel(const AppendArgs p) {
+  __shared__ uint32_t s_top[kMaxHeads];
+  __shared__ float s_old[kMaxHeads], s_scale[kMaxHeads];
   pdl_wait();
   pdl_trigger();
-  if ((int)blockIdx.x < p.q_ctas)
-    rotate_unit(p.r, (int64_t)blockIdx.x * kRotThreads + threadIdx.x);
+  if ((int)blockIdx.x < p.kv_ctas)
+    append_piece<kPasses>(p, (int)blockIdx.x, s_top, s_old, s_scale);
   else
-    append_piece<kPasses>(p, (int)blockIdx.x - p.q_ctas, red);
+    rotate_unit(p.r, (int64_t)((int)blockIdx.x - p.kv_ctas) * kRotThreads + threadIdx.x);
 }
 
 int64_t rotary_units(int T, int H, int log_j) {
@@ -384,14 +422,17 @@ gdn_status_t launch_rotary_kv_append(const void* q, int64_t q_stride, const void
   p.ks = ks;
   p.vs = vs;
   const int64_t q_ctas = q ? (rotary_units(T, Hq, p.r.log_j) + kRotThreads - 1) / kRotThreads : 0;
-  const int64_t ctas = q_ctas + 2 * (int64_t)piece_cap * Hk;
+  const int per_head = block_tokens * d / 16;                  // threads of one head's block
+  p.hg = std::max(1, std::min(Hk, 4 * kRotThreads / per_head));
+  p.head_groups = (Hk + p.hg - 1) / p.hg;
+  const int64_t ctas = q_ctas + 2 * (int64_t)piece_cap * p.head_groups;
   if (ctas > 0x7fffffff) return GDN_ERR_UNSUPPORTED;
   if (ctas == 0) return GDN_OK;
-  p.q_ctas = (int)q_ctas;
-  const int passes = block_tokens * d / 16 / kRotThreads;
+  p.kv_ctas = 2 * piece_cap * p.head_groups;
+  const int passes = (per_head * p.hg + kRotThreads - 1) / kRotThreads;
   auto kern = passes <= 1   ? rotary_append_kernel<1>
-              : passes == 2 ? rotary_append_kernel<2>
-              : passes == 4 ? rotary_append_kernel<4>
+              : passes <= 2 ? rotary_append_kernel<2>
+              : passes <= 4 ? rotary_append_kernel<4>
                             : rotary_append_kernel<8>;
   return check_launch(launch_pdl(kern, dim3((unsigned)ctas), dim3(kRotThreads), 0, st, p));
 }
