@@ -1,4 +1,5 @@
-"""Python binding of the GDN C ABI (``include/gdn.h``), via ctypes.
+"""Python binding of the GDN C ABI (``include/gdn.h``), via ctypes (the calls on
+the attention side: via the compiled ``csrc/marshal.cpp``).
 
 Argument marshalling only: every function passes device pointers, sizes and
 the current CUDA stream of PyTorch to the library entry point of the same name
@@ -13,7 +14,7 @@ import os
 
 import torch
 
-from .build import LIB_PATH
+from .build import LIB_PATH, MARSHAL_PATH
 
 GDN_OK = 0
 GDN_ERR_INVALID_ARG = -1
@@ -374,40 +375,28 @@ def delta_rule_prefill_chunked_slots(q, k, v, a, b, cu_seqlens, S, has_initial_s
 
 ROTARY_SCALINGS = {"plain": 0, "linear": 1, "by_parts": 2}
 
-# The checks below are written out with few attribute reads: a call's host time
-# is what a small step costs.
-_int32, _int64, _bf16, _float32 = torch.int32, torch.int64, torch.bfloat16, torch.float32
+_MARSHAL = None
 
 
-def _bad(what: str):
-    raise ValueError(what)
+def _marshal():
+    """The compiled argument marshalling of these calls (csrc/marshal.cpp)."""
+    global _MARSHAL
+    if _MARSHAL is None:
+        load_library()
+        if not os.path.exists(MARSHAL_PATH):
+            raise RuntimeError(f"GDN binding not built: {MARSHAL_PATH} is missing "
+                               "(run __graft_entry__.build() or python -m "
+                               "gated_deltanet_linear_build_gb300.build)")
+        from . import _marshal as module
+        _MARSHAL = module
+    return _MARSHAL
 
 
-def _rows(t, d: int, name: str) -> int:
-    """Token stride of a bfloat16 [T, H, d] tensor whose heads are contiguous."""
-    s0, s1, s2 = t.stride()
-    T, H, _ = t.shape
-    if t.dtype is not _bf16 or (s2 != 1 and d > 1) or (s1 != d and H > 1):
-        _bad(f"{name}: bfloat16 [T, H, d] with contiguous heads expected")
-    return s0 if T > 1 else H * d
-
-
-def _ints(t, name: str, dtype=torch.int32):
-    if t.dtype is not dtype or not t.is_contiguous():
-        _bad(f"{name}: contiguous {dtype} expected")
-    return t.data_ptr()
-
-
-def _cache_shape(k_cache, v_cache, k_scale, v_scale):
-    shape = k_cache.shape
-    if v_cache.shape != shape or k_cache.element_size() != 1 or v_cache.element_size() != 1 or not (
-            k_cache.is_contiguous() and v_cache.is_contiguous()):
-        _bad("k_cache, v_cache: contiguous 8-bit [num_blocks, Hk, B, d] expected")
-    if k_scale.dtype is not _float32 or v_scale.dtype is not _float32 or not (
-            k_scale.is_contiguous() and v_scale.is_contiguous()) or (
-            k_scale.shape != shape[:2] or v_scale.shape != shape[:2]):
-        _bad("k_scale, v_scale: contiguous float32 [num_blocks, Hk] expected")
-    return shape
+def _handle(stream):
+    """A stream argument as an integer handle (None: the current stream)."""
+    if stream is None:
+        return None
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def build_block_tables(cu_seqlens, context_lens, free_blocks, block_table, kv_lens, positions,
@@ -420,21 +409,9 @@ def build_block_tables(cu_seqlens, context_lens, free_blocks, block_table, kv_le
     kv_lens int32 [N], positions int32 [T], slots int64 [T], pieces int32
     [capacity, 4] ({block, tok_start, len, offset}; T // block_tokens + 2 N
     always suffice), counts int32 [2] (pieces, blocks taken)."""
-    N, M = block_table.shape
-    stride, inner = block_table.stride()
-    T, = positions.shape
-    cap, width = pieces.shape
-    if block_table.dtype is not _int32 or (inner != 1 and M > 1):
-        _bad("block_table: int32 [N, M] with contiguous rows expected")
-    if cu_seqlens.shape[0] != N + 1 or context_lens.shape[0] != N or kv_lens.shape[0] != N or (
-            slots.shape[0] != T) or width != 4 or counts.shape[0] < 2:
-        _bad("build_block_tables: sizes do not agree")
-    rc = (_LIB or load_library()).gdn_build_block_tables(
-        _ints(cu_seqlens, "cu_seqlens"), _ints(context_lens, "context_lens"),
-        _ints(free_blocks, "free_blocks"), free_blocks.shape[0], N, T, block_tokens,
-        block_table.data_ptr(), stride if N > 1 else M, M, _ints(kv_lens, "kv_lens"),
-        _ints(positions, "positions"), _ints(slots, "slots", _int64), _ints(pieces, "pieces"),
-        cap, _ints(counts, "counts"), _ptr(device_status), _stream(stream))
+    rc = (_MARSHAL or _marshal()).build_block_tables(
+        cu_seqlens, context_lens, free_blocks, block_table, kv_lens, positions, slots, pieces,
+        counts, block_tokens, device_status, _handle(stream))
     if rc:
         _check(rc, "gdn_build_block_tables")
 
@@ -456,24 +433,8 @@ def rotary(q, k, positions, phases, q_out, k_out, *, interleaved: bool = False,
     """Rotary positions on q [T, Hq, d] and k [T, Hk, d] (k and k_out may be
     None) into q_out, k_out (which may be q, k). positions int32 [T], phases
     int64 [rot_dim // 2]. ``inverse`` turns the other way (the gradient)."""
-    shape = q.shape
-    T, Hq, d = shape
-    if q_out.shape != shape or positions.shape[0] != T:
-        _bad("rotary: shapes do not agree")
-    if k is None:
-        Hk = k_ptr = k_stride = ko_ptr = ko_stride = 0
-    else:
-        k_shape = k.shape
-        Tk, Hk, dk = k_shape
-        if Tk != T or dk != d or k_out.shape != k_shape:
-            _bad("rotary: shapes do not agree")
-        k_ptr, k_stride = k.data_ptr(), _rows(k, d, "k")
-        ko_ptr, ko_stride = k_out.data_ptr(), _rows(k_out, d, "k_out")
-    rc = (_LIB or load_library()).gdn_rotary(
-        q.data_ptr(), _rows(q, d, "q"), k_ptr, k_stride, _ints(positions, "positions"),
-        _ints(phases, "phases", _int64), q_out.data_ptr(), _rows(q_out, d, "q_out"), ko_ptr,
-        ko_stride, T, Hq, Hk, d, 2 * phases.shape[0], interleaved, inverse, scale,
-        _stream(stream))
+    rc = (_MARSHAL or _marshal()).rotary(q, k, positions, phases, q_out, k_out, interleaved, inverse,
+                                         scale, _handle(stream))
     if rc:
         _check(rc, "gdn_rotary")
 
@@ -484,33 +445,9 @@ def rotary_kv_append(q, k, v, positions, phases, pieces, num_pieces, q_out, k_ca
     """Rotate q into q_out, rotate k, and append k and v [T, Hk, d] to the
     cache by the step's page pieces (build_block_tables; num_pieces = counts).
     phases None appends without rotation; q and q_out may then be None."""
-    k_shape = k.shape
-    T, Hk, d = k_shape
-    blocks, heads, B, width = _cache_shape(k_cache, v_cache, k_scale, v_scale)
-    if v.shape != k_shape or heads != Hk or width != d:
-        _bad("rotary_kv_append: shapes do not agree")
-    if phases is None:
-        rot = pos_ptr = ph_ptr = 0
-    else:
-        rot = 2 * phases.shape[0]
-        pos_ptr, ph_ptr = _ints(positions, "positions"), _ints(phases, "phases", _int64)
-        if positions.shape[0] != T:
-            _bad("rotary_kv_append: shapes do not agree")
-    if q is None:
-        Hq = q_ptr = q_stride = qo_ptr = qo_stride = 0
-    else:
-        q_shape = q.shape
-        Tq, Hq, dq = q_shape
-        if Tq != T or dq != d or q_out.shape != q_shape:
-            _bad("rotary_kv_append: shapes do not agree")
-        q_ptr, q_stride = q.data_ptr(), _rows(q, d, "q")
-        qo_ptr, qo_stride = q_out.data_ptr(), _rows(q_out, d, "q_out")
-    rc = (_LIB or load_library()).gdn_rotary_kv_append(
-        q_ptr, q_stride, k.data_ptr(), _rows(k, d, "k"), v.data_ptr(), _rows(v, d, "v"),
-        pos_ptr, ph_ptr, _ints(pieces, "pieces"), _ints(num_pieces, "num_pieces"),
-        pieces.shape[0], qo_ptr, qo_stride, k_cache.data_ptr(), v_cache.data_ptr(),
-        k_scale.data_ptr(), v_scale.data_ptr(), blocks, B, T, Hq, Hk, d, rot, interleaved, scale,
-        _stream(stream))
+    rc = (_MARSHAL or _marshal()).rotary_kv_append(
+        q, k, v, positions, phases, pieces, num_pieces, q_out, k_cache, v_cache, k_scale, v_scale,
+        interleaved, scale, _handle(stream))
     if rc:
         _check(rc, "gdn_rotary_kv_append")
 
@@ -523,9 +460,12 @@ def paged_attention_plan(cu_seqlens, kv_lens, workspace, *, T: int, Hq: int, Hk:
                          block_tokens: int, max_blocks: int, max_new_tokens: int, stream=None):
     """Build the step's row tiles into ``workspace``; the step's attention
     calls then pass planned=True. max_blocks = block_table.shape[1]."""
+    for t, name in ((cu_seqlens, "cu_seqlens"), (kv_lens, "kv_lens")):
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous int32 expected")
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     rc = _lib().gdn_paged_attention_plan(
-        _ints(cu_seqlens, "cu_seqlens"), _ints(kv_lens, "kv_lens"), cu_seqlens.numel() - 1, T,
+        _ptr(cu_seqlens), _ptr(kv_lens), cu_seqlens.numel() - 1, T,
         Hq, Hk, d, block_tokens, max_blocks, max_new_tokens, _ptr(workspace), nbytes,
         _stream(stream))
     _check(rc, "gdn_paged_attention_plan")
@@ -538,25 +478,9 @@ def paged_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqle
     that already holds them, into o [T, Hq, d]. block_table int32 [N, M],
     cu_seqlens int32 [N+1], kv_lens int32 [N]; max_new_tokens bounds the new
     tokens of a sequence (1 for a decode step)."""
-    shape = q.shape
-    T, Hq, d = shape
-    blocks, Hk, B, width = _cache_shape(k_cache, v_cache, k_scale, v_scale)
-    N, M = block_table.shape
-    stride, inner = block_table.stride()
-    if width != d or o.shape != shape or o.dtype is not _bf16 or not o.is_contiguous() or (
-            kv_lens.shape[0] != N) or cu_seqlens.shape[0] != N + 1 or (
-            block_table.dtype is not _int32) or (inner != 1 and M > 1):
-        _bad("paged_attention: shapes do not agree")
-    if workspace is None:
-        ws_ptr = nbytes = 0
-    else:
-        ws_ptr, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    rc = (_LIB or load_library()).gdn_paged_attention(
-        q.data_ptr(), _rows(q, d, "q"), k_cache.data_ptr(), v_cache.data_ptr(),
-        k_scale.data_ptr(), v_scale.data_ptr(), blocks, B, block_table.data_ptr(),
-        stride if N > 1 else M, M, _ints(cu_seqlens, "cu_seqlens"), _ints(kv_lens, "kv_lens"), N,
-        T, max_new_tokens, o.data_ptr(), Hq, Hk, d, softmax_scale,
-        GDN_FLAG_PLANNED if planned else 0, ws_ptr, nbytes, _stream(stream))
+    rc = (_MARSHAL or _marshal()).paged_attention(
+        q, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, kv_lens, o, workspace,
+        softmax_scale, max_new_tokens, planned, _handle(stream))
     if rc:
         _check(rc, "gdn_paged_attention")
 
