@@ -232,7 +232,8 @@ gdn_status_t gdn_paged_attention(const void* q, int64_t q_stride, const void* k_
       !aligned(v_scale, 4) || !aligned(block_table, 4))
     return GDN_ERR_ALIGNMENT;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if ((flags & GDN_FLAG_PLANNED) == 0) {
+  const bool self_plan = (flags & GDN_FLAG_PLANNED) == 0 && attn::self_planned(N, T, Hq / Hk, max_new_tokens);
+  if ((flags & GDN_FLAG_PLANNED) == 0 && !self_plan) {
     rc = launch_attn_plan(cu_seqlens, kv_lens, N, T, Hq, Hk, d,
                           (int64_t)max_blocks * block_tokens, max_new_tokens, workspace, st);
     if (rc != GDN_OK) return rc;
@@ -264,7 +265,9 @@ gdn_status_t gdn_paged_attention(const void* q, int64_t q_stride, const void* k_
   a.partials = reinterpret_cast<float*>(ws + l.partials);
   a.tiles = reinterpret_cast<attn::Item*>(ws + l.tiles);
   a.sorted_tiles = reinterpret_cast<attn::Item*>(ws + l.sorted_tiles);
-  a.starts = reinterpret_cast<const attn::Start*>(ws + l.starts);
+  a.self_plan = self_plan ? 1 : 0;
+  // A plan in the workspace stays as it is.
+  a.starts = reinterpret_cast<attn::Start*>(ws + (self_plan ? l.self_starts : l.starts));
   a.tile_starts = reinterpret_cast<const attn::Start*>(ws + l.tile_starts);
   a.split_rows = l.split_rows;
   a.split_grid = attn::split_grid(d, l.split_rows);

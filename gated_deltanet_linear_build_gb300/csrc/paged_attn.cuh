@@ -33,9 +33,12 @@ struct alignas(64) Start {
 };
 
 struct Layout {
-  size_t starts, tile_starts, items, partials, tiles, sorted_tiles, tile_partials, total;
+  size_t starts, self_starts, tile_starts, items, partials, tiles, sorted_tiles, tile_partials, total;
   int item_cap, tile_cap, split_rows, tile_rows;
 };
+
+// Rows of a split tile: 16 where the query heads of a token need more than 8.
+inline int split_rows(int G) { return G > 8 ? 16 : 8; }
 
 // Rows of a tile of the tensor-core kernel.
 inline int tile_rows(int d) { return d == 256 ? 128 : 256; }
@@ -53,9 +56,14 @@ inline Kernels kernels_of(int N, int T, int G, int max_new_tokens) {
   const int64_t longest = N == 1 ? T : max_new_tokens, limit = split_limit(G);
   return {!(N == 1 && longest * G > limit), longest * G > limit};
 }
-
-// Rows of a split tile: 16 where the query heads of a token need more than 8.
-inline int split_rows(int G) { return G > 8 ? 16 : 8; }
+// Whether the split kernel's CTAs can plan the step by themselves: one tile a
+// sequence, no more of them than one block scans. A decode step of 32 requests
+// takes MEASURED_SELF us with a plan of its own, and MEASURED_PLAN us with the
+// plan's kernel.
+inline bool self_planned(int N, int T, int G, int max_new_tokens) {
+  const int64_t longest = N == 1 ? T : max_new_tokens;
+  return N <= 1024 && longest * G <= split_rows(G);
+}
 
 // CTAs of the split kernel: one wave.
 constexpr int kSplitGridMax = 320;
@@ -108,7 +116,9 @@ struct Args {
   float* partials;
   Item *tiles, *sorted_tiles;          // in sequence order; by length
   int split_rows, split_grid, tile_grid;
-  const Start *starts, *tile_starts;
+  Start* starts;
+  const Start* tile_starts;
+  int self_plan;                       // the split kernel's CTAs plan by themselves
   float* tile_partials;
 };
 

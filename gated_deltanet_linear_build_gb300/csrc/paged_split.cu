@@ -52,6 +52,8 @@ Layout layout(int T, int N, int Hq, int Hk, int d) {
   size_t at = 0;
   l.starts = at;
   at += kSplitGridMax * sizeof(Start);
+  l.self_starts = at;
+  at += kSplitGridMax * sizeof(Start);
   l.tile_starts = at;
   at = up(at + tile_grid() * sizeof(Start));
   l.items = at;
@@ -353,7 +355,8 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 // Split kernel
 // ---------------------------------------------------------------------------
 constexpr int kWarps = 8;
-constexpr int kJoinCols = 4;             // CTAs that share the elements of a joined item
+constexpr int kSelfPlan = 1024;          // sequences that a CTA plans itself
+constexpr int kJoinThreads = 256;
 
 template <int D, int QM>
 struct Cfg {
@@ -381,7 +384,8 @@ struct Cfg {
   static constexpr int o_nan = o_l + rows * 2 * 4;
   static constexpr int o_bar = o_nan + D * 4;
   static constexpr int o_flag = o_bar + kWarps * slots * 8;
-  static constexpr int total = o_flag + 16;
+  static constexpr int o_cum = o_flag + 16;            // units before each sequence (self plan)
+  static constexpr int total = o_cum + (kSelfPlan + 1) * 4;
 };
 
 // The K rows of an MMA's 8 columns and the V rows of its k index are free to
@@ -474,7 +478,74 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
   int posted = 0, taken = 0;                           // half units, over all segments
   pdl_wait();
   pdl_trigger();
-  const Start start = read_start(p.starts + blockIdx.x);
+  Start start;
+  int* s_cum = reinterpret_cast<int*>(smem + C::o_cum);
+  if (p.self_plan) {
+    // One tile a sequence: every CTA forms the line itself (one round of loads and
+    // a scan), which is sooner than a kernel before this one.
+    int2* sums = reinterpret_cast<int2*>(s_ml);
+    constexpr int per = kSelfPlan / (kWarps * 32);
+    int u4[per], mine = 0;
+#pragma unroll
+    for (int k = 0; k < per; ++k) {
+      const int n = tid * per + k;
+      u4[k] = 0;
+      if (n < p.N) {
+        const Seq q = seq_of(p.cu, p.kv, n, p.T, (int64_t)p.max_blocks << p.log_b);
+        if (q.len > 0) u4[k] = max(1, (visible(q, q.len - 1) + kUnit - 1) / kUnit);
+      }
+      mine += u4[k];
+    }
+    int inc = mine;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, k);
+      if (lane >= k) inc += v;
+    }
+    if (lane == 31) sums[w].x = inc;
+    __syncthreads();
+    int before = inc - mine, total = 0;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      if (k < w) before += sums[k].x;
+      total += sums[k].x;
+    }
+#pragma unroll
+    for (int k = 0; k < per; ++k) {
+      s_cum[tid * per + k] = before;
+      before += u4[k];
+    }
+    if (tid == 0) s_cum[kSelfPlan] = total;
+    __syncthreads();
+    const long long all = (long long)total * p.Hk;
+    start.num_items = p.N;
+    start.units = total;
+    start.per_cta = (int)max((long long)kWarps, (all + gridDim.x - 1) / gridDim.x);
+    start.u = min(all, (long long)blockIdx.x * start.per_cta);
+    start.u_end = min(all, start.u + start.per_cta);
+    start.item = start.head = 0;
+    start.it = {0, 0, 0, 0};
+    start.first = start.len = start.kv = 0;
+    if (start.u < start.u_end) {
+      start.head = (int)((unsigned long long)start.u / (unsigned)total);
+      const int x = (int)(start.u - (long long)start.head * total);
+      int lo = 0, hi = p.N - 1;          // last sequence that begins at or before x
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_cum[mid] <= x) lo = mid; else hi = mid - 1;
+      }
+      start.item = lo;
+      start.it = {lo, 0, s_cum[lo + 1] - s_cum[lo], s_cum[lo]};
+      const Seq q = seq_of(p.cu, p.kv, lo, p.T, (int64_t)p.max_blocks << p.log_b);
+      start.first = q.first;
+      start.len = q.len;
+      start.kv = q.kv;
+    }
+    if (tid < 4)                         // for the joining kernel
+      reinterpret_cast<int4*>(p.starts + blockIdx.x)[tid] = reinterpret_cast<const int4*>(&start)[tid];
+  } else {
+    start = read_start(p.starts + blockIdx.x);
+  }
   const int num_items = start.num_items, units1 = start.units;
   long long u = start.u;
   const long long u_end = start.u_end;
@@ -493,6 +564,19 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
 
     // ---- this warp's units: first_unit + w, + 8, ... --------------------------
     const int mine = seg > w ? (seg - w + kWarps - 1) / kWarps : 0;
+    // Q's rows of this warp, on their way before the first table read is waited for.
+    constexpr int per = D / 32;
+    uint32_t q_raw[QM][per / 2];
+#pragma unroll
+    for (int rq = 0; rq < QM; ++rq) {
+      const int r = w + rq * kWarps;
+      const int row = row0 + r, tok = row / G;
+      const __nv_bfloat16* src = p.q + (int64_t)(s.first + tok) * p.q_stride +
+                                 (int64_t)(head * G + row - tok * G) * D + lane * per;
+#pragma unroll
+      for (int i = 0; i < per / 2; ++i)
+        q_raw[rq][i] = r < n_rows ? __ldg(reinterpret_cast<const uint32_t*>(src) + i) : 0u;
+    }
     // Block of this lane's box of unit i; read a unit before it is needed.
     auto block_of = [&](int i) {
       const int key = (first_unit + w + i * kWarps) * kUnit + (page << log_box);
@@ -547,23 +631,16 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
     if (tid == 0) s_flag[1] = 0;
 
     // ---- Q of the tile: hi and lo codes, one power-of-two scale per row -------
-    for (int r = w; r < C::rows; r += kWarps) {
-      constexpr int per = D / 32;
+#pragma unroll
+    for (int rq = 0; rq < QM; ++rq) {
+      const int r = w + rq * kWarps;
       float v[per];
       float top = 0.f;
       bool bad = false;
-      if (r < n_rows) {
-        const int row = row0 + r, tok = s.first + row / G, hq = head * G + row % G;
-        const __nv_bfloat16* src = p.q + (int64_t)tok * p.q_stride + (int64_t)hq * D + lane * per;
 #pragma unroll
-        for (int i = 0; i < per; i += 2) {
-          const uint32_t two = __ldg(reinterpret_cast<const uint32_t*>(src + i));
-          v[i] = bf16lo(two);
-          v[i + 1] = bf16hi(two);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < per; ++i) v[i] = 0.f;
+      for (int i = 0; i < per; i += 2) {
+        v[i] = bf16lo(q_raw[rq][i / 2]);
+        v[i + 1] = bf16hi(q_raw[rq][i / 2]);
       }
 #pragma unroll
       for (int i = 0; i < per; ++i) {
@@ -885,13 +962,22 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
     tc::fence_smem_to_async();           // before the next copies into the ring
     __syncthreads();                     // the ring, Q and s_ml are free again
     u += seg;
-    if (first_unit + seg == n_units && ++lo == num_items) {
-      lo = 0;
-      ++head;
-    }
-    if (u < u_end) {
-      const int4 raw = __ldg(reinterpret_cast<const int4*>(p.items) + lo);
-      it = {raw.x, raw.y, raw.z, raw.w};
+    if (u < u_end) {                     // the piece goes on with the next item
+      if (++lo == num_items) {
+        lo = 0;
+        ++head;
+      }
+      if (p.self_plan) {
+        while (s_cum[lo + 1] == s_cum[lo])               // sequences without new tokens
+          if (++lo == num_items) {
+            lo = 0;
+            ++head;
+          }
+        it = {lo, 0, s_cum[lo + 1] - s_cum[lo], s_cum[lo]};
+      } else {
+        const int4 raw = __ldg(reinterpret_cast<const int4*>(p.items) + lo);
+        it = {raw.x, raw.y, raw.z, raw.w};
+      }
       s = seq_of(p.cu, p.kv, it.seq, p.T, (int64_t)p.max_blocks << p.log_b);
     }
   }
@@ -901,83 +987,130 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       tc::mbar_wait(full + h % C::slots, (h / C::slots) & 1);
 }
 
-// Joins the partial results of items that were cut: CTA (c0, y) takes the item
-// that begins in CTA c0's piece and goes on past its end, a quarter of its
-// elements. Thread groups share a long item's partials; each adds its own in CTA
-// order, and the groups are added in order: the order is fixed.
-template <int D, int QM>
-__global__ void __launch_bounds__(256) attn_split_join_kernel(const Args p) {
-  constexpr int rows = 8 * QM, elems = rows * D / 4 / kJoinCols;      // float4 of this CTA
-  constexpr int groups = 256 / elems < 1 ? 1 : 256 / elems;
-  static_assert(256 % elems == 0, "whole groups");
+// Joins the partial results of items that were cut: CTA (k, y) takes the k-th of
+// them and its y-th share of the elements. The grid is bounded by the step's
+// items, few CTAs where they are few: 1,216 CTAs of which most had nothing to do
+// cost the step 12 us. Thread groups share a long item's partials; each adds its
+// own in CTA order, and the groups are added in order: the order is fixed.
+template <int D, int QM, int COLS>
+__global__ void __launch_bounds__(kJoinThreads) attn_split_join_kernel(const Args p, const int pieces) {
+  constexpr int rows = 8 * QM, elems = rows * D / 4 / COLS;           // float4 of this CTA
+  constexpr int lanes = elems < kJoinThreads ? elems : kJoinThreads;  // threads of a group
+  constexpr int groups = kJoinThreads / lanes;
+  static_assert(kJoinThreads % lanes == 0 && elems % lanes == 0, "whole groups");
   __shared__ float fs[kSplitGridMax * rows];                          // factors [partial][row]
   __shared__ float s_l[rows];
-  __shared__ float4 s_o[groups][elems];
+  __shared__ float4 s_o[groups][lanes];
+  __shared__ int s_count[kJoinThreads / 32], s_c0;
   pdl_wait();
   pdl_trigger();
-  const int c0 = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
-  if (c0 + 1 >= (int)gridDim.x) return;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  // The k-th piece that begins an item and ends inside it.
+  int left = blockIdx.x, c0 = -1;
+  for (int base = 0; base + 1 < pieces; base += kJoinThreads) {
+    const int c = base + tid;
+    bool cut = false;
+    if (c + 1 < pieces) {
+      const Start next = read_start(p.starts + c + 1);
+      if (next.u < next.u_end) {
+        const long long at0 = (long long)next.head * next.units + next.it.cum;
+        cut = at0 != next.u && at0 / next.per_cta == c;
+      }
+    }
+    const unsigned vote = __ballot_sync(0xffffffffu, cut);
+    if (lane == 0) s_count[w] = __popc(vote);
+    if (tid == 0) s_c0 = -1;
+    __syncthreads();
+    int before = __popc(vote & ((1u << lane) - 1)), total = 0;
+#pragma unroll
+    for (int k = 0; k < kJoinThreads / 32; ++k) {
+      if (k < w) before += s_count[k];
+      total += s_count[k];
+    }
+    if (cut && before == left) s_c0 = c;
+    __syncthreads();
+    c0 = s_c0;
+    if (c0 >= 0) break;
+    left -= total;
+    __syncthreads();
+  }
+  if (c0 < 0) return;
   const Start next = read_start(p.starts + c0 + 1);
-  if (next.u >= next.u_end) return;
   const long long at0 = (long long)next.head * next.units + next.it.cum;
-  if (at0 == next.u || at0 / next.per_cta != c0) return;    // not cut here, or begun earlier
   const int n = (int)((at0 + next.it.units - 1) / next.per_cta) - c0 + 1;
   const float* base = p.partials + ((size_t)c0 * 2 + 1) * (rows * (D + 2));
   auto part = [&](int c) { return base + (c == 0 ? 0 : (size_t)(2 * c - 1) * (rows * (D + 2))); };
-  for (int r = tid >> 5; r < rows; r += 8) {
+  const int group = tid / lanes, from = n * group / groups, to = n * (group + 1) / groups;
+  // Eight loads at a time (a chain of single ones would take 0.5 us each), the
+  // first of them before the factors are known.
+  float4 v[8];
+  auto fetch = [&](int e, int c) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c + k < to) v[k] = __ldcg(reinterpret_cast<const float4*>(part(c + k) + 2 * rows + e));
+  };
+  const int e0 = (blockIdx.y * elems + tid % lanes) * 4;
+  fetch(e0, from);
+  for (int r = w; r < rows; r += kJoinThreads / 32) {
     float top = -INFINITY, l = 0.f;
-    for (int c = lane; c < n; c += 32) {
-      const float m = __ldcg(part(c) + r * 2);
-      fs[c * rows + r] = m;
-      top = fmaxf(top, m);
+    constexpr int per = (kSplitGridMax + 31) / 32;
+    float2 ml[per];
+#pragma unroll
+    for (int k = 0; k < per; ++k) {
+      const int c = lane + 32 * k;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (c < n) ml[k] = __ldcg(reinterpret_cast<const float2*>(part(c)) + r);
+      top = fmaxf(top, ml[k].x);
     }
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-    for (int c = lane; c < n; c += 32) {
-      const float m = fs[c * rows + r];
+#pragma unroll
+    for (int k = 0; k < per; ++k) {
+      const int c = lane + 32 * k;
       // NaN sums pass on: a NaN row has m = -inf and its l as it is.
-      const float f = m == -INFINITY ? 1.f : ex2_approx(m - top);
-      fs[c * rows + r] = f;
-      l += __ldcg(part(c) + r * 2 + 1) * f;
+      const float f = ml[k].x == -INFINITY ? 1.f : ex2_approx(ml[k].x - top);
+      if (c < n) fs[c * rows + r] = f;
+      l += ml[k].y * f;
     }
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
     if (lane == 0) s_l[r] = l;
   }
   __syncthreads();
-  const int group = tid / elems, e = (blockIdx.y * elems + tid % elems) * 4, r = e / D;
-  const int from = n * group / groups, to = n * (group + 1) / groups;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  // Eight loads at a time: a chain of single ones would take 0.5 us each.
-  for (int c = from; c < to; c += 8) {
-    float4 v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (c + k < to) v[k] = __ldcg(reinterpret_cast<const float4*>(part(c + k) + 2 * rows + e));
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (c + k < to) {
-        const float f = fs[(c + k) * rows + r];
-        o.x = fmaf(v[k].x, f, o.x);
-        o.y = fmaf(v[k].y, f, o.y);
-        o.z = fmaf(v[k].z, f, o.z);
-        o.w = fmaf(v[k].w, f, o.w);
-      }
-  }
-  s_o[group][tid % elems] = o;
-  __syncthreads();
-  if (group > 0) return;
-#pragma unroll
-  for (int k = 1; k < groups; ++k) {
-    const float4 v = s_o[k][tid];
-    o.x += v.x;
-    o.y += v.y;
-    o.z += v.z;
-    o.w += v.w;
-  }
   const int G = p.Hq / p.Hk;
   const RowsOut out = {p.o, next.first, next.it.row0, min(rows, next.len * G - next.it.row0), G, p.Hq, next.head};
-  put_row4<D>(out, r, e % D, o, s_l[r]);
+#pragma unroll 1
+  for (int i = 0; i < elems; i += lanes) {
+    const int e = e0 + i * 4, r = e / D;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int c = from; c < to; c += 8) {
+      if (c > from || i > 0) fetch(e, c);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c + k < to) {
+          const float f = fs[(c + k) * rows + r];
+          o.x = fmaf(v[k].x, f, o.x);
+          o.y = fmaf(v[k].y, f, o.y);
+          o.z = fmaf(v[k].z, f, o.z);
+          o.w = fmaf(v[k].w, f, o.w);
+        }
+    }
+    if constexpr (groups > 1) {
+      s_o[group][tid % lanes] = o;
+      __syncthreads();
+      if (group > 0) return;                   // elems == lanes here
+#pragma unroll
+      for (int k = 1; k < groups; ++k) {
+        const float4 a = s_o[k][tid];
+        o.x += a.x;
+        o.y += a.y;
+        o.z += a.z;
+        o.w += a.w;
+      }
+    }
+    put_row4<D>(out, r, e % D, o, s_l[r]);
+  }
 }
 
 template <int D, int QM>
@@ -997,8 +1130,16 @@ gdn_status_t launch_split(const Args& a, cudaStream_t st) {
                                                   dim3(kWarps * 32), Cfg<D, QM>::total, st, a, k_map,
                                                   v_map));
   if (rc != GDN_OK) return rc;
-  return check_launch(launch_pdl(attn_split_join_kernel<D, QM>, dim3(a.split_grid, kJoinCols),
-                                 dim3(256), 0, st, a));
+  // At most one cut item per piece, and no more than there are items. Long items
+  // (many partials each) are few: more CTAs share one.
+  const int64_t items = ((int64_t)a.T * (a.Hq / a.Hk) / (8 * QM) + a.N) * a.Hk;
+  const int cuts = (int)std::min<int64_t>(a.split_grid - 1, items);
+  if (cuts <= 0) return rc;
+  if (cuts <= 16)
+    return check_launch(launch_pdl(attn_split_join_kernel<D, QM, 8>, dim3(cuts, 8), dim3(kJoinThreads),
+                                   0, st, a, a.split_grid));
+  return check_launch(launch_pdl(attn_split_join_kernel<D, QM, 2>, dim3(cuts, 2), dim3(kJoinThreads), 0,
+                                 st, a, a.split_grid));
 }
 
 }  // namespace

@@ -153,6 +153,19 @@ def test_planned_calls_and_reuse_of_a_workspace_give_the_same_bits():
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
 
 
+def test_an_unplanned_call_leaves_a_plan_in_the_workspace_alone():
+    from gated_deltanet_linear_build_gb300 import gdn
+    s = make(18, [1] * 5, [3000, 64, 1, 500, 31], 16, 2, 256, 64)
+    ws = torch.empty(gdn.paged_attention_workspace_size(5, 5, 16, 2, 256), dtype=torch.uint8, device="cuda")
+    gdn.paged_attention_plan(s["cu"], s["kv"], ws, T=5, Hq=16, Hk=2, d=256, block_tokens=64,
+                             max_blocks=s["table"].shape[1], max_new_tokens=1)
+    a = run(s, workspace=ws, planned=True)
+    other = make(19, [1] * 3, [700, 2, 90], 16, 2, 256, 64)
+    check(other, run(other, workspace=ws))
+    assert torch.equal(a, run(s, workspace=ws, planned=True))
+    check(s, a)
+
+
 def test_on_another_stream():
     s = make(10, [1] * 4, [1000, 70, 3, 400], 8, 2, 128, 32)
     torch.cuda.synchronize()
