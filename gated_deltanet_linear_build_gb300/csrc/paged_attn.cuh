@@ -23,13 +23,15 @@ struct Item {
 constexpr int kUnit = 32;              // keys per unit of the split kernel
 constexpr int kTileKeys = 64;         // keys per unit of the tensor-core kernel
 
-// A CTA's piece [u, u_end) of the work line (units of all heads), with all that
-// its first segment needs: one 64-byte line instead of a chain of loads.
+// A CTA's piece of the work line (units of all heads), `count` units from u, with
+// all that its first segment needs: one 64-byte line instead of a chain of loads.
 struct alignas(64) Start {
   int item, head, num_items, units;   // of unit u; of the list: tiles, one head's units
   Item it;
-  int first, len, kv, per_cta;        // the item's sequence; units per CTA (0: whole items)
-  long long u, u_end;
+  int first, len, kv;                 // the item's sequence
+  int c0;                             // the CTA that begins the item (-1: whole items are dealt)
+  long long u;
+  int count, pieces;                  // pieces of the item
 };
 
 struct Layout {
@@ -56,13 +58,14 @@ inline Kernels kernels_of(int N, int T, int G, int max_new_tokens) {
   const int64_t longest = N == 1 ? T : max_new_tokens, limit = split_limit(G);
   return {!(N == 1 && longest * G > limit), longest * G > limit};
 }
+constexpr int kSelfPlan = 512;
 // Whether the split kernel's CTAs can plan the step by themselves: one tile a
 // sequence, no more of them than one block scans. A decode step of 32 requests
 // takes MEASURED_SELF us with a plan of its own, and MEASURED_PLAN us with the
 // plan's kernel.
 inline bool self_planned(int N, int T, int G, int max_new_tokens) {
   const int64_t longest = N == 1 ? T : max_new_tokens;
-  return N <= 1024 && longest * G <= split_rows(G);
+  return N <= kSelfPlan && longest * G <= split_rows(G);
 }
 
 // CTAs of the split kernel: one wave.

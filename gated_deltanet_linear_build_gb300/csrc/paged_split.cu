@@ -186,35 +186,100 @@ __device__ void build_list(const PlanArgs& p, const ListArgs& a, int2* sums, int
   items = min(items, a.cap);
 }
 
-// Every CTA's piece of the line, of at least `least` units.
-__device__ void cut_line(const PlanArgs& p, const ListArgs& a, const int* s_cum, int num, int units) {
-  const int64_t all = (int64_t)units * p.Hk;
-  const int per_cta = (int)max((int64_t)a.least, (all + a.grid - 1) / a.grid);
+// The line is cut in one of two ways. Into equal pieces, which may end inside an
+// item and go on with the next: no SM is idle. Or, where items are no more than
+// half as many as CTAs, each item by itself into pieces of about `target` units:
+// a piece then is one segment, and each segment costs 4 us of latency (a CTA
+// with two held up a step of one 16,000-token request by 4 of 10 us). With
+// target >= all / (grid - items) the pieces are no more than the CTAs.
+struct Cut {
+  int per_cta, target;                 // target 0: equal pieces
+};
+__device__ __forceinline__ Cut cut_of(long long all, long long items, int grid, int least) {
+  Cut c;
+  c.per_cta = (int)max((long long)least, (all + grid - 1) / grid);
+  c.target = 0;
+  if (2 * items <= grid) c.target = (int)max((long long)least, (all + grid - items - 1) / (grid - items));
+  return c;
+}
+// Piece k of the n that an item of `units` units is cut into.
+__device__ __forceinline__ void piece_of(Start& at, int c, int k, int n) {
+  const int from = (int)((long long)at.it.units * k / n), to = (int)((long long)at.it.units * (k + 1) / n);
+  at.u = (long long)at.head * at.units + at.it.cum + from;
+  at.count = to - from;
+  at.c0 = c - k;
+  at.pieces = n;
+}
+__device__ __forceinline__ void piece_of_line(Start& at, int per_cta) {
+  const long long at0 = (long long)at.head * at.units + at.it.cum;
+  at.c0 = (int)(at0 / per_cta);
+  at.pieces = (int)((at0 + at.it.units - 1) / per_cta) - at.c0 + 1;
+}
+// Largest i < num with cum[i] <= x.
+template <typename F>
+__device__ __forceinline__ int find_item(int num, int x, F cum) {
+  int lo = 0, hi = num - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cum(mid) <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Every CTA's piece of the list's line. s_cum holds the units before each of the
+// first kPlanThreads items; s_pieces is room for as many.
+__device__ void cut_line(const PlanArgs& p, const ListArgs& a, const int* s_cum, int* s_pieces, int2* sums,
+                         int num, int units) {
+  const long long all = (long long)units * p.Hk;
+  const Cut cut = cut_of(all, (long long)num * p.Hk, a.grid, a.least);
   __syncthreads();                              // the list is written
+  int pieces = 0;                               // of one head
+  if (cut.target) {
+    const int n = threadIdx.x < num ? (a.items[threadIdx.x].units + cut.target - 1) / cut.target : 0;
+    int2 tot;
+    const int2 inc = block_scan(make_int2(n, 0), sums, tot);
+    s_pieces[threadIdx.x] = inc.x - n;
+    pieces = tot.x;
+    __syncthreads();
+  }
   for (int c = threadIdx.x; c < a.grid; c += kPlanThreads) {
     Start at;
-    at.u = min((long long)all, (long long)c * per_cta);
-    at.u_end = min((long long)all, at.u + per_cta);
-    at.item = at.head = 0;
+    at.u = all;
+    at.item = at.head = at.count = at.pieces = at.first = at.len = at.kv = at.c0 = 0;
     at.num_items = num;
     at.units = units;
-    at.per_cta = per_cta;
     at.it = {0, 0, 0, 0};
-    at.first = at.len = at.kv = 0;
-    if (at.u < all) {
-      at.head = (int)((unsigned long long)at.u / (unsigned)units);
-      const int x = (int)(at.u - (int64_t)at.head * units);
-      int lo = 0, hi = num - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if ((num <= kPlanThreads ? s_cum[mid] : a.items[mid].cum) <= x) lo = mid; else hi = mid - 1;
+    int y = 0;
+    bool work;
+    if (cut.target) {
+      work = pieces > 0 && c < pieces * p.Hk;
+      if (work) {
+        at.head = c / pieces;
+        y = c - at.head * pieces;
+        at.item = find_item(num, y, [&](int i) { return s_pieces[i]; });
       }
-      at.item = lo;
-      at.it = a.items[lo];
+    } else {
+      at.u = min(all, (long long)c * cut.per_cta);
+      at.count = (int)(min(all, at.u + cut.per_cta) - at.u);
+      work = at.count > 0;
+      if (work) {
+        at.head = (int)((unsigned long long)at.u / (unsigned)units);
+        const int x = (int)(at.u - (long long)at.head * units);
+        at.item = find_item(num, x, [&](int i) { return num <= kPlanThreads ? s_cum[i] : a.items[i].cum; });
+      }
+    }
+    if (work) {
+      at.it = a.items[at.item];
       const Seq s = seq_of(p.cu, p.kv, at.it.seq, p.T, p.kv_max);
       at.first = s.first;
       at.len = s.len;
       at.kv = s.kv;
+      if (cut.target) {
+        const int k = y - s_pieces[at.item];
+        piece_of(at, c, k, (at.it.units + cut.target - 1) / cut.target);
+      } else {
+        piece_of_line(at, cut.per_cta);
+      }
     }
     a.starts[c] = at;
   }
@@ -277,15 +342,16 @@ __device__ void deal_starts(const PlanArgs& p, const ListArgs& a, int num) {
   for (int c = threadIdx.x; c < a.grid; c += kPlanThreads) {
     Start at;
     at.num_items = num;
-    at.units = at.per_cta = 0;
+    at.units = at.pieces = 0;
     at.u = 0;
+    at.c0 = -1;
     // Rounds in which this CTA has an item.
     const int64_t full = total / a.grid;
     const int rest = (int)(total - full * a.grid);
-    at.u_end = full + (((full & 1) ? a.grid - 1 - c : c) < rest ? 1 : 0);
+    at.count = (int)full + (((full & 1) ? a.grid - 1 - c : c) < rest ? 1 : 0);
     at.it = {0, 0, 0, 0};
     at.item = at.head = at.first = at.len = at.kv = 0;
-    if (at.u_end > 0) {
+    if (at.count > 0) {
       at.item = c / p.Hk;
       at.head = c - at.item * p.Hk;
       at.it = a.sorted[at.item];
@@ -310,7 +376,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
     int items, units;
     build_list(p, a, sums, s_first, s_cum, items, units);
     if (a.sorted && deal_items(p, a, sums, s_first, items, units)) deal_starts(p, a, items);
-    else cut_line(p, a, s_cum, items, units);
+    else cut_line(p, a, s_cum, s_first, sums, items, units);
     __syncthreads();                            // s_cum is free again
   }
 }
@@ -355,7 +421,6 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 // Split kernel
 // ---------------------------------------------------------------------------
 constexpr int kWarps = 8;
-constexpr int kSelfPlan = 1024;          // sequences that a CTA plans itself
 constexpr int kJoinThreads = 256;
 
 template <int D, int QM>
@@ -384,8 +449,8 @@ struct Cfg {
   static constexpr int o_nan = o_l + rows * 2 * 4;
   static constexpr int o_bar = o_nan + D * 4;
   static constexpr int o_flag = o_bar + kWarps * slots * 8;
-  static constexpr int o_cum = o_flag + 16;            // units before each sequence (self plan)
-  static constexpr int total = o_cum + (kSelfPlan + 1) * 4;
+  static constexpr int o_cum = o_flag + 16;            // units and pieces before each sequence (self plan)
+  static constexpr int total = o_cum + (2 * kSelfPlan + 1) * 4;
 };
 
 // The K rows of an MMA's 8 columns and the V rows of its k index are free to
@@ -482,10 +547,12 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
   int* s_cum = reinterpret_cast<int*>(smem + C::o_cum);
   if (p.self_plan) {
     // One tile a sequence: every CTA forms the line itself (one round of loads and
-    // a scan), which is sooner than a kernel before this one.
+    // a scan or two), which is sooner than a kernel before this one.
     int2* sums = reinterpret_cast<int2*>(s_ml);
+    int* s_pieces = s_cum + kSelfPlan + 1;
     constexpr int per = kSelfPlan / (kWarps * 32);
-    int u4[per], mine = 0;
+    int u4[per];
+    int2 mine = make_int2(0, 0), total;
 #pragma unroll
     for (int k = 0; k < per; ++k) {
       const int n = tid * per + k;
@@ -494,52 +561,87 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         const Seq q = seq_of(p.cu, p.kv, n, p.T, (int64_t)p.max_blocks << p.log_b);
         if (q.len > 0) u4[k] = max(1, (visible(q, q.len - 1) + kUnit - 1) / kUnit);
       }
-      mine += u4[k];
+      mine.x += u4[k];
+      mine.y += u4[k] > 0;
     }
-    int inc = mine;
+    // Exclusive sums of a pair over the block.
+    auto scan = [&](int2 v, int2& tot) {
+      int2 inc = v;
 #pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, k);
-      if (lane >= k) inc += v;
-    }
-    if (lane == 31) sums[w].x = inc;
-    __syncthreads();
-    int before = inc - mine, total = 0;
+      for (int k = 1; k < 32; k <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc.x, k), y = __shfl_up_sync(0xffffffffu, inc.y, k);
+        if (lane >= k) { inc.x += x; inc.y += y; }
+      }
+      __syncthreads();
+      if (lane == 31) sums[w] = inc;
+      __syncthreads();
+      int2 before = make_int2(inc.x - v.x, inc.y - v.y);
+      tot = make_int2(0, 0);
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      if (k < w) before += sums[k].x;
-      total += sums[k].x;
-    }
+      for (int k = 0; k < kWarps; ++k) {
+        if (k < w) { before.x += sums[k].x; before.y += sums[k].y; }
+        tot.x += sums[k].x;
+        tot.y += sums[k].y;
+      }
+      return before;
+    };
+    int before = scan(mine, total).x;
 #pragma unroll
     for (int k = 0; k < per; ++k) {
       s_cum[tid * per + k] = before;
       before += u4[k];
     }
-    if (tid == 0) s_cum[kSelfPlan] = total;
-    __syncthreads();
-    const long long all = (long long)total * p.Hk;
-    start.num_items = p.N;
-    start.units = total;
-    start.per_cta = (int)max((long long)kWarps, (all + gridDim.x - 1) / gridDim.x);
-    start.u = min(all, (long long)blockIdx.x * start.per_cta);
-    start.u_end = min(all, start.u + start.per_cta);
-    start.item = start.head = 0;
-    start.it = {0, 0, 0, 0};
-    start.first = start.len = start.kv = 0;
-    if (start.u < start.u_end) {
-      start.head = (int)((unsigned long long)start.u / (unsigned)total);
-      const int x = (int)(start.u - (long long)start.head * total);
-      int lo = 0, hi = p.N - 1;          // last sequence that begins at or before x
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s_cum[mid] <= x) lo = mid; else hi = mid - 1;
+    if (tid == 0) s_cum[kSelfPlan] = total.x;
+    const long long all = (long long)total.x * p.Hk;
+    const Cut cut = cut_of(all, (long long)total.y * p.Hk, gridDim.x, kWarps);
+    int pieces = 0;                      // of one head
+    if (cut.target) {
+      int2 n = make_int2(0, 0), tot;
+#pragma unroll
+      for (int k = 0; k < per; ++k) n.x += (u4[k] + cut.target - 1) / cut.target;
+      before = scan(n, tot).x;
+#pragma unroll
+      for (int k = 0; k < per; ++k) {
+        s_pieces[tid * per + k] = before;
+        before += (u4[k] + cut.target - 1) / cut.target;
       }
-      start.item = lo;
-      start.it = {lo, 0, s_cum[lo + 1] - s_cum[lo], s_cum[lo]};
-      const Seq q = seq_of(p.cu, p.kv, lo, p.T, (int64_t)p.max_blocks << p.log_b);
+      pieces = tot.x;
+    }
+    __syncthreads();
+    const int c = blockIdx.x;
+    start.num_items = p.N;
+    start.units = total.x;
+    start.u = all;
+    start.item = start.head = start.count = start.pieces = start.first = start.len = start.kv = start.c0 = 0;
+    start.it = {0, 0, 0, 0};
+    int y = 0;
+    bool work;
+    if (cut.target) {
+      work = pieces > 0 && c < pieces * p.Hk;
+      if (work) {
+        start.head = c / pieces;
+        y = c - start.head * pieces;
+        start.item = find_item(p.N, y, [&](int i) { return s_pieces[i]; });
+      }
+    } else {
+      start.u = min(all, (long long)c * cut.per_cta);
+      start.count = (int)(min(all, start.u + cut.per_cta) - start.u);
+      work = start.count > 0;
+      if (work) {
+        start.head = (int)((unsigned long long)start.u / (unsigned)total.x);
+        start.item = find_item(p.N, (int)(start.u - (long long)start.head * total.x),
+                               [&](int i) { return s_cum[i]; });
+      }
+    }
+    if (work) {
+      const int i = start.item;
+      start.it = {i, 0, s_cum[i + 1] - s_cum[i], s_cum[i]};
+      const Seq q = seq_of(p.cu, p.kv, i, p.T, (int64_t)p.max_blocks << p.log_b);
       start.first = q.first;
       start.len = q.len;
       start.kv = q.kv;
+      if (cut.target) piece_of(start, c, y - s_pieces[i], (start.it.units + cut.target - 1) / cut.target);
+      else piece_of_line(start, cut.per_cta);
     }
     if (tid < 4)                         // for the joining kernel
       reinterpret_cast<int4*>(p.starts + blockIdx.x)[tid] = reinterpret_cast<const int4*>(&start)[tid];
@@ -548,7 +650,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
   }
   const int num_items = start.num_items, units1 = start.units;
   long long u = start.u;
-  const long long u_end = start.u_end;
+  const long long u_end = u + start.count;
   int lo = start.item, head = start.head;
   Item it = start.it;
   Seq s = {start.first, start.len, start.kv};
@@ -1002,6 +1104,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_split_join_kernel(const Arg
   __shared__ float s_l[rows];
   __shared__ float4 s_o[groups][lanes];
   __shared__ int s_count[kJoinThreads / 32], s_c0;
+  __shared__ Start s_next;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -1010,12 +1113,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_split_join_kernel(const Arg
   for (int base = 0; base + 1 < pieces; base += kJoinThreads) {
     const int c = base + tid;
     bool cut = false;
+    Start next;
     if (c + 1 < pieces) {
-      const Start next = read_start(p.starts + c + 1);
-      if (next.u < next.u_end) {
-        const long long at0 = (long long)next.head * next.units + next.it.cum;
-        cut = at0 != next.u && at0 / next.per_cta == c;
-      }
+      next = read_start(p.starts + c + 1);
+      cut = next.count > 0 && next.c0 == c && next.u != (long long)next.head * next.units + next.it.cum;
     }
     const unsigned vote = __ballot_sync(0xffffffffu, cut);
     if (lane == 0) s_count[w] = __popc(vote);
@@ -1027,7 +1128,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_split_join_kernel(const Arg
       if (k < w) before += s_count[k];
       total += s_count[k];
     }
-    if (cut && before == left) s_c0 = c;
+    if (cut && before == left) {
+      s_c0 = c;
+      s_next = next;
+    }
     __syncthreads();
     c0 = s_c0;
     if (c0 >= 0) break;
@@ -1035,9 +1139,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_split_join_kernel(const Arg
     __syncthreads();
   }
   if (c0 < 0) return;
-  const Start next = read_start(p.starts + c0 + 1);
-  const long long at0 = (long long)next.head * next.units + next.it.cum;
-  const int n = (int)((at0 + next.it.units - 1) / next.per_cta) - c0 + 1;
+  const Start& next = s_next;
+  const int n = next.pieces;
   const float* base = p.partials + ((size_t)c0 * 2 + 1) * (rows * (D + 2));
   auto part = [&](int c) { return base + (c == 0 ? 0 : (size_t)(2 * c - 1) * (rows * (D + 2))); };
   const int group = tid / lanes, from = n * group / groups, to = n * (group + 1) / groups;

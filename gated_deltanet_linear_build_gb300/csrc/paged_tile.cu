@@ -191,11 +191,11 @@ __device__ __forceinline__ Line line_of(const Args& p) {
   l.units1 = at.units;
   l.lo = at.item;
   l.head = at.head;
-  l.deal = at.per_cta == 0 ? 0 : -1;
+  l.deal = at.c0 < 0 ? 0 : -1;
   l.it = at.it;
   l.s = {at.first, at.len, at.kv};
   l.u = at.u;
-  l.u_end = at.u_end;
+  l.u_end = at.u + at.count;
   return l;
 }
 
@@ -807,10 +807,11 @@ __global__ void __launch_bounds__(256) attn_tile_join_kernel(const Args p) {
   const int col0 = (threadIdx.x >> 5) * kCols;
   if (c0 + 1 >= (int)gridDim.x) return;
   const Start next = read_start(p.tile_starts + c0 + 1);
-  if (next.per_cta == 0 || next.u >= next.u_end) return;    // whole items, or no work
-  const long long at0 = (long long)next.head * next.units + next.it.cum;
-  if (at0 == next.u || at0 / next.per_cta != c0) return;    // not cut here, or begun earlier
-  const int c1 = (int)((at0 + next.it.units - 1) / next.per_cta);
+  // Not cut here (whole items, or no work, among others), or begun earlier.
+  if (next.count == 0 || next.c0 != c0 ||
+      next.u == (long long)next.head * next.units + next.it.cum)
+    return;
+  const int c1 = c0 + next.pieces - 1;
   const int G = p.Hq / p.Hk;
   const int row = next.it.row0 + m * 128 + r, tok = row / G;
   if (row >= next.len * G) return;
