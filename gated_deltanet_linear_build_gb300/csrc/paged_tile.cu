@@ -27,8 +27,8 @@
 // leaves float32 partial results, which a second kernel joins in CTA order.
 //
 // Roles (four warpgroups): 0 .. kM - 1: softmax of one 128-row tile each; the
-// others up to 2: Q, widening of V; warp 12: MMAs; warp 13: TMA copies of K, and
-// the blocks' scales; warp 14: TMA copies of V's codes.
+// others up to 2: Q, widening of V; warps 12 and 15: MMAs of a tile each; warp
+// 13: TMA copies of K, and the blocks' scales; warp 14: TMA copies of V's codes.
 // K and V's codes lie as TMA leaves them, rows of 128 (64 for d = 64) bytes
 // with their 16-byte chunks XOR-swizzled; Q and the widened V as 8 x 16-byte
 // core matrices. Copies issued by threads instead (cp.async and register
@@ -79,7 +79,7 @@ struct TC {
   // Exponents of the rows' scales, int8 [2 segments][rows].
   static constexpr int o_ex = o_nan + NR * D * 2;
   static constexpr int o_bar = o_ex + 2 * M * 128;
-  static constexpr int n_bar = 2 * KS + 2 * VR + 2 * VS + 8 + 4 + 4 + 4 + 2 + 2;
+  static constexpr int n_bar = 2 * KS + 2 * VR + 2 * VS + 8 + 4 + 4 + 4 + 2 + 3;
   static constexpr int o_misc = o_bar + n_bar * 8;      // tmem base, abort, flags
   static constexpr int total = o_misc + 32;
   static_assert(total <= 232448, "shared memory of one CTA");
@@ -120,6 +120,25 @@ __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
         "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr) : "memory");
+}
+// 16 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr) : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
@@ -164,6 +183,7 @@ __device__ __forceinline__ bool elect_one() {
 
 // A bounded wait of a whole warp: all lanes go on, or none does.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, mbar_wait_abortable(bar, parity, abort));
 }
 
@@ -310,7 +330,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
   if (tid == 0) {
     for (int i = 0; i < C::KS; ++i) {
       tc::mbar_init(k_full + i, 1);
-      tc::mbar_init(k_empty + i, 1);
+      tc::mbar_init(k_empty + i, kM);
     }
     for (int i = 0; i < C::VR; ++i) {
       tc::mbar_init(vr_full + i, 1);
@@ -318,7 +338,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
     }
     for (int i = 0; i < C::VS; ++i) {
       tc::mbar_init(v_full + i, C::loaders);
-      tc::mbar_init(v_empty + i, 1);
+      tc::mbar_init(v_empty + i, kM);
     }
     for (int i = 0; i < 8; ++i) tc::mbar_init(sc_full + i, 4);
     for (int i = 0; i < 4; ++i) {
@@ -328,7 +348,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
     }
     for (int i = 0; i < 2; ++i) tc::mbar_init(q_full + i, C::loaders);
     tc::mbar_init(nan_sync, C::loaders);
-    tc::mbar_init(drained, 1);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(drained + i, 1);
     *s_abort = 0;
     *s_any_nan = 0;
   }
@@ -347,73 +367,85 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
   if (wg == 3) {
     // ======================= MMA warp ==========================================
     regs_down<C::mma_regs>();
-    // The whole warp walks the role, so that descriptors stay in uniform
-    // registers, and one elected lane issues: 66 cycles per 128 x 128 MMA, the
-    // tensor core's own rate, where a lone lane's loop took above 200.
-    if (warp == 12) {
+    // One warp per 128-row tile. The whole warp walks the role, so that descriptors
+    // stay in uniform registers, and one elected lane issues: 66 cycles per 128 x
+    // 128 MMA, the tensor core's own rate, where a lone lane's loop took above 200.
+    // What the role does beside issuing is the tensor core's idle time: stages and
+    // phases are counted along, not divided out, and two tiles have two warps
+    // (4,096 tokens of 16,384, d = 128: MEASURED_ONE -> MEASURED_TWO us).
+    if (warp == 12 || (kM == 2 && warp == 15)) {
+      const int m = warp == 12 ? 0 : 1;
       const bool one = elect_one();
-      const uint32_t id_qk = idesc_f32(128, kKeys);
-      const uint32_t id_pv = idesc_f32(128, D) | tc::kTransB;
-      const uint32_t sq = tc::smem_u32(smem + C::o_q), sk = tc::smem_u32(smem + C::o_k),
-                     sv = tc::smem_u32(smem + C::o_v);
-      int unit = 0, segs = 0;                  // running counts: stages and phases
+      constexpr uint32_t id_qk = idesc_f32(128, kKeys), id_pv = idesc_f32(128, D) | tc::kTransB;
+      const uint32_t s_buf = tmem + m * 128, o_buf = tmem + C::c_o(0) + m * D;
+      const uint64_t qd = tc::tile_desc(tc::smem_u32(smem + C::o_q) + m * 2 * C::q_part, D / 2, 0);
+      const uint64_t kd = desc_swizzled<C::row>(tc::smem_u32(smem + C::o_k));
+      const uint64_t vd = tc::mn_desc(tc::smem_u32(smem + C::o_v), D, 0);
+      uint64_t* sf = s_full + m * 2;
+      uint64_t* pf = p_full + m * 2;
+      uint64_t* od = o_done + m * 2;
+      // Stages and phases of the next unit to score and the next to add.
+      int ks = 0, vs = 0, s_b = 0, p_b = 0, seg_b = 0;
+      uint32_t kp = 0, vp = 0, pp = 0, qp = 0;
       bool ok = true;
-      // S of unit u for every tile, two units ahead of the softmax.
-      auto qk = [&](int u, int m) {
-        const int st = u % C::KS;
-        if (m == 0) {
-          ok = ok && warp_wait(k_full + st, (u / C::KS) & 1, s_abort);
-          tc::fence_after_sync();
-        }
+      auto qk = [&]() {
+        ok = ok && warp_wait(k_full + ks, kp, s_abort);
+        tc::fence_after_sync();
         if (!ok) return;
-        const uint32_t d = tmem + m * 128 + (u & 1) * 64;
-        const uint64_t b = desc_swizzled<C::row>(sk + st * C::c_stage);
-        const uint64_t a = tc::tile_desc(sq + m * 2 * C::q_part, D / 2, 0);
+        const uint32_t d = s_buf + s_b * 64;
+        const uint64_t b = kd + ks * (C::c_stage / 16);
         if (one) {
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
-              mma_f8(d, a + part * (C::q_part / 16) + k * 16,
+              mma_f8(d, qd + part * (C::q_part / 16) + k * 16,
                      b + (k * 32 / C::row) * (kKeys * C::row / 16) + (k * 32 % C::row) / 16, id_qk,
                      part | k);
-          tc::mma_commit(s_full + m * 2 + (u & 1));
-          if (m == kM - 1) tc::mma_commit(k_empty + st);
+          tc::mma_commit(sf + s_b);
+          tc::mma_commit(k_empty + ks);
+        }
+        s_b ^= 1;
+        if (++ks == C::KS) {
+          ks = 0;
+          kp ^= 1;
         }
       };
       while (ok && l.more()) {
         const Seg g = seg_at(p, l, kRows);
-        ok = ok && warp_wait(q_full + (segs & 1), (segs >> 1) & 1, s_abort);
+        ok = ok && warp_wait(q_full + seg_b, qp, s_abort);
         tc::fence_after_sync();
-        for (int u = 0; ok && u < min(2, g.count); ++u)
+        qp ^= seg_b;
+        seg_b ^= 1;
+        qk();
+        if (g.count > 1) qk();
+        for (int j = 0; ok && j < g.count; ++j) {
+          ok = ok && warp_wait(v_full + vs, vp, s_abort);
+          ok = ok && warp_wait(pf + p_b, pp, s_abort);
+          tc::fence_after_sync();
+          if (!ok) break;
+          const uint32_t at = s_buf + p_b * 64;
+          const uint64_t b = vd + vs * (C::v_stage / 16);
+          if (one) {
 #pragma unroll
-          for (int m = 0; m < kM; ++m) qk(unit + u, m);
-        for (int j = 0; ok && j < g.count; ++j, ++unit) {
-#pragma unroll
-          for (int m = 0; m < kM; ++m) {
-            ok = ok && warp_wait(p_full + m * 2 + (unit & 1), (unit >> 1) & 1, s_abort);
-            const int st = unit % C::VS;
-            if (m == 0) ok = ok && warp_wait(v_full + st, (unit / C::VS) & 1, s_abort);
-            tc::fence_after_sync();
-            if (!ok) break;
-            const uint32_t d = tmem + C::c_o(m), a = tmem + m * 128 + (unit & 1) * 64;
-            const uint64_t b = tc::mn_desc(sv + st * C::v_stage, D, 0);
-            if (one) {
-#pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k)
-                tc::mma_bf16_tmem_a(d, a + k * 8, b + k * 2 * D, id_pv, j > 0 || k > 0);
-              tc::mma_commit(o_done + m * 2 + (unit & 1));
-              if (m == kM - 1) tc::mma_commit(v_empty + st);
-            }
-            if (j + 2 < g.count) qk(unit + 2, m);
+            for (int k = 0; k < kKeys / 16; ++k)
+              tc::mma_bf16_tmem_a(o_buf, at + k * 8, b + k * 2 * D, id_pv, j > 0 || k > 0);
+            tc::mma_commit(od + p_b);
+            tc::mma_commit(v_empty + vs);
           }
+          pp ^= p_b;
+          p_b ^= 1;
+          if (++vs == C::VS) {
+            vs = 0;
+            vp ^= 1;
+          }
+          if (j + 2 < g.count) qk();
         }
-        ++segs;
         pass(p, l, g);
       }
-      // Nothing of this CTA's tensor work is in flight when TMEM is freed.
-      if (one) tc::mma_commit(drained);
-      if (!tc::mbar_wait(drained, 0)) record_device_status(GDN_ERR_TIMEOUT);
+      // Nothing of this warp's tensor work is in flight when TMEM is freed.
+      if (one) tc::mma_commit(drained + m);
+      if (!tc::mbar_wait(drained + m, 0)) record_device_status(GDN_ERR_TIMEOUT);
       __syncwarp();
     } else if (warp == 13 || warp == 14) {
       // ===================== TMA copies ==========================================
@@ -661,14 +693,8 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < g.count; ++j, ++unit) {
         const int buf = m * 2 + (unit & 1);
-        ok = ok && warp_wait(s_full + buf, (unit >> 1) & 1, s_abort);
+        // The unit's scales, long there, before its scores.
         ok = ok && warp_wait(sc_full + (unit & 7), (unit >> 3) & 1, s_abort);
-        if (!ok) break;
-        tc::fence_after_sync();
-        float x[64];
-        const uint32_t ts = tmem + lane_base + m * 128 + (unit & 1) * 64;
-        tmem_ld32_async(ts, x);
-        tmem_ld32_async(ts + 32, x + 32);
         const float* sc = s_sc + (unit & 7) * 12;
         float fa[4], fb[4], fi[4];
         *reinterpret_cast<float4*>(fa) = *reinterpret_cast<const float4*>(sc);
@@ -676,6 +702,13 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         *reinterpret_cast<float4*>(fi) = *reinterpret_cast<const float4*>(sc + 8);
 #pragma unroll
         for (int gr = 0; gr < 4; ++gr) fa[gr] = factor(rs * fa[gr]);
+        ok = ok && warp_wait(s_full + buf, (unit >> 1) & 1, s_abort);
+        if (!ok) break;
+        tc::fence_after_sync();
+        float x[64];
+        const uint32_t ts = tmem + lane_base + m * 128 + (unit & 1) * 64;
+        tmem_ld32_async(ts, x);
+        tmem_ld32_async(ts + 32, x + 32);
         tmem_wait_ld();
         const int key0 = (g.first_unit + j) * kKeys;
         if (part_tile || key0 + kKeys > min_lim) {
@@ -683,58 +716,60 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
           for (int k = 0; k < 64; ++k)
             if (key0 + k >= lim) x[k] = -INFINITY;
         }
-        float mx = -INFINITY;
-#pragma unroll
-        for (int gr = 0; gr < 4; ++gr) {
-          float g0 = x[gr * 16], g1 = x[gr * 16 + 1];
-#pragma unroll
-          for (int k = 2; k < 16; k += 2) {
-            g0 = fmaxf(g0, x[gr * 16 + k]);
-            g1 = fmaxf(g1, x[gr * 16 + k + 1]);
-          }
-          mx = fmaxf(mx, fmaf(fmaxf(g0, g1), fa[gr], fb[gr]));
-        }
-        if (__any_sync(0xffffffffu, mx > m_run + 8.f)) {
-          const float m_new = fmaxf(mx, m_run);
-          const float al = m_new > m_run ? ex2_approx(m_run - m_new) : 1.f;
-          m_run = m_new;
-          l_run *= al;
-          if (j > 0) {
-            // The products of the unit before are in O; this unit's wait for P.
-            ok = ok && warp_wait(o_done + m * 2 + ((unit - 1) & 1), ((unit - 1) >> 1) & 1, s_abort);
-            if (!ok) break;
-            tc::fence_after_sync();
-            const uint32_t to = tmem + lane_base + C::c_o(m);
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float v[32];
-              tmem_ld32_async(to + c, v);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] *= al;
-              tmem_st32_async(to + c, reinterpret_cast<uint32_t*>(v));
-            }
-            tmem_wait_st();
-          }
-        }
-        const float ref = (m_run == -INFINITY ? 0.f : m_run) - 7.f;
+        // The weights on the running maximum as it was, beside this unit's maximum:
+        // neither waits for the other. Where the maximum grew by more than 2^8 (the
+        // first unit, and few others), once more on the new one.
         uint32_t pk[32];
-        float lsum = 0.f;
+        float lsum;
+        bool again;
+#pragma unroll 1
+        do {
+          const float ref = (m_run == -INFINITY ? 0.f : m_run) - 7.f;
+          float mx = -INFINITY;
+          lsum = 0.f;
 #pragma unroll
-        for (int gr = 0; gr < 4; ++gr) {
-          const float2 a2 = make_float2(fa[gr], fa[gr]), b2 = make_float2(fb[gr] - ref, fb[gr] - ref);
-          float2 sum = make_float2(0.f, 0.f);
+          for (int gr = 0; gr < 4; ++gr) {
+            const float* y = x + gr * 16;
+            const float2 a2 = make_float2(fa[gr], fa[gr]), b2 = make_float2(fb[gr] - ref, fb[gr] - ref);
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float2 v = fma2(make_float2(x[gr * 16 + 2 * k], x[gr * 16 + 2 * k + 1]), a2, b2);
-            v.x = ex2_approx(v.x);
-            v.y = ex2_approx(v.y);
-            sum = add2(sum, v);
-            const __half2 h = __floats2half2_rn(v.x, v.y);
-            pk[gr * 8 + k] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int k = 0; k < 8; ++k) {
+              float2 v = fma2(make_float2(y[2 * k], y[2 * k + 1]), a2, b2);
+              v.x = ex2_approx(v.x);
+              v.y = ex2_approx(v.y);
+              sum = add2(sum, v);
+              const __half2 h = __floats2half2_rn(v.x, v.y);
+              pk[gr * 8 + k] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            lsum = fmaf(sum.x + sum.y, fi[gr], lsum);
+            const float t0 = max3(y[0], y[1], y[2]), t1 = max3(y[3], y[4], y[5]), t2 = max3(y[6], y[7], y[8]),
+                        t3 = max3(y[9], y[10], y[11]), t4 = max3(y[12], y[13], y[14]);
+            mx = fmaxf(mx, fmaf(max3(max3(t0, t1, t2), max3(t3, t4, y[15]), -INFINITY), fa[gr], fb[gr]));
           }
-          lsum = fmaf(sum.x + sum.y, fi[gr], lsum);
-        }
+          again = __any_sync(0xffffffffu, mx > m_run + 8.f);
+          if (again) {
+            const float m_new = fmaxf(mx, m_run);
+            const float al = m_new > m_run ? ex2_approx(m_run - m_new) : 1.f;
+            m_run = m_new;
+            l_run *= al;
+            if (j > 0) {
+              // The products of the unit before are in O; this unit's wait for P.
+              ok = warp_wait(o_done + m * 2 + ((unit - 1) & 1), ((unit - 1) >> 1) & 1, s_abort);
+              if (!ok) break;
+              tc::fence_after_sync();
+              const uint32_t to = tmem + lane_base + C::c_o(m);
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                float v[16];
+                tmem_ld16(to + c, v);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] *= al;
+                tc::tmem_st16(to + c, *reinterpret_cast<uint32_t(*)[16]>(v));
+              }
+            }
+          }
+        } while (again);
+        if (!ok) break;
         l_run += lsum;
         tmem_st32_async(ts, pk);
         tmem_wait_st();
