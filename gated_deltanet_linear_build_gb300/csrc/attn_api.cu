@@ -275,7 +275,8 @@ gdn_status_t gdn_paged_attention(const void* q, int64_t q_stride, const void* k_
   a.tile_partials = reinterpret_cast<float*>(ws + l.tile_partials);
   // The two kernels share a step's sequences by their rows; a step whose
   // lengths rule one of them out launches the other alone.
-  const attn::Kernels use = attn::kernels_of(N, T, Hq / Hk, max_new_tokens);
+  const attn::Kernels use =
+      attn::kernels_of(N, T, Hq / Hk, Hk, max_new_tokens, (int64_t)max_blocks * block_tokens);
   if (use.split) rc = launch_attn_split(a, st);
   if (rc == GDN_OK && use.tile) rc = launch_attn_tile(a, st);
   return rc;

@@ -49,14 +49,24 @@ inline int tile_grid() { return num_sms() < 160 ? num_sms() : 160; }
 // Sequences of at most this many rows (new tokens x G) go to the split kernel.
 inline int split_limit(int G) { return 64; }
 
-// Which kernels a step's lengths leave work for. One sequence is exactly as
-// long as the step.
+// Which kernels a step's lengths leave work for, and the most rows that go to the
+// split kernel. One sequence is exactly as long as the step. A step with longer
+// sequences whose short ones cannot hold up the tensor-core kernel (all of them
+// with full tables are two units an SM at most) leaves the split kernel out: two
+// launches with next to nothing to do are 5 us.
 struct Kernels {
   bool split, tile;
+  int limit;
 };
-inline Kernels kernels_of(int N, int T, int G, int max_new_tokens) {
-  const int64_t longest = N == 1 ? T : max_new_tokens, limit = split_limit(G);
-  return {!(N == 1 && longest * G > limit), longest * G > limit};
+inline Kernels kernels_of(int N, int T, int G, int Hk, int max_new_tokens, int64_t kv_max) {
+  const int64_t longest = N == 1 ? T : max_new_tokens;
+  Kernels k = {true, longest * G > split_limit(G), split_limit(G)};
+  const int64_t short_units = (int64_t)N * Hk * ((kv_max + kTileKeys - 1) / kTileKeys);
+  if (k.tile && (N == 1 || short_units <= 2 * tile_grid())) {
+    k.split = false;
+    k.limit = 0;
+  }
+  return k;
 }
 constexpr int kSelfPlan = 512;
 // Whether the split kernel's CTAs can plan the step by themselves: one tile a

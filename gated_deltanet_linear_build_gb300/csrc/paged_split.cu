@@ -95,6 +95,21 @@ struct PlanArgs {
   ListArgs list[2];                    // split kernel, tensor-core kernel
 };
 
+// A list's first kPlanThreads items stay here: the plan's steps follow one another
+// through global memory at 0.4 us each otherwise (2,048 tokens in 4 prompts: 7.9
+// us).
+struct PlanShared {
+  int2 sums[32];
+  int first[kPlanThreads];
+  Item items[kPlanThreads], sorted[kPlanThreads];
+};
+__device__ __forceinline__ Item item_at(const PlanShared& sh, const ListArgs& a, int i) {
+  return i < kPlanThreads ? sh.items[i] : a.items[i];
+}
+__device__ __forceinline__ Item sorted_at(const PlanShared& sh, const ListArgs& a, int i) {
+  return i < kPlanThreads ? sh.sorted[i] : a.sorted[i];
+}
+
 // Inclusive scan of a pair over the block; the total in tot.
 __device__ __forceinline__ int2 block_scan(int2 v, int2* sums, int2& tot) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -128,9 +143,10 @@ __device__ __forceinline__ Item item_of(const PlanArgs& p, const ListArgs& a, co
   return it;
 }
 
-__device__ void build_list(const PlanArgs& p, const ListArgs& a, int2* sums, int* s_first,
-                           int* s_cum, int& items, int& units) {
+__device__ void build_list(const PlanArgs& p, const ListArgs& a, PlanShared& sh, int& items, int& units) {
   const int tid = threadIdx.x;
+  int2* sums = sh.sums;
+  int* s_first = sh.first;
   items = units = 0;
   for (int n0 = 0; n0 < p.N; n0 += kPlanThreads) {
     int tiles = 0;
@@ -150,7 +166,7 @@ __device__ void build_list(const PlanArgs& p, const ListArgs& a, int2* sums, int
       const int at = items + inc.x - 1;
       if (tiles && at < a.cap) {
         a.items[at] = it;
-        if (at < kPlanThreads) s_cum[at] = it.cum;
+        if (at < kPlanThreads) sh.items[at] = it;
       }
       items += tot.x;
       units += tot.y;
@@ -176,7 +192,7 @@ __device__ void build_list(const PlanArgs& p, const ListArgs& a, int2* sums, int
       it.cum = units + cum.y - it.units;
       if (i < tot.x && items + i < a.cap) {
         a.items[items + i] = it;
-        if (items + i < kPlanThreads) s_cum[items + i] = it.cum;
+        if (items + i < kPlanThreads) sh.items[items + i] = it;
       }
       units += tot_units.y;
     }
@@ -226,16 +242,16 @@ __device__ __forceinline__ int find_item(int num, int x, F cum) {
   return lo;
 }
 
-// Every CTA's piece of the list's line. s_cum holds the units before each of the
-// first kPlanThreads items; s_pieces is room for as many.
-__device__ void cut_line(const PlanArgs& p, const ListArgs& a, const int* s_cum, int* s_pieces, int2* sums,
-                         int num, int units) {
+// Every CTA's piece of the list's line.
+__device__ void cut_line(const PlanArgs& p, const ListArgs& a, PlanShared& sh, int num, int units) {
+  int2* sums = sh.sums;
+  int* s_pieces = sh.first;
   const long long all = (long long)units * p.Hk;
   const Cut cut = cut_of(all, (long long)num * p.Hk, a.grid, a.least);
   __syncthreads();                              // the list is written
   int pieces = 0;                               // of one head
   if (cut.target) {
-    const int n = threadIdx.x < num ? (a.items[threadIdx.x].units + cut.target - 1) / cut.target : 0;
+    const int n = threadIdx.x < num ? (sh.items[threadIdx.x].units + cut.target - 1) / cut.target : 0;
     int2 tot;
     const int2 inc = block_scan(make_int2(n, 0), sums, tot);
     s_pieces[threadIdx.x] = inc.x - n;
@@ -265,11 +281,11 @@ __device__ void cut_line(const PlanArgs& p, const ListArgs& a, const int* s_cum,
       if (work) {
         at.head = (int)((unsigned long long)at.u / (unsigned)units);
         const int x = (int)(at.u - (long long)at.head * units);
-        at.item = find_item(num, x, [&](int i) { return num <= kPlanThreads ? s_cum[i] : a.items[i].cum; });
+        at.item = find_item(num, x, [&](int i) { return item_at(sh, a, i).cum; });
       }
     }
     if (work) {
-      at.it = a.items[at.item];
+      at.it = item_at(sh, a, at.item);
       const Seq s = seq_of(p.cu, p.kv, at.it.seq, p.T, p.kv_max);
       at.first = s.first;
       at.len = s.len;
@@ -291,13 +307,15 @@ __device__ void cut_line(const PlanArgs& p, const ListArgs& a, const int* s_cum,
 // kItemCost units more (Q, the first scores, the results) and a cut kCutCost.
 // (2,048 tokens in 4 prompts, d = 256: measured figures stand at the kernel.)
 constexpr int kItemCost = 5, kCutCost = 16, kMaxRounds = 12;
-__device__ bool deal_items(const PlanArgs& p, const ListArgs& a, int2* sums, int* s_hist, int num, int units) {
+__device__ bool deal_items(const PlanArgs& p, const ListArgs& a, PlanShared& sh, int num, int units) {
+  int2* sums = sh.sums;
+  int* s_hist = sh.first;
   const int tid = threadIdx.x;
   const int64_t total = (int64_t)num * p.Hk;
   // Counting sort by length, in kPlanThreads classes up to the longest.
   __syncthreads();                              // the list is written
   int longest = 1;
-  for (int i = tid; i < num; i += kPlanThreads) longest = max(longest, a.items[i].units);
+  for (int i = tid; i < num; i += kPlanThreads) longest = max(longest, item_at(sh, a, i).units);
   s_hist[tid] = 0;
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, k));
@@ -307,7 +325,7 @@ __device__ bool deal_items(const PlanArgs& p, const ListArgs& a, int2* sums, int
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, k));
   auto cls = [&](int u) { return (int)((int64_t)(longest - u) * (kPlanThreads - 1) / longest); };
-  for (int i = tid; i < num; i += kPlanThreads) atomicAdd(s_hist + cls(a.items[i].units), 1);
+  for (int i = tid; i < num; i += kPlanThreads) atomicAdd(s_hist + cls(item_at(sh, a, i).units), 1);
   __syncthreads();
   const int mine = s_hist[tid];
   int2 tot;
@@ -315,8 +333,10 @@ __device__ bool deal_items(const PlanArgs& p, const ListArgs& a, int2* sums, int
   s_hist[tid] = inc.x - mine;
   __syncthreads();
   for (int i = tid; i < num; i += kPlanThreads) {
-    const Item it = a.items[i];
-    a.sorted[atomicAdd(s_hist + cls(it.units), 1)] = it;
+    const Item it = item_at(sh, a, i);
+    const int at = atomicAdd(s_hist + cls(it.units), 1);
+    a.sorted[at] = it;
+    if (at < kPlanThreads) sh.sorted[at] = it;
   }
   __syncthreads();
   if (total > (int64_t)kMaxRounds * a.grid) return true;        // many: any deal is even
@@ -324,7 +344,7 @@ __device__ bool deal_items(const PlanArgs& p, const ListArgs& a, int2* sums, int
   if (tid < a.grid)
     for (int k = 0; k < kMaxRounds; ++k) {
       const int at = k * a.grid + ((k & 1) ? a.grid - 1 - tid : tid);
-      if (at < total) load += a.sorted[at / p.Hk].units + kItemCost;
+      if (at < total) load += sorted_at(sh, a, at / p.Hk).units + kItemCost;
     }
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) load = max(load, __shfl_xor_sync(0xffffffffu, load, k));
@@ -337,7 +357,7 @@ __device__ bool deal_items(const PlanArgs& p, const ListArgs& a, int2* sums, int
   return load <= even;
 }
 
-__device__ void deal_starts(const PlanArgs& p, const ListArgs& a, int num) {
+__device__ void deal_starts(const PlanArgs& p, const ListArgs& a, const PlanShared& sh, int num) {
   const int64_t total = (int64_t)num * p.Hk;
   for (int c = threadIdx.x; c < a.grid; c += kPlanThreads) {
     Start at;
@@ -354,7 +374,7 @@ __device__ void deal_starts(const PlanArgs& p, const ListArgs& a, int num) {
     if (at.count > 0) {
       at.item = c / p.Hk;
       at.head = c - at.item * p.Hk;
-      at.it = a.sorted[at.item];
+      at.it = sorted_at(sh, a, at.item);
       const Seq s = seq_of(p.cu, p.kv, at.it.seq, p.T, p.kv_max);
       at.first = s.first;
       at.len = s.len;
@@ -365,8 +385,7 @@ __device__ void deal_starts(const PlanArgs& p, const ListArgs& a, int num) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs p) {
-  __shared__ int2 sums[32];
-  __shared__ int s_first[kPlanThreads], s_cum[kPlanThreads];
+  __shared__ PlanShared sh;
   pdl_wait();
   pdl_trigger();
 #pragma unroll 1
@@ -374,10 +393,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
     const ListArgs& a = p.list[k];
     if (a.grid == 0) continue;                  // that kernel has no sequence in this step
     int items, units;
-    build_list(p, a, sums, s_first, s_cum, items, units);
-    if (a.sorted && deal_items(p, a, sums, s_first, items, units)) deal_starts(p, a, items);
-    else cut_line(p, a, s_cum, s_first, sums, items, units);
-    __syncthreads();                            // s_cum is free again
+    build_list(p, a, sh, items, units);
+    if (a.sorted && deal_items(p, a, sh, items, units)) deal_starts(p, a, sh, items);
+    else cut_line(p, a, sh, items, units);
+    __syncthreads();                            // sh is free again
   }
 }
 
@@ -1251,8 +1270,9 @@ gdn_status_t launch_attn_plan(const int32_t* cu, const int32_t* kv, int N, int T
                               int d, int64_t kv_max, int max_new_tokens, void* workspace,
                               cudaStream_t st) {
   const Layout l = layout(T, N, Hq, Hk, d);
-  const int G = Hq / Hk, limit = split_limit(G);
-  const Kernels use = kernels_of(N, T, G, max_new_tokens);
+  const int G = Hq / Hk;
+  const Kernels use = kernels_of(N, T, G, Hk, max_new_tokens, kv_max);
+  const int limit = use.limit;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   PlanArgs p;
   p.cu = cu;
