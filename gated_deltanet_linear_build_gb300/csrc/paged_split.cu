@@ -78,10 +78,8 @@ using namespace attn;
 // ---------------------------------------------------------------------------
 // Plan: the row tiles of the step, in sequence order, with the running sum of
 // their kv units, and the pieces that the line of units is cut into. One CTA:
-// latency bounds it (two rounds of dependent loads and a scan each), so a list
-// that fits (up to 1,024 tiles, every decode step) stays in shared memory.
+// latency bounds it (two rounds of dependent loads and a scan each).
 // ---------------------------------------------------------------------------
-constexpr int kPlanThreads = 1024;
 
 struct ListArgs {
   int rows, keys, above, upto, cap, grid, least;   // tiles of the sequences with above < rows <= upto
@@ -98,20 +96,25 @@ struct PlanArgs {
 // A list's first kPlanThreads items stay here: the plan's steps follow one another
 // through global memory at 0.4 us each otherwise (2,048 tokens in 4 prompts: 7.9
 // us).
+template <int kPlanThreads>
 struct PlanShared {
   int2 sums[32];
   int first[kPlanThreads];
   Item items[kPlanThreads], sorted[kPlanThreads];
 };
-__device__ __forceinline__ Item item_at(const PlanShared& sh, const ListArgs& a, int i) {
+template <int kPlanThreads>
+__device__ __forceinline__ Item item_at(const PlanShared<kPlanThreads>& sh, const ListArgs& a, int i) {
   return i < kPlanThreads ? sh.items[i] : a.items[i];
 }
-__device__ __forceinline__ Item sorted_at(const PlanShared& sh, const ListArgs& a, int i) {
+template <int kPlanThreads>
+__device__ __forceinline__ Item sorted_at(const PlanShared<kPlanThreads>& sh, const ListArgs& a, int i) {
   return i < kPlanThreads ? sh.sorted[i] : a.sorted[i];
 }
 
 // Inclusive scan of a pair over the block; the total in tot.
+template <int kPlanThreads>
 __device__ __forceinline__ int2 block_scan(int2 v, int2* sums, int2& tot) {
+  constexpr int kLast = kPlanThreads / 32 - 1;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -121,14 +124,15 @@ __device__ __forceinline__ int2 block_scan(int2 v, int2* sums, int2& tot) {
   __syncthreads();                     // earlier readers of sums are done
   if (lane == 31) sums[w] = v;
   __syncthreads();
-  int2 s = sums[lane];                 // every warp scans the warps' sums itself
+  // Every warp scans the warps' sums itself.
+  int2 s = lane <= kLast ? sums[lane] : make_int2(0, 0);
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int a = __shfl_up_sync(0xffffffffu, s.x, d), b = __shfl_up_sync(0xffffffffu, s.y, d);
     if (lane >= d) { s.x += a; s.y += b; }
   }
-  tot.x = __shfl_sync(0xffffffffu, s.x, 31);
-  tot.y = __shfl_sync(0xffffffffu, s.y, 31);
+  tot.x = __shfl_sync(0xffffffffu, s.x, kLast);
+  tot.y = __shfl_sync(0xffffffffu, s.y, kLast);
   const int bx = __shfl_sync(0xffffffffu, s.x, (w + 31) & 31), by = __shfl_sync(0xffffffffu, s.y, (w + 31) & 31);
   if (w > 0) { v.x += bx; v.y += by; }
   return v;
@@ -143,7 +147,8 @@ __device__ __forceinline__ Item item_of(const PlanArgs& p, const ListArgs& a, co
   return it;
 }
 
-__device__ void build_list(const PlanArgs& p, const ListArgs& a, PlanShared& sh, int& items, int& units) {
+template <int kPlanThreads>
+__device__ void build_list(const PlanArgs& p, const ListArgs& a, PlanShared<kPlanThreads>& sh, int& items, int& units) {
   const int tid = threadIdx.x;
   int2* sums = sh.sums;
   int* s_first = sh.first;
@@ -161,7 +166,7 @@ __device__ void build_list(const PlanArgs& p, const ListArgs& a, PlanShared& sh,
       Item it = {0, 0, 0, 0};
       if (tiles) it = item_of(p, a, s, n0 + tid, 0);
       int2 tot;
-      const int2 inc = block_scan(make_int2(tiles, it.units), sums, tot);
+      const int2 inc = block_scan<kPlanThreads>(make_int2(tiles, it.units), sums, tot);
       it.cum = units + inc.y - it.units;
       const int at = items + inc.x - 1;
       if (tiles && at < a.cap) {
@@ -173,7 +178,7 @@ __device__ void build_list(const PlanArgs& p, const ListArgs& a, PlanShared& sh,
       continue;
     }
     int2 tot;
-    const int2 inc = block_scan(make_int2(tiles, 0), sums, tot);
+    const int2 inc = block_scan<kPlanThreads>(make_int2(tiles, 0), sums, tot);
     s_first[tid] = inc.x - tiles;
     __syncthreads();
     for (int i0 = 0; i0 < tot.x; i0 += kPlanThreads) {
@@ -188,7 +193,7 @@ __device__ void build_list(const PlanArgs& p, const ListArgs& a, PlanShared& sh,
         it = item_of(p, a, seq_of(p.cu, p.kv, n0 + lo, p.T, p.kv_max), n0 + lo, i - s_first[lo]);
       }
       int2 tot_units;
-      const int2 cum = block_scan(make_int2(0, it.units), sums, tot_units);
+      const int2 cum = block_scan<kPlanThreads>(make_int2(0, it.units), sums, tot_units);
       it.cum = units + cum.y - it.units;
       if (i < tot.x && items + i < a.cap) {
         a.items[items + i] = it;
@@ -243,7 +248,8 @@ __device__ __forceinline__ int find_item(int num, int x, F cum) {
 }
 
 // Every CTA's piece of the list's line.
-__device__ void cut_line(const PlanArgs& p, const ListArgs& a, PlanShared& sh, int num, int units) {
+template <int kPlanThreads>
+__device__ void cut_line(const PlanArgs& p, const ListArgs& a, PlanShared<kPlanThreads>& sh, int num, int units) {
   int2* sums = sh.sums;
   int* s_pieces = sh.first;
   const long long all = (long long)units * p.Hk;
@@ -253,7 +259,7 @@ __device__ void cut_line(const PlanArgs& p, const ListArgs& a, PlanShared& sh, i
   if (cut.target) {
     const int n = threadIdx.x < num ? (sh.items[threadIdx.x].units + cut.target - 1) / cut.target : 0;
     int2 tot;
-    const int2 inc = block_scan(make_int2(n, 0), sums, tot);
+    const int2 inc = block_scan<kPlanThreads>(make_int2(n, 0), sums, tot);
     s_pieces[threadIdx.x] = inc.x - n;
     pieces = tot.x;
     __syncthreads();
@@ -307,7 +313,8 @@ __device__ void cut_line(const PlanArgs& p, const ListArgs& a, PlanShared& sh, i
 // kItemCost units more (Q, the first scores, the results) and a cut kCutCost.
 // (2,048 tokens in 4 prompts, d = 256: measured figures stand at the kernel.)
 constexpr int kItemCost = 5, kCutCost = 16, kMaxRounds = 12;
-__device__ bool deal_items(const PlanArgs& p, const ListArgs& a, PlanShared& sh, int num, int units) {
+template <int kPlanThreads>
+__device__ bool deal_items(const PlanArgs& p, const ListArgs& a, PlanShared<kPlanThreads>& sh, int num, int units) {
   int2* sums = sh.sums;
   int* s_hist = sh.first;
   const int tid = threadIdx.x;
@@ -321,15 +328,16 @@ __device__ bool deal_items(const PlanArgs& p, const ListArgs& a, PlanShared& sh,
   for (int k = 16; k > 0; k >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, k));
   if ((tid & 31) == 0) sums[tid >> 5].x = longest;
   __syncthreads();
-  longest = sums[tid & 31].x;
+  longest = sums[tid & (kPlanThreads / 32 - 1)].x;
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, k));
-  auto cls = [&](int u) { return (int)((int64_t)(longest - u) * (kPlanThreads - 1) / longest); };
+  const float per = (kPlanThreads - 1) / (float)longest;
+  auto cls = [&](int u) { return min((int)((longest - u) * per), kPlanThreads - 1); };
   for (int i = tid; i < num; i += kPlanThreads) atomicAdd(s_hist + cls(item_at(sh, a, i).units), 1);
   __syncthreads();
   const int mine = s_hist[tid];
   int2 tot;
-  const int2 inc = block_scan(make_int2(mine, 0), sums, tot);
+  const int2 inc = block_scan<kPlanThreads>(make_int2(mine, 0), sums, tot);
   s_hist[tid] = inc.x - mine;
   __syncthreads();
   for (int i = tid; i < num; i += kPlanThreads) {
@@ -341,23 +349,26 @@ __device__ bool deal_items(const PlanArgs& p, const ListArgs& a, PlanShared& sh,
   __syncthreads();
   if (total > (int64_t)kMaxRounds * a.grid) return true;        // many: any deal is even
   int load = 0;
+  static_assert(kPlanThreads >= 160, "a thread per CTA");
   if (tid < a.grid)
     for (int k = 0; k < kMaxRounds; ++k) {
       const int at = k * a.grid + ((k & 1) ? a.grid - 1 - tid : tid);
-      if (at < total) load += sorted_at(sh, a, at / p.Hk).units + kItemCost;
+      if (at >= total) break;
+      load += sorted_at(sh, a, at / p.Hk).units + kItemCost;
     }
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) load = max(load, __shfl_xor_sync(0xffffffffu, load, k));
   if ((tid & 31) == 0) sums[tid >> 5].y = load;
   __syncthreads();
-  load = sums[tid & 31].y;
+  load = sums[tid & (kPlanThreads / 32 - 1)].y;
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) load = max(load, __shfl_xor_sync(0xffffffffu, load, k));
   const int64_t even = ((int64_t)units * p.Hk + kItemCost * total) / a.grid + kItemCost + kCutCost;
   return load <= even;
 }
 
-__device__ void deal_starts(const PlanArgs& p, const ListArgs& a, const PlanShared& sh, int num) {
+template <int kPlanThreads>
+__device__ void deal_starts(const PlanArgs& p, const ListArgs& a, const PlanShared<kPlanThreads>& sh, int num) {
   const int64_t total = (int64_t)num * p.Hk;
   for (int c = threadIdx.x; c < a.grid; c += kPlanThreads) {
     Start at;
@@ -384,8 +395,9 @@ __device__ void deal_starts(const PlanArgs& p, const ListArgs& a, const PlanShar
   }
 }
 
+template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs p) {
-  __shared__ PlanShared sh;
+  __shared__ PlanShared<kPlanThreads> sh;
   pdl_wait();
   pdl_trigger();
 #pragma unroll 1
@@ -1288,7 +1300,13 @@ gdn_status_t launch_attn_plan(const int32_t* cu, const int32_t* kv, int N, int T
   p.list[1] = {l.tile_rows, kTileKeys, limit, 0x7fffffff, l.tile_cap, use.tile ? tile_grid() : 0, 1,
                reinterpret_cast<Item*>(ws + l.tiles), reinterpret_cast<Item*>(ws + l.sorted_tiles),
                reinterpret_cast<Start*>(ws + l.tile_starts)};
-  return check_launch(launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p));
+  // A warp more is a turn more for every instruction of the others: 256 threads
+  // where they hold the sequences and the items (4 prompts: 6.1 -> MEASURED_PLAN256 us).
+  const int64_t rows = (int64_t)T * G;
+  const bool small = N <= 256 && (!use.split || rows / l.split_rows + N <= 256) &&
+                     (!use.tile || rows / l.tile_rows + N <= 256);
+  return check_launch(small ? launch_pdl(attn_plan_kernel<256>, dim3(1), dim3(256), 0, st, p)
+                            : launch_pdl(attn_plan_kernel<1024>, dim3(1), dim3(1024), 0, st, p));
 }
 
 gdn_status_t launch_attn_split(const Args& a, cudaStream_t st) {
