@@ -79,7 +79,7 @@ struct TC {
   // Exponents of the rows' scales, int8 [2 segments][rows].
   static constexpr int o_ex = o_nan + NR * D * 2;
   static constexpr int o_bar = o_ex + 2 * M * 128;
-  static constexpr int n_bar = 2 * KS + 2 * VR + 2 * VS + 8 + 4 + 4 + 4 + 2 + 3;
+  static constexpr int n_bar = 2 * KS + 2 * VR + 2 * VS + 8 + 4 + 4 + 4 + 2 + 2 + 3;
   static constexpr int o_misc = o_bar + n_bar * 8;      // tmem base, abort, flags
   static constexpr int total = o_misc + 32;
   static_assert(total <= 232448, "shared memory of one CTA");
@@ -88,6 +88,13 @@ struct TC {
   // Tensor-memory columns: two score buffers of 64 keys per tile, then O.
   static constexpr int c_s(int m, int b) { return m * 128 + b * 64; }
   static constexpr int c_o(int m) { return 256 + m * D; }
+  // With one tile there is room for Q as well (hi, then lo): a 128 x 64 score
+  // product then reads 2 KB of shared memory instead of 6, and 33 cycles are the
+  // tensor core's instead of 49 (an 8,192-token prompt, 16 heads: 446 -> 381 us).
+  // It also frees Q's place at once, so that the next segment's Q is prepared
+  // during this one.
+  static constexpr bool q_in_tmem = M == 1;
+  static constexpr int c_q(int part) { return 128 + part * (D / 4); }
 };
 
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
@@ -97,6 +104,19 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, 
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n"
       :: "r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+// A in tensor memory: row m in lane m, four K elements a column.
+__device__ __forceinline__ void mma_f8_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}\n"
+      :: "r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+// 128 rows x 32 bytes of a K-major tile to 8 columns of tensor memory.
+__device__ __forceinline__ void copy_128x256b(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" :: "r"(tmem), "l"(desc) : "memory");
 }
 // kind::f8f6f4: e4m3 A and B (format 0), float32 D. kind::f16: f16 A and B.
 __host__ __device__ constexpr uint32_t idesc_f32(int M, int N) {
@@ -316,7 +336,8 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
   // more than one phase away from what it waits for.
   uint64_t* o_done = p_full + 4;
   uint64_t* q_full = o_done + 4;
-  uint64_t* nan_sync = q_full + 2;           // the widening threads among themselves
+  uint64_t* q_empty = q_full + 2;            // [2] by the segment's parity
+  uint64_t* nan_sync = q_empty + 2;          // the widening threads among themselves
   uint64_t* drained = nan_sync + 1;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::o_misc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::o_misc + 4);
@@ -346,7 +367,10 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       tc::mbar_init(p_full + i, 128);
       tc::mbar_init(o_done + i, 1);
     }
-    for (int i = 0; i < 2; ++i) tc::mbar_init(q_full + i, C::loaders);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(q_full + i, C::loaders);
+      tc::mbar_init(q_empty + i, 1);
+    }
     tc::mbar_init(nan_sync, C::loaders);
     for (int i = 0; i < 2; ++i) tc::mbar_init(drained + i, 1);
     *s_abort = 0;
@@ -372,7 +396,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
     // 128 MMA, the tensor core's own rate, where a lone lane's loop took above 200.
     // What the role does beside issuing is the tensor core's idle time: stages and
     // phases are counted along, not divided out, and two tiles have two warps
-    // (4,096 tokens of 16,384, d = 128: MEASURED_ONE -> MEASURED_TWO us).
+    // (4,096 tokens of 16,384, d = 128: 797 -> 731 us).
     if (warp == 12 || (kM == 2 && warp == 15)) {
       const int m = warp == 12 ? 0 : 1;
       const bool one = elect_one();
@@ -398,10 +422,13 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-              mma_f8(d, qd + part * (C::q_part / 16) + k * 16,
-                     b + (k * 32 / C::row) * (kKeys * C::row / 16) + (k * 32 % C::row) / 16, id_qk,
-                     part | k);
+            for (int k = 0; k < D / 32; ++k) {
+              const uint64_t bk = b + (k * 32 / C::row) * (kKeys * C::row / 16) + (k * 32 % C::row) / 16;
+              if constexpr (C::q_in_tmem)
+                mma_f8_tmem_a(d, tmem + C::c_q(part) + k * 8, bk, id_qk, part | k);
+              else
+                mma_f8(d, qd + part * (C::q_part / 16) + k * 16, bk, id_qk, part | k);
+            }
           tc::mma_commit(sf + s_b);
           tc::mma_commit(k_empty + ks);
         }
@@ -415,6 +442,18 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         const Seg g = seg_at(p, l, kRows);
         ok = ok && warp_wait(q_full + seg_b, qp, s_abort);
         tc::fence_after_sync();
+        if constexpr (C::q_in_tmem) {
+          // The scores of the segment before are done, as their softmax is (p_full);
+          // those of this one come behind the copy in the tensor core's order.
+          if (ok && one) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k)
+                copy_128x256b(tmem + C::c_q(part) + k * 8, qd + part * (C::q_part / 16) + k * 16);
+            tc::mma_commit(q_empty + seg_b);
+          }
+        }
         qp ^= seg_b;
         seg_b ^= 1;
         qk();
@@ -558,8 +597,12 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         };
         uint4 w[passes], ahead[passes];
         fetch(0, ahead);
-        // The last scores of the segment before are done with Q's place.
-        if (unit > 0) ok = ok && warp_wait(k_empty + (unit - 1) % C::KS, ((unit - 1) / C::KS) & 1, s_abort);
+        // Q's place is free: copied on, or the last scores of the segment before done.
+        if constexpr (C::q_in_tmem) {
+          if (seg > 0) ok = ok && warp_wait(q_empty + ((seg - 1) & 1), ((seg - 1) >> 1) & 1, s_abort);
+        } else {
+          if (unit > 0) ok = ok && warp_wait(k_empty + (unit - 1) % C::KS, ((unit - 1) / C::KS) & 1, s_abort);
+        }
 #pragma unroll 1
         for (int a = 0; ok && a < groups; ++a) {
 #pragma unroll
