@@ -81,8 +81,15 @@ using namespace attn;
 // list: latency bounds it (two rounds of dependent loads and a scan each).
 // ---------------------------------------------------------------------------
 
+// What an item costs beside its units, in units: a segment's start and end. (Split
+// kernel, 0 / 8 / 16 / 32: 256 decode requests of up to 1,000 tokens 77 / 69 / 66
+// / 68 us, 400 of up to 2,000 at d = 256 95 / 84 / 81 / 85 us. Tensor-core kernel,
+// 5 / 8 / 12: 4,096 tokens behind 4,000, d = 256, 294 / 288 / 286 us.)
+constexpr int kSplitOver = 16, kItemCost = 10;
+
 struct ListArgs {
-  int rows, keys, above, upto, cap, grid, least;   // tiles of the sequences with above < rows <= upto
+  int rows, keys, above, upto, cap, grid;          // tiles of the sequences with above < rows <= upto
+  int least, over;                                 // units of a piece; of an item's overhead (Cut)
   Item *items, *sorted;                            // sorted: room for the items by length, or null
   Start* starts;
 };
@@ -207,18 +214,19 @@ __device__ void build_list(const PlanArgs& p, const ListArgs& a, PlanShared<kPla
   items = min(items, a.cap);
 }
 
-// The line is cut in one of two ways. Into equal pieces, which may end inside an
-// item and go on with the next: no SM is idle. Or, where items are no more than
+// The line is cut in one of two ways. Into pieces of equal cost, which may end
+// inside an item and go on with the next: no SM is idle. An item costs its units
+// and `over` more (a segment's start and end). Or, where items are no more than
 // half as many as CTAs, each item by itself into pieces of about `target` units:
-// a piece then is one segment, and each segment costs 4 us of latency (a CTA
-// with two held up a step of one 16,000-token request by 4 of 10 us). With
-// target >= all / (grid - items) the pieces are no more than the CTAs.
+// a piece then is one segment (a CTA with two held up a step of one 16,000-token
+// request by 4 of 10 us). With target >= all / (grid - items) the pieces are no
+// more than the CTAs.
 struct Cut {
-  int per_cta, target;                 // target 0: equal pieces
+  int per_cta, target;                 // target 0: pieces of equal cost
 };
-__device__ __forceinline__ Cut cut_of(long long all, long long items, int grid, int least) {
+__device__ __forceinline__ Cut cut_of(long long all, long long items, int grid, int least, int over) {
   Cut c;
-  c.per_cta = (int)max((long long)least, (all + grid - 1) / grid);
+  c.per_cta = (int)max((long long)least, (all + items * over + grid - 1) / grid);
   c.target = 0;
   if (2 * items <= grid) c.target = (int)max((long long)least, (all + grid - items - 1) / (grid - items));
   return c;
@@ -231,20 +239,41 @@ __device__ __forceinline__ void piece_of(Start& at, int c, int k, int n) {
   at.c0 = c - k;
   at.pieces = n;
 }
-__device__ __forceinline__ void piece_of_line(Start& at, int per_cta) {
-  const long long at0 = (long long)at.head * at.units + at.it.cum;
-  at.c0 = (int)(at0 / per_cta);
-  at.pieces = (int)((at0 + at.it.units - 1) / per_cta) - at.c0 + 1;
-}
-// Largest i < num with cum[i] <= x.
+// Largest i < num with cum(i) <= x.
 template <typename F>
-__device__ __forceinline__ int find_item(int num, int x, F cum) {
+__device__ __forceinline__ int find_item(int num, long long x, F cum) {
   int lo = 0, hi = num - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (cum(mid) <= x) lo = mid; else hi = mid - 1;
   }
   return lo;
+}
+// CTA c's piece of equal cost: at.u, at.count and, if that is not 0, at.item and
+// at.head. cost(i) and units(i): of one head's items before item i; cost_all: of
+// one head. The first unit of item i is at cost(i) + over.
+template <typename FC, typename FU>
+__device__ __forceinline__ bool piece_of_line(Start& at, int c, int Hk, long long cost_all, int per_cta, int over,
+                                              FC cost, FU units) {
+  auto unit_at = [&](long long x, int& item, int& head) {
+    head = Hk;
+    item = 0;
+    if (x >= cost_all * Hk) return (long long)at.units * Hk;
+    head = (int)((unsigned long long)x / (unsigned long long)cost_all);
+    const long long y = x - head * cost_all;
+    item = find_item(at.num_items, y, cost);
+    return (long long)head * at.units + units(item) + (int)max(0ll, (long long)(y - cost(item) - over));
+  };
+  int item, head;
+  at.u = unit_at((long long)c * per_cta, at.item, at.head);
+  at.count = (int)(unit_at((long long)(c + 1) * per_cta, item, head) - at.u);
+  return at.count > 0;
+}
+// The pieces of its item, which takes cost_before of the line before it.
+__device__ __forceinline__ void pieces_of_line(Start& at, long long cost_before, int per_cta, int over) {
+  const long long first = cost_before + over;
+  at.c0 = (int)(first / per_cta);
+  at.pieces = (int)((first + at.it.units - 1) / per_cta) - at.c0 + 1;
 }
 
 // Every CTA's piece of the list's line.
@@ -253,7 +282,8 @@ __device__ void cut_line(const PlanArgs& p, const ListArgs& a, PlanShared<kPlanT
   int2* sums = sh.sums;
   int* s_pieces = sh.first;
   const long long all = (long long)units * p.Hk;
-  const Cut cut = cut_of(all, (long long)num * p.Hk, a.grid, a.least);
+  const Cut cut = cut_of(all, (long long)num * p.Hk, a.grid, a.least, a.over);
+  const long long cost_all = units + (long long)num * a.over;   // of one head
   __syncthreads();                              // the list is written
   int pieces = 0;                               // of one head
   if (cut.target) {
@@ -281,14 +311,9 @@ __device__ void cut_line(const PlanArgs& p, const ListArgs& a, PlanShared<kPlanT
         at.item = find_item(num, y, [&](int i) { return s_pieces[i]; });
       }
     } else {
-      at.u = min(all, (long long)c * cut.per_cta);
-      at.count = (int)(min(all, at.u + cut.per_cta) - at.u);
-      work = at.count > 0;
-      if (work) {
-        at.head = (int)((unsigned long long)at.u / (unsigned)units);
-        const int x = (int)(at.u - (long long)at.head * units);
-        at.item = find_item(num, x, [&](int i) { return item_at(sh, a, i).cum; });
-      }
+      auto before = [&](int i) { return item_at(sh, a, i).cum; };
+      work = piece_of_line(at, c, p.Hk, cost_all, cut.per_cta, a.over,
+                           [&](int i) { return before(i) + (long long)i * a.over; }, before);
     }
     if (work) {
       at.it = item_at(sh, a, at.item);
@@ -300,7 +325,7 @@ __device__ void cut_line(const PlanArgs& p, const ListArgs& a, PlanShared<kPlanT
         const int k = y - s_pieces[at.item];
         piece_of(at, c, k, (at.it.units + cut.target - 1) / cut.target);
       } else {
-        piece_of_line(at, cut.per_cta);
+        pieces_of_line(at, (long long)at.head * cost_all + at.it.cum + (long long)at.item * a.over, cut.per_cta, a.over);
       }
     }
     a.starts[c] = at;
@@ -309,10 +334,10 @@ __device__ void cut_line(const PlanArgs& p, const ListArgs& a, PlanShared<kPlanT
 
 // Whole items, longest first, dealt out back and forth over the CTAs: without
 // cuts there are no partial results to write and join. Taken where the most
-// loaded CTA then ends before an even cut of the line would, each item counted
-// kItemCost units more (Q, the first scores, the results) and a cut kCutCost.
-// (2,048 tokens in 4 prompts, d = 256: measured figures stand at the kernel.)
-constexpr int kItemCost = 5, kCutCost = 16, kMaxRounds = 12;
+// loaded CTA then ends before an even cut of the line would, with kCutCost for the
+// partial results and their join (4: 8 prompts of 100-500 tokens behind up to
+// 3,000 take 104 us instead of 97).
+constexpr int kCutCost = 16, kMaxRounds = 12;
 template <int kPlanThreads>
 __device__ bool deal_items(const PlanArgs& p, const ListArgs& a, PlanShared<kPlanThreads>& sh, int num, int units) {
   int2* sums = sh.sums;
@@ -584,15 +609,19 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       }
       return before;
     };
-    int before = scan(mine, total).x;
+    const int2 both = scan(mine, total);
+    int before = both.x, cost = both.x + both.y * kSplitOver;
 #pragma unroll
     for (int k = 0; k < per; ++k) {
       s_cum[tid * per + k] = before;
+      s_pieces[tid * per + k] = cost;
       before += u4[k];
+      cost += u4[k] + (u4[k] > 0 ? kSplitOver : 0);
     }
     if (tid == 0) s_cum[kSelfPlan] = total.x;
     const long long all = (long long)total.x * p.Hk;
-    const Cut cut = cut_of(all, (long long)total.y * p.Hk, gridDim.x, kWarps);
+    const Cut cut = cut_of(all, (long long)total.y * p.Hk, gridDim.x, kWarps, kSplitOver);
+    const int cost_all = total.x + total.y * kSplitOver;
     int pieces = 0;                      // of one head
     if (cut.target) {
       int2 n = make_int2(0, 0), tot;
@@ -623,14 +652,8 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         start.item = find_item(p.N, y, [&](int i) { return s_pieces[i]; });
       }
     } else {
-      start.u = min(all, (long long)c * cut.per_cta);
-      start.count = (int)(min(all, start.u + cut.per_cta) - start.u);
-      work = start.count > 0;
-      if (work) {
-        start.head = (int)((unsigned long long)start.u / (unsigned)total.x);
-        start.item = find_item(p.N, (int)(start.u - (long long)start.head * total.x),
-                               [&](int i) { return s_cum[i]; });
-      }
+      work = piece_of_line(start, c, p.Hk, cost_all, cut.per_cta, kSplitOver,
+                           [&](int i) { return s_pieces[i]; }, [&](int i) { return s_cum[i]; });
     }
     if (work) {
       const int i = start.item;
@@ -640,7 +663,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       start.len = q.len;
       start.kv = q.kv;
       if (cut.target) piece_of(start, c, y - s_pieces[i], (start.it.units + cut.target - 1) / cut.target);
-      else piece_of_line(start, cut.per_cta);
+      else pieces_of_line(start, (long long)start.head * cost_all + s_pieces[i], cut.per_cta, kSplitOver);
     }
     if (tid < 4)                         // for the joining kernel
       reinterpret_cast<int4*>(p.starts + blockIdx.x)[tid] = reinterpret_cast<const int4*>(&start)[tid];
@@ -1127,10 +1150,10 @@ gdn_status_t launch_attn_plan(const int32_t* cu, const int32_t* kv, int N, int T
   // A piece of the split kernel gives each of its 8 warps a unit at least.
   if (use.split)
     p.list[lists++] = {l.split_rows, kUnit, 0, limit, l.item_cap, split_grid(d, l.split_rows), kWarps,
-                       reinterpret_cast<Item*>(ws + l.items), nullptr, reinterpret_cast<Start*>(ws + l.starts)};
+                       kSplitOver,                        reinterpret_cast<Item*>(ws + l.items), nullptr, reinterpret_cast<Start*>(ws + l.starts)};
   if (use.tile)
     p.list[lists++] = {l.tile_rows, kTileKeys, limit, 0x7fffffff, l.tile_cap, tile_grid(), 1,
-                       reinterpret_cast<Item*>(ws + l.tiles), reinterpret_cast<Item*>(ws + l.sorted_tiles),
+                       kItemCost,                        reinterpret_cast<Item*>(ws + l.tiles), reinterpret_cast<Item*>(ws + l.sorted_tiles),
                        reinterpret_cast<Start*>(ws + l.tile_starts)};
   // A warp more is a turn more for every instruction of the others: 256 threads
   // where they hold the sequences and the items (4 prompts: 6.1 -> 4.7 us).

@@ -22,9 +22,10 @@
 //   rescaled only when a row's maximum grows by more than 2^8.
 //
 // Work split: where items are many or alike enough, whole items are dealt out by
-// length (the plan compares the two). Otherwise, as in the split kernel, all (tile, kv head, 64 keys) units form
-// one line cut into equal pieces, one per SM; a tile cut by the end of a piece
-// leaves float32 partial results, which a second kernel joins in CTA order.
+// length (the plan compares the two). Otherwise, as in the split kernel, all (tile,
+// kv head, 64 keys) units form one line cut into pieces of equal cost, one per SM;
+// a tile cut by the end of a piece leaves float32 partial results, which another
+// kernel joins in CTA order.
 //
 // Roles (four warpgroups): 0 .. kM - 1: softmax of one 128-row tile each; the
 // others up to 2: Q, widening of V; warps 12 and 15: MMAs of a tile each; warp
