@@ -87,6 +87,22 @@ class SyntheticServingStack:
     def _logits(self, h_rows):
         return _rms_bf16(h_rows).float() @ self.head
 
+    # The token mixer of a layer, and what a run and a step open before it (a stack with
+    # layers of another kind overrides these).
+    def _begin_run(self, n_decode):
+        pass
+
+    def _begin_step(self, new):
+        pass
+
+    def _prefill_mix(self, stack, l, cu_d, has_d, first, n, x, y, o):
+        a, b = self._gates(l, x)
+        stack.prefill_layer(l, cu_d, has_d, first, n, x, a, b, y, o)
+
+    def _decode_mix(self, stack, l, x, y, o):
+        a, b = self._gates(l, x)
+        stack.decode_layer(l, x, a, b, y, o)
+
     @torch.no_grad()
     def generate(self, n_decode: int = 128, forced=None, keep_logits=()):
         """Prefill every prompt in steps of at most ``budget`` tokens, then run
@@ -106,6 +122,7 @@ class SyntheticServingStack:
         n_out = n_decode + 1
         ids = torch.zeros((self.n_seqs, n_out), dtype=torch.int64, device=dev)
         kept = {s: [] for s in keep_logits}
+        self._begin_run(n_decode)
 
         for step in pack_prefill_steps(lengths, self.budget):
             cu, has, first = stack.step_meta(step)
@@ -118,10 +135,13 @@ class SyntheticServingStack:
             y = torch.empty((T, C), dtype=torch.bfloat16, device=dev)
             o = torch.empty((T, self.hv, self.d), dtype=torch.bfloat16, device=dev)
             stack.build_chunks(cu_d, T)
+            new = [0] * self.n_seqs
+            for sg in step.segments:
+                new[sg.seq] = sg.length
+            self._begin_step(new)
             for l in range(self.layers):
                 x = _rms_bf16(h).contiguous()
-                a, b = self._gates(l, x)
-                stack.prefill_layer(l, cu_d, has_d, first, n, x, a, b, y, o)
+                self._prefill_mix(stack, l, cu_d, has_d, first, n, x, y, o)
                 h = self._residual(l, h, o)
             for i, sg in enumerate(step.segments):
                 if sg.start + sg.length == lengths[sg.seq]:
@@ -141,10 +161,10 @@ class SyntheticServingStack:
             if forced:
                 cur[forced_rows] = forced_ids[:, t]
             h = self.embed[cur].float()
+            self._begin_step([1] * N)
             for l in range(self.layers):
                 x = _rms_bf16(h).contiguous()
-                a, b = self._gates(l, x)
-                stack.decode_layer(l, x, a, b, y, o)
+                self._decode_mix(stack, l, x, y, o)
                 h = self._residual(l, h, o)
             lg = self._logits(h)
             ids[:, t + 1] = torch.argmax(lg, dim=1)
