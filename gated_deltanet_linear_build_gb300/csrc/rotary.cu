@@ -5,9 +5,13 @@
 // phase_i = f_i / (2 pi) turns per token held as a 64-bit fixed-point fraction.
 // The product wraps modulo 2^64, which IS the reduction to one turn: exact for
 // every 32-bit position, where a float32 product p f_i is off by 0.06 rad at a
-// million tokens. The top 32 bits, as a signed fraction of a turn, give an
-// angle in [-pi, pi], where the hardware sine and cosine are within 2^-21:
-// far below the BF16 or 8-bit rounding of the results.
+// million tokens. Its top 32 bits are the angle. BF16 results take the hardware's
+// sine and cosine of it as a signed fraction of a turn, which are within 2^-21 on
+// [-pi, pi]. 8-bit codes, where that moved one in some ten thousand to its
+// neighbour, take the quadrant and the Taylor series on [-pi/4, pi/4] (to x^9 and
+// x^10: below 2^-29), right to float32's last bits: 16,384 tokens of 8 heads of
+// 128 appended take 64.3 us instead of 63.2. (In rotary alone, 32 + 8 heads:
+// 53.6 instead of 52.0.)
 //
 // Both kernels are one pass over memory. A thread owns two 8-element vectors
 // of a head (the two halves of its 8 pairs) and keeps its 8 sines and cosines
@@ -52,18 +56,51 @@ __device__ __forceinline__ void load_phases(const uint64_t* phases, int j, uint6
   }
 }
 
+template <bool kExact>
 __device__ __forceinline__ void angles(const uint64_t (&ph)[8], int pos, float scale, int inverse,
                                        float (&co)[8], float (&si)[8]) {
   constexpr float kTurn = 1.4629180792671596e-09f;     // 2 pi / 2^32
   const float ss = inverse ? -scale : scale;
+  auto turn_of = [&](int i) { return (uint32_t)(((uint64_t)(int64_t)pos * ph[i]) >> 32); };
+  if constexpr (!kExact) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint64_t turn = (uint64_t)(int64_t)pos * ph[i];
-    const float a = (float)(int32_t)(turn >> 32) * kTurn;
-    float s, c;
-    __sincosf(a, &s, &c);
-    co[i] = c * scale;
-    si[i] = s * ss;
+    for (int i = 0; i < 8; ++i) {
+      float s, c;
+      __sincosf((float)(int32_t)turn_of(i) * kTurn, &s, &c);
+      co[i] = c * scale;
+      si[i] = s * ss;
+    }
+    return;
+  }
+  // Two angles at a time, for the packed float32 instructions.
+  auto both = [](float v) { return make_float2(v, v); };
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    uint32_t quadrant[2];
+    float r[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t turn = turn_of(i + e);
+      quadrant[e] = (turn + 0x20000000u) >> 30;
+      r[e] = (float)(int32_t)(turn - (quadrant[e] << 30));
+    }
+    const float2 x = mul2(make_float2(r[0], r[1]), both(kTurn)), x2 = mul2(x, x);
+    float2 a = fma2(x2, both(1.f / 362880.f), both(-1.f / 5040.f));
+    float2 b = fma2(x2, both(-1.f / 3628800.f), both(1.f / 40320.f));
+    a = fma2(x2, a, both(1.f / 120.f));
+    b = fma2(x2, b, both(-1.f / 720.f));
+    a = fma2(x2, a, both(-1.f / 6.f));
+    b = fma2(x2, b, both(1.f / 24.f));
+    a = fma2(mul2(x, x2), a, x);
+    b = fma2(x2, b, both(-0.5f));
+    b = fma2(x2, b, both(1.f));
+    const float sn[2] = {a.x, a.y}, cs[2] = {b.x, b.y};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t q = quadrant[e];
+      si[i + e] = __uint_as_float(__float_as_uint(q & 1 ? cs[e] : sn[e]) ^ ((q & 2) << 30)) * ss;
+      co[i + e] = __uint_as_float(__float_as_uint(q & 1 ? sn[e] : cs[e]) ^ (((q + 1) & 2) << 30)) * scale;
+    }
   }
 }
 
@@ -122,7 +159,7 @@ __device__ __forceinline__ void rotate_unit(const RotArgs& p, int64_t u) {
   if (turn) {
     uint64_t ph[8];
     load_phases(p.phases, j, ph);
-    angles(ph, __ldg(p.positions + tok), p.scale, p.inverse, co, si);
+    angles<false>(ph, __ldg(p.positions + tok), p.scale, p.inverse, co, si);
   }
 #pragma unroll
   for (int i = 0; i < kHeads; ++i) {
@@ -317,7 +354,7 @@ __device__ __forceinline__ void append_piece(const AppendArgs& p, int unit, uint
       float x[16];
       unpack16(a[i], b[i], x);
       if (turn) {
-        if (t != t_of) angles(ph, __ldg(p.r.positions + first + t), p.r.scale, p.r.inverse, co, si);
+        if (t != t_of) angles<true>(ph, __ldg(p.r.positions + first + t), p.r.scale, p.r.inverse, co, si);
         t_of = t;
         rotate16(x, co, si, p.r.interleaved);
       }

@@ -273,6 +273,40 @@ def test_append(interleaved, Hq, Hk, d, rot, B):
     assert torch.equal(R.e4m3_values(vc), rv)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_angles_hold_float32(interleaved):
+    # Codes differ from those of the 64-bit values only where a value lies on the middle of two but for
+    # float32's rounding: the sine and cosine (2 * 2^-24), their products with scale and value and the sum
+    # (1 + 2 * 1 of 2^-24 of the pair's length, at most sqrt 2 times in one component): below 2^-21.
+    from gated_deltanet_linear_build_gb300 import gdn
+    rng = np.random.default_rng(21)
+    B, Hk, d = 64, 2, 64
+    T = 1500
+    blocks, pos, pieces = make_step(rng, [T], [100000 // B * B], B)
+    _, k, v = make_qkv(rng, T, 1, Hk, d)
+    kc, vc, ks, vs = R.fill_cache(rng, blocks, Hk, B, d, "cuda")
+    old, ks0 = R.e4m3_values(kc), ks.cpu().double()
+    ph = gdn.rotary_phases(d, 10000.0)
+    qo = torch.empty((T, 1, d), dtype=torch.bfloat16, device="cuda")
+    gdn.rotary_kv_append(k[:, :1], k, v, dev(pos), ph, dev(pieces), dev([len(pieces)]), qo, kc, vc, ks, vs,
+                         interleaved=interleaved)
+    kd = k.cpu().double()
+    turns = ph.cpu().numpy().view(np.uint64).astype(np.float64) / 2.0 ** 64
+    kr = R.rotate(kd, pos, list(turns * 2 * math.pi), interleaved, 1.0)
+    ref, scales = R.append(kr, kd, pieces, old, ks0, 1)
+    assert torch.equal(ks.cpu().double(), scales)
+    u, w = (kd[..., 0::2], kd[..., 1::2]) if interleaved else (kd[..., :d // 2], kd[..., d // 2:])
+    pair = torch.sqrt(u * u + w * w)
+    length = torch.stack([pair, pair], -1).flatten(-2) if interleaved else torch.cat([pair, pair], -1)
+    got = R.e4m3_values(kc)
+    for block, first, count, off in pieces:
+        for h in range(Hk):
+            g, r = got[block, h, off:off + count], ref[block, h, off:off + count]
+            x = kr[first:first + count, h] / scales[block, h]
+            err = 2.0 ** -21 * length[first:first + count, h] / scales[block, h]
+            assert (((x - (g + r) / 2).abs() <= err) | (g == r)).all()
+
+
 def test_append_without_rotation_and_special_values():
     from gated_deltanet_linear_build_gb300 import gdn
     rng = np.random.default_rng(8)
