@@ -548,7 +548,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
   float* s_ml = reinterpret_cast<float*>(smem + C::o_ml);
   float* s_l = reinterpret_cast<float*>(smem + C::o_l);
   int* s_nan = reinterpret_cast<int*>(smem + C::o_nan);
-  int* s_flag = reinterpret_cast<int*>(smem + C::o_flag);   // unused | a NaN in V | gave up
+  int* s_flag = reinterpret_cast<int*>(smem + C::o_flag);   // a NaN in V | gave up
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   unsigned char* ring = smem + w * (C::slots * C::slot_bytes);
@@ -561,7 +561,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
   const int absent = max(p.num_blocks * p.Hk, 1);      // a box past the end reads zeros
 
   if (lane < C::slots) tc::mbar_init(full + lane, 1);
-  if (tid == 0) s_flag[2] = 0;
+  if (tid == 0) s_flag[1] = 0;
   __syncwarp();
   bool dead = false;                                   // a wait of this warp ran out
   int posted = 0, taken = 0;                           // half units, over all segments
@@ -742,7 +742,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       const int st = taken % C::slots;
       if (!dead && !__all_sync(0xffffffffu, tc::mbar_wait(full + st, (taken / C::slots) & 1))) {
         dead = true;
-        s_flag[2] = 1;
+        s_flag[1] = 1;
         record_device_status(GDN_ERR_TIMEOUT);
       }
       ++taken;
@@ -752,7 +752,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
     for (int h = 0; h < C::slots - 1; ++h) issue(h, h >> 1);
 
     for (int i = tid; i < D; i += kWarps * 32) s_nan[i] = 0x7fffffff;
-    if (tid == 0) s_flag[1] = 0;
+    if (tid == 0) s_flag[0] = 0;
 
     // ---- Q of the tile: hi and lo codes, one power-of-two scale per row -------
 #pragma unroll
@@ -910,7 +910,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       // meet a NaN (0 x NaN is NaN): a NaN of V is taken out of the slot and kept as
       // the first key whose column has one.
       if (cut && min_lim < key_end) {
-        if (take_nans<D>(slot, s_nan, unit * kUnit)) s_flag[1] = 1;
+        if (take_nans<D>(slot, s_nan, unit * kUnit)) s_flag[0] = 1;
         tc::fence_smem_to_async();
         __syncwarp();
       }
@@ -1056,7 +1056,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
           *reinterpret_cast<float2*>(dst + 16 * k) = make_float2(acc[m][k][e] * f, acc[m][k][2 + e] * f);
       }
     __syncthreads();
-    const bool whole = seg == n_units, gave_up = s_flag[2] != 0;
+    const bool whole = seg == n_units, gave_up = s_flag[1] != 0;
     float* part = p.partials + ((size_t)blockIdx.x * 2 + (first_unit == 0 ? 1 : 0)) * C::rows * (D + 2);
     const RowsOut out = {p.o, s.first, row0, gave_up ? 0 : n_rows, G, p.Hq, head};
 #pragma unroll
@@ -1071,7 +1071,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         o.z += v.z;
         o.w += v.w;
       }
-      if (s_flag[1] && r < n_rows) {
+      if (s_flag[0] && r < n_rows) {
         const int lim_r = visible(s, (row0 + r) / G);
         if (lim_r > s_nan[d_of<D>(pos)]) o.x = NAN;
         if (lim_r > s_nan[d_of<D>(pos + 1)]) o.y = NAN;

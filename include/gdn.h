@@ -613,7 +613,8 @@ GDN_API gdn_status_t gdn_paged_attention_plan(const int32_t* cu_seqlens, const i
  *               sequence n; kv_lens beyond max_blocks * B are cut off there. A
  *               block outside [0, num_blocks) reads as zeros and is reported as
  *               GDN_ERR_INVALID_ARG by gdn_device_status.
- *   max_new_tokens  an upper bound of the l_n (1 for a decode step).
+ *   max_new_tokens  an upper bound of the l_n (1 for a decode step). It chooses the
+ *               kernels; the rows of a longer sequence may be left unwritten.
  *   flags       0 or GDN_FLAG_PLANNED.
  * Sums, maxima and the accumulator are float32. Hq % Hk == 0, Hq / Hk <= 16.
  */
