@@ -480,9 +480,11 @@ struct Cfg {
   // 16 up to d = 64; the others have the SM to themselves.
   static constexpr int ctas = D * QM <= 128 ? 2 : 1;
   static constexpr int slots = D == 128 && QM == 2 ? 6 : 3;   // half units (K or V) in a warp's ring
-  // Q's fragments, 64 registers at d x rows = 256 x 16, are read from shared
-  // memory there (rows 64 bytes off a bank line: two rows x four chunks at once).
-  static constexpr bool q_in_regs = D * QM <= 256;
+  // Q's fragments stay in registers for 8 rows; for 16 they are read from shared
+  // memory (100 requests of 3k-30k tokens, 12 heads a kv head of 128: 191 -> 184 us;
+  // 16 of 64: 178 -> 168; for 8 rows of 128 233 -> 234), rows 64 bytes off a bank
+  // line: two rows x four chunks at once.
+  static constexpr bool q_in_regs = QM == 1;
   static constexpr int q_pitch = 2 * D + 64;
   static constexpr int slot_bytes = kUnit * D;
   static constexpr int row = box_row(D), boxes = D / row;
