@@ -390,8 +390,11 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
   const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
   // Behind the split kernel, the plan and the step's inputs are two launches back,
   // hence complete: this kernel goes on as soon as it has an SM, and waits for the
-  // split kernel at its end, for those that follow.
-  if constexpr (!kAfterSplit) {
+  // split kernel at its end, for those that follow. The fence takes the place of
+  // the wait's acquire: nothing that this SM's L1 holds from before is read.
+  if constexpr (kAfterSplit) {
+    __threadfence();
+  } else {
     pdl_wait();
     pdl_trigger();
   }

@@ -274,3 +274,34 @@ def test_refusals():
                      ("table", s["table"].long()), ("kv", s["kv"].long()), ("cu", s["cu"].long())):
         with pytest.raises(ValueError):
             run(dict(s, **{key: bad}))
+
+
+@pytest.mark.parametrize("planned", [False, True])
+def test_mixed_steps_back_to_back_see_their_own_inputs(planned):
+    # Both kernels of a mixed step, without a wait between calls whose q, scales and outputs change in place.
+    from gated_deltanet_linear_build_gb300 import gdn
+    new, kv = [1] * 20 + [130, 90, 300], list(range(50, 2050, 100)) + [700, 1200, 300]
+    s = make(31, new, kv, 32, 8, 128, 64)
+    T, N = sum(new), len(new)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    qs = [torch.randn((T, 32, 128), generator=g, device="cuda").bfloat16() for _ in range(4)]
+    base = s["vs"].clone()
+    s["q"] = torch.empty_like(qs[0])
+    ws = torch.empty(gdn.paged_attention_workspace_size(T, N, 32, 8, 128), dtype=torch.uint8, device="cuda")
+    if planned:
+        gdn.paged_attention_plan(s["cu"], s["kv"], ws, T=T, Hq=32, Hk=8, d=128, block_tokens=64,
+                                 max_blocks=s["table"].shape[1], max_new_tokens=max(new))
+
+    def step(i):
+        s["q"].copy_(qs[i % 4])
+        torch.mul(base, 2.0 ** (i % 3), out=s["vs"])
+        return run(s, planned=planned, workspace=ws)
+    expect = []
+    for i in range(12):
+        expect.append(step(i))
+        torch.cuda.synchronize()
+    got = [step(i) for i in range(12)]
+    for i in range(12):
+        assert torch.equal(got[i], expect[i]), i
+    s["q"].copy_(qs[11 % 4])
+    check(s, got[11])
