@@ -708,7 +708,6 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
             *s_any_nan = 1;
           }
         }
-        tc::mbar_arrive(vr_empty + sr);
 #pragma unroll
         for (int it = 0; it < v_it; ++it) {
           const uint4 w = raw[it];
@@ -718,6 +717,9 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
           *reinterpret_cast<uint4*>(at + 128) = make_uint4(e4m3x2_half2(w.z), e4m3x2_half2(w.z >> 16),
                                                            e4m3x2_half2(w.w), e4m3x2_half2(w.w >> 16));
         }
+        // Only now: an arrival right behind the loads overtook them, and a copy landed in
+        // codes not yet read (one step in some thousands).
+        tc::mbar_arrive(vr_empty + sr);
         tc::fence_smem_to_async();
         tc::mbar_arrive(v_full + st);
       }

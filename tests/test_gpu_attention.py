@@ -305,3 +305,23 @@ def test_mixed_steps_back_to_back_see_their_own_inputs(planned):
         assert torch.equal(got[i], expect[i]), i
     s["q"].copy_(qs[11 % 4])
     check(s, got[11])
+
+
+@pytest.mark.parametrize("Hq,Hk,d", [(32, 8, 128), (16, 2, 256), (8, 8, 64)])
+@pytest.mark.parametrize("decode", [0, 20])
+def test_a_step_repeats_bit_by_bit(Hq, Hk, d, decode):
+    # Copies that land while a step's data are still read would show in one step of thousands.
+    from gated_deltanet_linear_build_gb300 import gdn
+    new = [1] * decode + [130, 90, 300]
+    kv = list(range(50, 50 + 100 * decode, 100)) + [700, 1200, 300]
+    s = make(32, new, kv, Hq, Hk, d, 64)
+    T, N = sum(new), len(new)
+    ws = torch.empty(gdn.paged_attention_workspace_size(T, N, Hq, Hk, d), dtype=torch.uint8, device="cuda")
+    first = run(s, workspace=ws)
+    check(s, first)
+    o, off = torch.empty_like(first), torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(4000):
+        gdn.paged_attention(s["q"], s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["cu"], s["kv"], o, ws,
+                            softmax_scale=s["scale"], max_new_tokens=300)
+        off += (o != first).any()
+    assert int(off) == 0
