@@ -4,6 +4,8 @@
 // or the partial results' bytes, which are in L2. One launch for both kernels,
 // and a grid bounded by the step's items, few CTAs where they are few: 1,216 CTAs
 // of which most had nothing to do cost a step 12 us.
+// Measured: 8 heads' tiles of 19 pieces 3 us (64 tokens behind 30,000), 40 MB of
+// partial results of 4,096 tokens 10 us.
 #include <algorithm>
 
 #include "paged_attn.cuh"

@@ -30,6 +30,11 @@
 // (equal inputs give equal bits). Joining inside this kernel, by the CTA that
 // arrives last, took as long as that launch does, and its code cost the stream its
 // registers (48 requests of 3k-30k tokens: 232 -> 335 us).
+//
+// Measured: 48 requests of 3k-30k tokens, 32 query and 8 kv heads of 128, 1.42 GB:
+// 233 us, 6.1 TB/s, 90% of the copy rate. 16 rows a tile (12 heads a kv head) have
+// twice the instructions a byte and half of the warps: 66%. 32 requests of 100 to
+// 1,900 tokens, 28 MB: 15.7 us, of which 9 are there for a single short request.
 #include <algorithm>
 
 #include <cuda_fp16.h>

@@ -13,6 +13,10 @@
 // 128 appended take 64.3 us instead of 63.2. (In rotary alone, 32 + 8 heads:
 // 53.6 instead of 52.0.)
 //
+// Measured: rotation of 16,384 tokens, 32 + 8 heads of 128, 336 MB: 52.0 us, 6.46
+// TB/s, 95% of the copy rate; with the append of 8 heads of K and V, 370 MB: 64.3
+// us, 85%.
+//
 // Both kernels are one pass over memory. A thread owns two 8-element vectors
 // of a head (the two halves of its 8 pairs) and keeps its 8 sines and cosines
 // in registers over kHeads heads, all of whose loads are issued first.
