@@ -87,6 +87,8 @@ inline int split_grid(int d, int rows) {
 
 Layout layout(int T, int N, int Hq, int Hk, int d);
 
+constexpr int kWarps = 8;              // warps of a CTA of the split kernel
+
 // Bytes of a cache row in one TMA box: the widest swizzle.
 __host__ __device__ constexpr int box_row(int d) { return d == 64 ? 64 : 128; }
 // The cache as (d, token of the block, block x head), boxes of `rows` tokens.
@@ -162,6 +164,74 @@ __device__ __forceinline__ Start read_start(const Start* at) {
 // Keys that row r of the sequence sees: [0, visible).
 __device__ __forceinline__ int visible(const Seq& s, int token) {
   return max(0, s.kv - s.len + token + 1);
+}
+
+// What an item costs beside its units, in units: a segment's start and end. (Split
+// kernel, 0 / 8 / 16 / 32: 256 decode requests of up to 1,000 tokens 77 / 69 / 66
+// / 68 us, 400 of up to 2,000 at d = 256 95 / 84 / 81 / 85 us. Tensor-core kernel,
+// 5 / 8 / 12: 4,096 tokens behind 4,000, d = 256, 294 / 288 / 286 us.)
+constexpr int kSplitOver = 16, kItemCost = 10;
+
+// The line is cut in one of two ways. Into pieces of equal cost, which may end
+// inside an item and go on with the next: no SM is idle. An item costs its units
+// and `over` more (a segment's start and end). Or, where items are no more than
+// half as many as CTAs, each item by itself into pieces of about `target` units:
+// a piece then is one segment (a CTA with two held up a step of one 16,000-token
+// request by 4 of 10 us). With target >= all / (grid - items) the pieces are no
+// more than the CTAs.
+struct Cut {
+  int per_cta, target;                 // target 0: pieces of equal cost
+};
+__device__ __forceinline__ Cut cut_of(long long all, long long items, int grid, int least, int over) {
+  Cut c;
+  c.per_cta = (int)max((long long)least, (all + items * over + grid - 1) / grid);
+  c.target = 0;
+  if (2 * items <= grid) c.target = (int)max((long long)least, (all + grid - items - 1) / (grid - items));
+  return c;
+}
+// Piece k of the n that an item of `units` units is cut into.
+__device__ __forceinline__ void piece_of(Start& at, int c, int k, int n) {
+  const int from = (int)((long long)at.it.units * k / n), to = (int)((long long)at.it.units * (k + 1) / n);
+  at.u = (long long)at.head * at.units + at.it.cum + from;
+  at.count = to - from;
+  at.c0 = c - k;
+  at.pieces = n;
+}
+// Largest i < num with cum(i) <= x.
+template <typename F>
+__device__ __forceinline__ int find_item(int num, long long x, F cum) {
+  int lo = 0, hi = num - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cum(mid) <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+// CTA c's piece of equal cost: at.u, at.count and, if that is not 0, at.item and
+// at.head. cost(i) and units(i): of one head's items before item i; cost_all: of
+// one head. The first unit of item i is at cost(i) + over.
+template <typename FC, typename FU>
+__device__ __forceinline__ bool piece_of_line(Start& at, int c, int Hk, long long cost_all, int per_cta, int over,
+                                              FC cost, FU units) {
+  auto unit_at = [&](long long x, int& item, int& head) {
+    head = Hk;
+    item = 0;
+    if (x >= cost_all * Hk) return (long long)at.units * Hk;
+    head = (int)((unsigned long long)x / (unsigned long long)cost_all);
+    const long long y = x - head * cost_all;
+    item = find_item(at.num_items, y, cost);
+    return (long long)head * at.units + units(item) + (int)max(0ll, (long long)(y - cost(item) - over));
+  };
+  int item, head;
+  at.u = unit_at((long long)c * per_cta, at.item, at.head);
+  at.count = (int)(unit_at((long long)(c + 1) * per_cta, item, head) - at.u);
+  return at.count > 0;
+}
+// The pieces of its item, which takes cost_before of the line before it.
+__device__ __forceinline__ void pieces_of_line(Start& at, long long cost_before, int per_cta, int over) {
+  const long long first = cost_before + over;
+  at.c0 = (int)(first / per_cta);
+  at.pieces = (int)((first + at.it.units - 1) / per_cta) - at.c0 + 1;
 }
 
 // The split kernel's V chunk of lane group g.
