@@ -181,7 +181,15 @@ __device__ void cut_line(const PlanArgs& p, const ListArgs& a, PlanShared<kPlanT
   int2* sums = sh.sums;
   int* s_pieces = sh.first;
   const long long all = (long long)units * p.Hk;
-  const Cut cut = cut_of(all, (long long)num * p.Hk, a.grid, a.least, a.over);
+  int longest = 0;
+  if (by_longest((long long)num * p.Hk, a.grid)) {   // no more items than threads, then
+    __syncthreads();                             // the list is written
+    longest = __reduce_max_sync(0xffffffffu, threadIdx.x < num ? sh.items[threadIdx.x].units : 0);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5].x = longest;
+    __syncthreads();
+    longest = __reduce_max_sync(0xffffffffu, sums[threadIdx.x & (kPlanThreads / 32 - 1)].x);
+  }
+  const Cut cut = cut_of(all, (long long)num * p.Hk, longest, a.grid, a.least, a.over);
   const long long cost_all = units + (long long)num * a.over;   // of one head
   __syncthreads();                              // the list is written
   int pieces = 0;                               // of one head

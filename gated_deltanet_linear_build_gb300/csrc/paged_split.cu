@@ -154,6 +154,16 @@ __device__ __noinline__ bool take_nans(unsigned char* slot, int* first_nan, int 
   return any;
 }
 
+// Largest value of the block. (Out of line: few steps need it.)
+__device__ __noinline__ int block_max(int x, int* warps) {
+  x = __reduce_max_sync(0xffffffffu, x);
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = x;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k) x = max(x, warps[k]);
+  return x;
+}
+
 template <int D, int QM>
 __global__ void __launch_bounds__(kWarps * 32, Cfg<D, QM>::ctas)
 attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
@@ -237,7 +247,13 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
     }
     if (tid == 0) s_cum[kSelfPlan] = total.x;
     const long long all = (long long)total.x * p.Hk;
-    const Cut cut = cut_of(all, (long long)total.y * p.Hk, gridDim.x, kWarps, kSplitOver);
+    int longest = 0;
+    if (by_longest((long long)total.y * p.Hk, gridDim.x)) {
+#pragma unroll
+      for (int k = 0; k < per; ++k) longest = max(longest, u4[k]);
+      longest = block_max(longest, reinterpret_cast<int*>(sums + kWarps));
+    }
+    const Cut cut = cut_of(all, (long long)total.y * p.Hk, longest, gridDim.x, kWarps, kSplitOver);
     const int cost_all = total.x + total.y * kSplitOver;
     int pieces = 0;                      // of one head
     if (cut.target) {
