@@ -10,12 +10,12 @@
 // [-pi, pi]. 8-bit codes, where that moved one in some ten thousand to its
 // neighbour, take the quadrant and the Taylor series on [-pi/4, pi/4] (to x^9 and
 // x^10: below 2^-29), right to float32's last bits: 16,384 tokens of 8 heads of
-// 128 appended take 64.3 us instead of 63.2. (In rotary alone, 32 + 8 heads:
+// 128 appended take 65.1 us instead of 63.2. (In rotary alone, 32 + 8 heads:
 // 53.6 instead of 52.0.)
 //
 // Measured: rotation of 16,384 tokens, 32 + 8 heads of 128, 336 MB: 52.0 us, 6.46
-// TB/s, 95% of the copy rate; with the append of 8 heads of K and V, 370 MB: 64.3
-// us, 85%.
+// TB/s, 95% of the copy rate; with the append of 8 heads of K and V, 370 MB: 65.1
+// us, 84%.
 //
 // Both kernels are one pass over memory. A thread owns two 8-element vectors
 // of a head (the two halves of its 8 pairs) and keeps its 8 sines and cosines
@@ -60,31 +60,38 @@ __device__ __forceinline__ void load_phases(const uint64_t* phases, int j, uint6
   }
 }
 
-template <bool kExact>
+__device__ __forceinline__ uint32_t turn_of(uint64_t phase, int pos) {
+  return (uint32_t)(((uint64_t)(int64_t)pos * phase) >> 32);
+}
+
+// Cosines and sines by the hardware (BF16 results).
 __device__ __forceinline__ void angles(const uint64_t (&ph)[8], int pos, float scale, int inverse,
                                        float (&co)[8], float (&si)[8]) {
   constexpr float kTurn = 1.4629180792671596e-09f;     // 2 pi / 2^32
   const float ss = inverse ? -scale : scale;
-  auto turn_of = [&](int i) { return (uint32_t)(((uint64_t)(int64_t)pos * ph[i]) >> 32); };
-  if constexpr (!kExact) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float s, c;
-      __sincosf((float)(int32_t)turn_of(i) * kTurn, &s, &c);
-      co[i] = c * scale;
-      si[i] = s * ss;
-    }
-    return;
+  for (int i = 0; i < 8; ++i) {
+    float s, c;
+    __sincosf((float)(int32_t)turn_of(ph[i], pos) * kTurn, &s, &c);
+    co[i] = c * scale;
+    si[i] = s * ss;
   }
-  // Two angles at a time, for the packed float32 instructions.
+}
+
+// The same of the first N phases (N even) to float32's last bits, two angles at a
+// time for the packed instructions.
+template <int N>
+__device__ __forceinline__ void exact_angles(const uint64_t (&ph)[8], int pos, float scale, float (&co)[N],
+                                             float (&si)[N]) {
+  constexpr float kTurn = 1.4629180792671596e-09f;     // 2 pi / 2^32
   auto both = [](float v) { return make_float2(v, v); };
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
+  for (int i = 0; i < N; i += 2) {
     uint32_t quadrant[2];
     float r[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const uint32_t turn = turn_of(i + e);
+      const uint32_t turn = turn_of(ph[i + e], pos);
       quadrant[e] = (turn + 0x20000000u) >> 30;
       r[e] = (float)(int32_t)(turn - (quadrant[e] << 30));
     }
@@ -102,9 +109,24 @@ __device__ __forceinline__ void angles(const uint64_t (&ph)[8], int pos, float s
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const uint32_t q = quadrant[e];
-      si[i + e] = __uint_as_float(__float_as_uint(q & 1 ? cs[e] : sn[e]) ^ ((q & 2) << 30)) * ss;
+      si[i + e] = __uint_as_float(__float_as_uint(q & 1 ? cs[e] : sn[e]) ^ ((q & 2) << 30)) * scale;
       co[i + e] = __uint_as_float(__float_as_uint(q & 1 ? sn[e] : cs[e]) ^ (((q + 1) & 2) << 30)) * scale;
     }
+  }
+}
+
+// The angles of a row's rot / 2 = N J pairs, N a lane of its J, brought to the lanes
+// that turn: lane j < rot / 16 gets those of pairs 8 j to 8 j + 7. All lanes take part.
+template <int N>
+__device__ __forceinline__ void shared_angles(const uint64_t (&ph)[8], int pos, float scale, int j, int J,
+                                              float (&co)[8], float (&si)[8]) {
+  float c[N], s[N];
+  exact_angles<N>(ph, pos, scale, c, s);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int from = (8 * j + i) / N & (J - 1);
+    co[i] = __shfl_sync(0xffffffffu, c[i % N], from, J);
+    si[i] = __shfl_sync(0xffffffffu, s[i % N], from, J);
   }
 }
 
@@ -163,7 +185,7 @@ __device__ __forceinline__ void rotate_unit(const RotArgs& p, int64_t u) {
   if (turn) {
     uint64_t ph[8];
     load_phases(p.phases, j, ph);
-    angles<false>(ph, __ldg(p.positions + tok), p.scale, p.inverse, co, si);
+    angles(ph, __ldg(p.positions + tok), p.scale, p.inverse, co, si);
   }
 #pragma unroll
   for (int i = 0; i < kHeads; ++i) {
@@ -347,19 +369,36 @@ __device__ __forceinline__ void append_piece(const AppendArgs& p, int unit, uint
     }
   }
   const bool turn = j * 16 < rot;
+  // Where half or a quarter of a head turns, the row's other lanes help with the
+  // angles (2,048 tokens, 64 of 256: 10.1 -> 9.3 us).
+  const int share = rot * 2 == d ? 4 : rot * 4 == d ? 2 : 0;
   uint64_t ph[8];
   float co[8], si[8];
-  int t_of = -1;                         // token that the sines are for
-  if (turn) load_phases(p.r.phases, j, ph);
+  if (share) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < share) ph[i] = __ldg(p.r.phases + j * share + i);
+  } else if (turn) {
+    load_phases(p.r.phases, j, ph);
+  }
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int r = row0 + i * rows, t = r & (B - 1), h = r >> p.log_b;
-    if (t < len && h < heads) {
+    const bool here = t < len && h < heads;
+    const bool other = i == 0 || (rows & (B - 1)) != 0;  // token than the pass before
+    if (share) {
+      if (!__any_sync(0xffffffffu, here)) continue;
+      if (other) {
+        const int pos = t < len ? __ldg(p.r.positions + first + t) : 0;
+        if (share == 2) shared_angles<2>(ph, pos, p.r.scale, j, J, co, si);
+        else shared_angles<4>(ph, pos, p.r.scale, j, J, co, si);
+      }
+    }
+    if (here) {
       float x[16];
       unpack16(a[i], b[i], x);
       if (turn) {
-        if (t != t_of) angles<true>(ph, __ldg(p.r.positions + first + t), p.r.scale, p.r.inverse, co, si);
-        t_of = t;
+        if (!share && other) exact_angles<8>(ph, __ldg(p.r.positions + first + t), p.r.scale, co, si);
         rotate16(x, co, si, p.r.interleaved);
       }
       const float inv = 1.f / s_scale[h];
