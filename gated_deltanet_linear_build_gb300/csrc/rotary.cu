@@ -489,12 +489,14 @@ gdn_status_t launch_rotary_kv_append(const void* q, int64_t q_stride, const void
   p.Hk = Hk;
   p.log_b = __builtin_ctz((unsigned)block_tokens);
   p.num_blocks = num_blocks;
-  // A rotation grows a coordinate by sqrt(2) at most, and `scale` multiplies it.
+  // A rotation grows a coordinate by sqrt(2) at most, and `scale` multiplies it; the
+  // values behind the rotated ones stay as they are, however small `scale` is.
   int grow = 0;
   if (rot > 0) {
     grow = 1;
     for (float s = 1.f; s < scale; s *= 2.f) ++grow;
     for (float s = 0.5f; s >= scale; s *= 0.5f) --grow;
+    if (rot < d) grow = std::max(grow, 0);
   }
   p.k_grow = grow;
   p.kc = static_cast<uint8_t*>(kc);

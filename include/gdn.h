@@ -561,10 +561,11 @@ GDN_API gdn_status_t gdn_rotary(const void* q, int64_t q_stride, const void* k,
  * Scales are powers of two, at least 2^-100. A piece that begins its block
  * (offset 0) sets the block's scale from its own tokens: the smallest power of
  * two that brings their largest finite magnitude to at most 448 (for a rotated
- * k, times 2 * 2^ceil(log2 scale): the most that the rotation can add). A piece
- * that continues a block keeps the larger of the block's scale and its own; if
- * the scale grew, the codes before `offset` are rounded to it. Rounding is to
- * nearest even; infinities become +-448 * scale and NaN stays NaN.
+ * k, times 2 * 2^ceil(log2 scale), the most that the rotation can add, and by no
+ * less than 1 where rot_dim < d: the values behind rot_dim are not scaled). A
+ * piece that continues a block keeps the larger of the block's scale and its
+ * own; if the scale grew, the codes before `offset` are rounded to it. Rounding
+ * is to nearest even; infinities become +-448 * scale and NaN stays NaN.
  *
  *   v           BF16 like k.   rot_dim  0 appends without rotation (q and q_out
  *               may then be NULL: nothing is done to q).

@@ -369,3 +369,45 @@ def test_whole_step_through_the_calls():
         ctx = kv.tolist()
         ref, a = R.attention(qo, kc, vc, ks, vs, table, new, ctx, d ** -0.5)
         assert ((o.cpu().double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -8 * a + 1e-6 * a.max()).all()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rot", [(64, 16), (128, 64), (256, 64), (256, 48), (64, 64), (128, 128)])
+@pytest.mark.parametrize("scale", [0.5, 0.25, 0.1, 2.0 ** -10])
+def test_append_with_a_small_scale_saturates_nothing(interleaved, d, rot, scale):
+    # Against the values, not the codes of another form: a code of 3 fraction bits is within 2^-4 of its
+    # value, or within 2^-10 of the block's scale where it is subnormal; the rotation adds 2^-21 of the
+    # pair's length (see the test of the angles). Values from rot on are not scaled and must not be clamped.
+    from gated_deltanet_linear_build_gb300 import gdn
+    rng = np.random.default_rng(d + rot)
+    B, Hk = 32, 3
+    new, ctx = [1, 40, 64, 5], [0, 7, 64, 31]
+    blocks, pos, pieces = make_step(rng, new, ctx, B)
+    T = sum(new)
+    _, k, v = make_qkv(rng, T, 1, Hk, d)
+    kc, vc, ks, vs = R.fill_cache(rng, blocks, Hk, B, d, "cuda", scale_exps=(-60, -50))
+    qo = torch.empty((T, 1, d), dtype=torch.bfloat16, device="cuda")
+    gdn.rotary_kv_append(k[:, :1], k, v, dev(pos), gdn.rotary_phases(rot, 10000.0), dev(pieces),
+                         dev([len(pieces)]), qo, kc, vc, ks, vs, interleaved=interleaved, scale=scale)
+    kd, f = k.cpu().double(), float(np.float32(scale))
+    kr = R.rotate(kd, pos, R.frequencies(rot, 10000.0), interleaved, f)
+    u, w = (kd[..., 0:rot:2], kd[..., 1:rot:2]) if interleaved else (kd[..., :rot // 2], kd[..., rot // 2:rot])
+    pair = torch.sqrt(u * u + w * w) * f
+    length = torch.zeros_like(kd)
+    length[..., :rot] = torch.stack([pair, pair], -1).flatten(-2) if interleaved else torch.cat([pair, pair], -1)
+    for values, got, s, room in ((kr, kc, ks, length), (v.cpu().double(), vc, vs, torch.zeros_like(kd))):
+        got, s = R.e4m3_values(got), s.cpu().double()
+        for block, first, count, off in pieces:
+            x = values[first:first + count].transpose(0, 1)
+            sc = s[block][:, None, None]
+            err = (got[block, :, off:off + count] * sc - x).abs()
+            lim = torch.maximum(2.0 ** -4 * x.abs(), 2.0 ** -10 * sc) + \
+                2.0 ** -20 * room[first:first + count].transpose(0, 1)
+            assert (err <= lim).all()
+    # And no coarser than the rule: the largest magnitude times what may multiply it.
+    grow = 1 + math.ceil(math.log2(f))
+    grow = max(grow, 0) if rot < d else grow
+    ref = R.append(kr, kd, pieces, R.e4m3_values(kc), torch.full_like(ks.cpu().double(), 2.0 ** -60), grow)[1]
+    for block, first, count, off in pieces:
+        if off == 0:
+            assert torch.equal(ks.cpu().double()[block], ref[block])
