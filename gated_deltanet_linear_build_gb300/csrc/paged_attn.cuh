@@ -242,6 +242,22 @@ __device__ __forceinline__ void pieces_of_line(Start& at, long long cost_before,
   at.pieces = (int)((first + at.it.units - 1) / per_cta) - at.c0 + 1;
 }
 
+// sum + y 2^x, with f = ex2_approx(x): 2^x alone may lie below float32's range where
+// the blocks' V scales lie far apart, and y above it by as much.
+__device__ __forceinline__ float add_scaled(float sum, float y, float f, float x) {
+  const float h = ex2_approx(0.5f * x);
+  return x < -100.f ? fmaf(y * h, h, sum) : fmaf(y, f, sum);
+}
+// A weight P' = 2^(s + log2 vs - m) of a small vs may be below float32's range though
+// P' / vs is as large as any. Where a unit's largest P' is 2^-kFarUnit or more, and the
+// V scales within it are within 2^kFarApart, what is lost is below 2^(kFarUnit +
+// kFarApart - 133) = 2^-33 of the unit's largest weight. In other units the sum takes
+// P' 2^100 instead, where 1 / vs makes room for that.
+constexpr float kFarUnit = 60.f, kFarApart = 40.f;
+// What the sum's exponents and factors change by, for a block of 1 / vs = iv.
+__device__ __forceinline__ float far_shift(float iv) { return iv >= 1.f ? 100.f : 0.f; }
+__device__ __forceinline__ float far_factor(float iv) { return iv >= 1.f ? iv * 7.888609052210118e-31f : iv; }
+
 // The split kernel's V chunk of lane group g.
 __device__ __forceinline__ int v_chunk(int g) { return (g >> 1) | ((g & 1) << 2); }
 // d of element `pos` of a row of O as the warps leave it: [m-tile k][g][2].

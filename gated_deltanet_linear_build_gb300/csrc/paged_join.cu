@@ -114,7 +114,7 @@ __device__ __forceinline__ void join_split(const Args& p, JoinShared& sh, int k0
       // NaN sums pass on: a NaN row has m = -inf and its l as it is.
       const float f = ml[k].x == -INFINITY ? 1.f : ex2_approx(ml[k].x - top);
       if (c < n) sh.split.f[c * rows + r] = f;
-      l += ml[k].y * f;
+      l = add_scaled(l, ml[k].y, f, ml[k].x - top);
     }
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
@@ -227,7 +227,7 @@ __device__ __forceinline__ void join_tile_few(const Args& p, JoinShared& sh, int
         const float2 ml = sh.ml[(c + i) * 32 + lane];
         // NaN sums pass on: a NaN row has m = -inf and its l as it is.
         const float f = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - top);
-        l = fmaf(ml.y, f, l);
+        l = add_scaled(l, ml.y, f, ml.x - top);
 #pragma unroll
         for (int k = 0; k < kCols; ++k) o[k] = fmaf(v[i][k], f, o[k]);
       }
@@ -260,7 +260,7 @@ __device__ __forceinline__ void join_tile_many(const Args& p, int c0, int y) {
     const float* q = part(c);
     const float mc = __ldcg(q);
     const float f = mc == -INFINITY ? 1.f : ex2_approx(mc - top);
-    l = fmaf(__ldcg(q + 128), f, l);
+    l = add_scaled(l, __ldcg(q + 128), f, mc - top);
 #pragma unroll
     for (int k = 0; k < kCols; ++k) o[k] = fmaf(__ldcg(q + (size_t)(2 + col0 + k) * 128), f, o[k]);
   }

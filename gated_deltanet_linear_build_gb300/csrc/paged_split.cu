@@ -154,6 +154,14 @@ __device__ __noinline__ bool take_nans(unsigned char* slot, int* first_nan, int 
   return any;
 }
 
+// This lane's sum of a unit's weights where V scales lie far apart (kFarUnit).
+__device__ __forceinline__ float far_sum(float4 x0, float4 x1, float ref, float iv0, float iv1) {
+  auto e = [](float x) { return ex2_approx(x); };
+  const float a = ref - far_shift(iv0), b = ref - far_shift(iv1);
+  return fmaf(e(x0.x - a) + e(x0.y - a) + e(x0.z - a) + e(x0.w - a), far_factor(iv0),
+              (e(x1.x - b) + e(x1.y - b) + e(x1.z - b) + e(x1.w - b)) * far_factor(iv1));
+}
+
 // Largest value of the block. (Out of line: few steps need it.)
 __device__ __noinline__ int block_max(int x, int* warps) {
   x = __reduce_max_sync(0xffffffffu, x);
@@ -445,7 +453,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       }
       rs[m] = s_qs[m * 8 + g] * p.scale_log2;
       const int r = m * 8 + g;
-      lim[m] = r < n_rows ? visible(s, (row0 + r) / G) : 0;
+      lim[m] = visible(s, (row0 + min(r, n_rows - 1)) / G);
       if (r < n_rows) min_lim = min(min_lim, lim[m]);
     }
     min_lim = __reduce_min_sync(0xffffffffu, min_lim);
@@ -474,6 +482,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         lvs[k] = lg2_approx(v);
         ivs[k] = __fdividef(1.f, v);
       }
+      const bool apart = fabsf(lvs[0] - lvs[1]) > kFarApart;
 #pragma unroll
       for (int k = 0; k + 1 < kAhead; ++k) sc_q[k] = sc_q[k + 1];
       // K of unit i has landed, and the slot before it is free again.
@@ -562,11 +571,13 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
           }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        if (__any_sync(0xffffffffu, mx > m_run[m] + 8.f)) {
-          const float m_new = fmaxf(mx, m_run[m]);
-          const float al = m_new > m_run[m] ? ex2_approx(m_run[m] - m_new) : 1.f;
+        // More than 8 above the running maximum, or kFarUnit below.
+        float far = 0.f;
+        if (__any_sync(0xffffffffu, apart || fabsf(mx - m_run[m] + (kFarUnit - 8.f) * 0.5f) > (kFarUnit + 8.f) * 0.5f)) {
+          const float m_old = m_run[m], m_new = fmaxf(mx, m_old);
+          const float al = m_new > m_old ? ex2_approx(m_old - m_new) : 1.f;
           m_run[m] = m_new;
-          l_run[m] *= al;
+          l_run[m] = add_scaled(0.f, l_run[m], al, m_new > m_old ? m_old - m_new : 0.f);
           const float a0 = __shfl_sync(0xffffffffu, al, 8 * t4);
           const float a1 = __shfl_sync(0xffffffffu, al, 8 * t4 + 4);
 #pragma unroll
@@ -576,6 +587,10 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
             acc[m][k][2] *= a0;
             acc[m][k][3] *= a1;
           }
+          if (__any_sync(0xffffffffu, apart || (mx < m_new - kFarUnit && mx > -INFINITY)))
+            far = far_sum(make_float4(sc[m][0][0], sc[m][0][1], sc[m][1][0], sc[m][1][1]),
+                          make_float4(sc[m][2][0], sc[m][2][1], sc[m][3][0], sc[m][3][1]),
+                          (m_new == -INFINITY ? 0.f : m_new) - 7.f, ivs[0], ivs[1]);
         }
         const float ref = (m_run[m] == -INFINITY ? 0.f : m_run[m]) - 7.f;
         float lsum = 0.f;
@@ -585,7 +600,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
           lsum = fmaf(p0 + p1, ivs[j >> 1], lsum);
           pf[m][j] = pack_half2(p0, p1);
         }
-        l_run[m] += lsum;
+        l_run[m] += far == 0.f ? lsum : far;
       }
       // O^T += V^T P^T: the two rows of m-tile k are bytes 2k and 2k + 1 of the
       // lane's own 16-byte chunk (8-byte one for d = 64) of the V rows.
@@ -668,7 +683,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         // A warp without keys has zeros; a NaN row keeps m = -inf and its l, a NaN.
         const float f = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - top);
         s_f[k * C::rows + tid] = f;
-        l += ml.y * f;
+        l = add_scaled(l, ml.y, f, ml.x - top);
       }
       s_l[tid * 2] = top;
       s_l[tid * 2 + 1] = l;

@@ -72,7 +72,8 @@ struct TC {
   static constexpr int o_k = o_q + M * 2 * q_part;
   static constexpr int o_vr = o_k + KS * c_stage;
   static constexpr int o_v = o_vr + VR * c_stage;
-  // Scales of a unit's 4 groups of 16 keys, float [8 units][ks | log2 vs | 1 / vs][4].
+  // Scales of a unit's 4 groups of 16 keys, float [8 units][ks | log2 vs | 1 / vs][4];
+  // 1 / vs is negative in units whose V scales lie far apart (kFarApart).
   // Unit n + KS is copied once the scores of n are done, so once the softmax of
   // n - 2 is: KS + 2 units are alive.
   static constexpr int o_sc = o_v + VS * v_stage;
@@ -559,7 +560,12 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
               float* sc = s_sc + (unit & 7) * 12;
               sc[lane] = a;
               sc[4 + lane] = lg2_approx(v);
-              sc[8 + lane] = __fdividef(1.f, v);
+              float iv = __fdividef(1.f, v);
+              if (log_box < 6) {                        // several blocks
+                const uint32_t ex = __float_as_uint(v) >> 23;
+                if (__reduce_max_sync(0xfu, ex) - __reduce_min_sync(0xfu, ex) >= (uint32_t)kFarApart) iv = -iv;
+              }
+              sc[8 + lane] = iv;
               tc::mbar_arrive(sc_full + (unit & 7));
             }
             __syncwarp();
@@ -783,7 +789,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         // first unit, and few others), once more on the new one.
         uint32_t pk[32];
         float lsum;
-        bool again;
+        bool again, far = false;
 #pragma unroll 1
         do {
           const float ref = (m_run == -INFINITY ? 0.f : m_run) - 7.f;
@@ -808,12 +814,19 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
                         t3 = max3(y[9], y[10], y[11]), t4 = max3(y[12], y[13], y[14]);
             mx = fmaxf(mx, fmaf(max3(max3(t0, t1, t2), max3(t3, t4, y[15]), -INFINITY), fa[gr], fb[gr]));
           }
+          again = false;
+          // More than 8 above the running maximum, or kFarUnit below.
+          const bool apart = fi[0] < 0.f;
+          if (!__any_sync(0xffffffffu, apart || fabsf(mx - m_run + (kFarUnit - 8.f) * 0.5f) > (kFarUnit + 8.f) * 0.5f))
+            break;
           again = __any_sync(0xffffffffu, mx > m_run + 8.f);
-          if (again) {
+          if (!again) {
+            far = __any_sync(0xffffffffu, apart || (mx < m_run - kFarUnit && mx > -INFINITY));
+          } else {
             const float m_new = fmaxf(mx, m_run);
-            const float al = m_new > m_run ? ex2_approx(m_run - m_new) : 1.f;
+            const float x_al = m_new > m_run ? m_run - m_new : 0.f, al = ex2_approx(x_al);
             m_run = m_new;
-            l_run *= al;
+            l_run = add_scaled(0.f, l_run, al, x_al);
             if (j > 0) {
               // The products of the unit before are in O; this unit's wait for P.
               ok = warp_wait(o_done + m * 2 + ((unit - 1) & 1), ((unit - 1) >> 1) & 1, s_abort);
@@ -832,6 +845,21 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
           }
         } while (again);
         if (!ok) break;
+        if (far) {                       // the sum anew, from the scores
+          const float ref = (m_run == -INFINITY ? 0.f : m_run) - 7.f;
+          lsum = 0.f;
+#pragma unroll 1
+          for (int gr = 0; gr < 4; ++gr) {
+            float y[16];
+            tmem_ld16(ts + gr * 16, y);
+            const float iv = fabsf(sc[8 + gr]), a = factor(rs * sc[gr]), b = sc[4 + gr] - ref + far_shift(iv);
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              sum += key0 + gr * 16 + k < lim ? ex2_approx(fmaf(y[k], a, b)) : 0.f;
+            lsum = fmaf(sum, far_factor(iv), lsum);
+          }
+        }
         l_run += lsum;
         tmem_st32_async(ts, pk);
         tmem_wait_st();

@@ -325,3 +325,32 @@ def test_a_step_repeats_bit_by_bit(Hq, Hk, d, decode):
                             softmax_scale=s["scale"], max_new_tokens=300)
         off += (o != first).any()
     assert int(off) == 0
+
+
+@pytest.mark.parametrize("new,B", [([1], 16), ([3, 1], 64), ([70], 16), ([300, 5], 64)])
+@pytest.mark.parametrize("Hq,Hk,d", [(8, 2, 64), (8, 2, 128), (16, 1, 128), (4, 1, 256)])
+@pytest.mark.parametrize("exps", [(-100, 34), (34, -100), (-100, 100), (100, -100), (-100, 40, 100), (-100, 0, -100, 100)])
+def test_value_scales_far_apart(new, B, Hq, Hk, d, exps):
+    # Keys of blocks whose V scale is 2^200 smaller than another's keep their share of the softmax.
+    kv = [l + 61 + 64 * 8 for l in new]
+    s = make(41, new, kv, Hq, Hk, d, B)
+    s["vs"].copy_(2.0 ** torch.tensor(exps, device="cuda")[torch.arange(len(s["vs"]), device="cuda") % len(exps)]
+                  .float()[:, None].expand_as(s["vs"]))
+    check(s, run(s))
+    # In sequence order: all of one scale first.
+    n = -(-kv[0] // B)
+    s["vs"][s["table"][0, :n].long()] = 2.0 ** torch.tensor([exps[min(i * len(exps) // n, len(exps) - 1)] for i in range(n)],
+                                                            device="cuda").float()[:, None]
+    check(s, run(s))
+
+
+@pytest.mark.parametrize("new,B", [([2], 16), ([70], 16), ([300], 64)])
+def test_blocks_of_zeros_keep_their_share(new, B):
+    # As the append leaves them: a block of zeros has the smallest scale.
+    s = make(42, new, [new[0] + 500], 8, 2, 128, B)
+    s["vs"].copy_(2.0 ** torch.tensor([40.0, 100.0], device="cuda")[torch.arange(len(s["vs"]), device="cuda") % 2]
+                  [:, None].expand_as(s["vs"]))
+    zero = s["table"][0, 0:-(-s["kvl"][0] // B):3].long()
+    s["vc"].view(torch.uint8)[zero] = 0
+    s["vs"][zero] = 2.0 ** -100
+    check(s, run(s))
