@@ -248,15 +248,21 @@ __device__ __forceinline__ float add_scaled(float sum, float y, float f, float x
   const float h = ex2_approx(0.5f * x);
   return x < -100.f ? fmaf(y * h, h, sum) : fmaf(y, f, sum);
 }
+// The sum of the weights P' / vs is kept 2^-16 times: P' reaches 2^15 and 1 / vs 2^100,
+// so that 4,096 keys of the smallest scale would pass float32's range.
+constexpr float kSumScale = 1.f / 65536.f;
+// What a row's outputs are to be multiplied by, for its sum l; put_one does.
+__device__ __forceinline__ float over_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float put_one(float o, float il) { return o * kSumScale * il; }
 // A weight P' = 2^(s + log2 vs - m) of a small vs may be below float32's range though
 // P' / vs is as large as any. Where a unit's largest P' is 2^-kFarUnit or more, and the
 // V scales within it are within 2^kFarApart, what is lost is below 2^(kFarUnit +
 // kFarApart - 133) = 2^-33 of the unit's largest weight. In other units the sum takes
 // P' 2^100 instead, where 1 / vs makes room for that.
 constexpr float kFarUnit = 60.f, kFarApart = 40.f;
-// What the sum's exponents and factors change by, for a block of 1 / vs = iv.
-__device__ __forceinline__ float far_shift(float iv) { return iv >= 1.f ? 100.f : 0.f; }
-__device__ __forceinline__ float far_factor(float iv) { return iv >= 1.f ? iv * 7.888609052210118e-31f : iv; }
+// What the sum's exponents and factors change by, for a block of kSumScale / vs = iv.
+__device__ __forceinline__ float far_shift(float iv) { return iv >= kSumScale ? 100.f : 0.f; }
+__device__ __forceinline__ float far_factor(float iv) { return iv >= kSumScale ? iv * 7.888609052210118e-31f : iv; }
 
 // The split kernel's V chunk of lane group g.
 __device__ __forceinline__ int v_chunk(int g) { return (g >> 1) | ((g & 1) << 2); }
@@ -278,10 +284,10 @@ template <int D>
 __device__ __forceinline__ void put_row4(const RowsOut& t, int r, int pos, float4 o, float l) {
   if (r >= t.n_rows) return;
   const int row = t.row0 + r, tok = row / t.G;
-  const float il = l == 0.f ? 0.f : 1.f / l;
+  const float il = over_sum(l);
   __nv_bfloat16* at = t.o + ((int64_t)(t.first + tok) * t.Hq + t.head * t.G + row - tok * t.G) * D;
-  *reinterpret_cast<uint32_t*>(at + d_of<D>(pos)) = pack_bf16x2(o.x * il, o.y * il);
-  *reinterpret_cast<uint32_t*>(at + d_of<D>(pos + 2)) = pack_bf16x2(o.z * il, o.w * il);
+  *reinterpret_cast<uint32_t*>(at + d_of<D>(pos)) = pack_bf16x2(put_one(o.x, il), put_one(o.y, il));
+  *reinterpret_cast<uint32_t*>(at + d_of<D>(pos + 2)) = pack_bf16x2(put_one(o.z, il), put_one(o.w, il));
 }
 
 }  // namespace attn

@@ -177,7 +177,7 @@ template <int N>
 __device__ __forceinline__ void put_cols(__nv_bfloat16* at, const float (&v)[N], float il) {
   uint32_t w[N / 2];
 #pragma unroll
-  for (int k = 0; k < N / 2; ++k) w[k] = pack_bf16x2(v[2 * k] * il, v[2 * k + 1] * il);
+  for (int k = 0; k < N / 2; ++k) w[k] = pack_bf16x2(put_one(v[2 * k], il), put_one(v[2 * k + 1], il));
   if constexpr (N % 8 == 0) {
 #pragma unroll
     for (int k = 0; k < N / 2; k += 4)
@@ -234,7 +234,7 @@ __device__ __forceinline__ void join_tile_few(const Args& p, JoinShared& sh, int
   }
   if (row < next.len * G)
     put_cols(p.o + ((int64_t)(next.first + tok) * p.Hq + next.head * G + row - tok * G) * D + col0, o,
-             l == 0.f ? 0.f : 1.f / l);
+             over_sum(l));
 }
 
 // Many tiles, of two or three pieces: CTA (c0, y) takes the one, if any, that CTA c0
@@ -265,7 +265,7 @@ __device__ __forceinline__ void join_tile_many(const Args& p, int c0, int y) {
     for (int k = 0; k < kCols; ++k) o[k] = fmaf(__ldcg(q + (size_t)(2 + col0 + k) * 128), f, o[k]);
   }
   put_cols(p.o + ((int64_t)(next.first + tok) * p.Hq + next.head * G + row - tok * G) * D + col0, o,
-           l == 0.f ? 0.f : 1.f / l);
+           over_sum(l));
 }
 
 // CTAs [0, split_ctas): the split kernel's items, `cuts` of them at most; the

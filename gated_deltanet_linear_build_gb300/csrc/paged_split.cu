@@ -480,7 +480,7 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         ksc[k] = __shfl_sync(0xffffffffu, sc_q[0], k);
         const float v = fmaxf(__shfl_sync(0xffffffffu, sc_q[0], 2 + k), 7.888609052210118e-31f);   // 2^-100
         lvs[k] = lg2_approx(v);
-        ivs[k] = __fdividef(1.f, v);
+        ivs[k] = __fdividef(kSumScale, v);
       }
       const bool apart = fabsf(lvs[0] - lvs[1]) > kFarApart;
 #pragma unroll

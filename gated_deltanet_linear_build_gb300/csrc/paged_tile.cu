@@ -72,8 +72,8 @@ struct TC {
   static constexpr int o_k = o_q + M * 2 * q_part;
   static constexpr int o_vr = o_k + KS * c_stage;
   static constexpr int o_v = o_vr + VR * c_stage;
-  // Scales of a unit's 4 groups of 16 keys, float [8 units][ks | log2 vs | 1 / vs][4];
-  // 1 / vs is negative in units whose V scales lie far apart (kFarApart).
+  // Scales of a unit's 4 groups of 16 keys, float [8 units][ks | log2 vs | kSumScale /
+  // vs][4]; the last is negative in units whose V scales lie far apart (kFarApart).
   // Unit n + KS is copied once the scores of n are done, so once the softmax of
   // n - 2 is: KS + 2 units are alive.
   static constexpr int o_sc = o_v + VS * v_stage;
@@ -560,7 +560,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
               float* sc = s_sc + (unit & 7) * 12;
               sc[lane] = a;
               sc[4 + lane] = lg2_approx(v);
-              float iv = __fdividef(1.f, v);
+              float iv = __fdividef(kSumScale, v);
               if (log_box < 6) {                        // several blocks
                 const uint32_t ex = __float_as_uint(v) >> 23;
                 if (__reduce_max_sync(0xfu, ex) - __reduce_min_sync(0xfu, ex) >= (uint32_t)kFarApart) iv = -iv;
@@ -875,7 +875,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       const bool whole = g.count == g.n_units;
       __nv_bfloat16* out = p.o + ((int64_t)(g.s.first + tok) * p.Hq + hq) * D;
       const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
-      const float il = l_run == 0.f ? 0.f : 1.f / l_run;
+      const float il = over_sum(l_run);
       const size_t part_sz = (size_t)(D + 2) * 128;
       float* part = p.tile_partials +
                     (((size_t)blockIdx.x * 2 + (g.first_unit == 0 ? 1 : 0)) * kM + m) * part_sz;
@@ -894,7 +894,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         if (whole) {
           if (live) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] *= il;
+            for (int k = 0; k < 32; ++k) v[k] = put_one(v[k], il);
             store16(out + c, v, wide);
             store16(out + c + 16, v + 16, wide);
           }

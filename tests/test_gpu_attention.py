@@ -354,3 +354,24 @@ def test_blocks_of_zeros_keep_their_share(new, B):
     s["vc"].view(torch.uint8)[zero] = 0
     s["vs"][zero] = 2.0 ** -100
     check(s, run(s))
+
+
+@pytest.mark.parametrize("new,N,keys", [(1, 400, 40000), (65, 160, 24000)])
+def test_many_keys_of_the_smallest_scale(new, N, keys):
+    # 2^-100 times every weight: sums of weights of up to 2^15 times 2^100 each. Equal sequences share blocks.
+    d, B = 64, 64
+    s = make(43, [new], [keys], 1, 1, d, B)
+    s["kc"].view(torch.uint8)[:] = 0
+    low = s["table"][0, :512 // B].long()                        # the first 512 keys are 2^-7.9 of the others
+    s["kc"][..., 0] = torch.ones((), device="cuda").to(torch.float8_e4m3fn)
+    s["kc"].view(torch.uint8)[low] = 0
+    s["ks"].fill_(1.0)
+    s["vs"].fill_(2.0 ** -100)
+    s["q"].fill_(0.0)
+    s["q"][..., 0] = 7.90625
+    s["scale"] = 0.6931471805599453
+    ref, a = R.attention(s["q"], s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["new"], s["kvl"], s["scale"])
+    many = dict(s, q=s["q"].repeat(N, 1, 1), table=s["table"].repeat(N, 1), kv=s["kv"].repeat(N), new=[new] * N,
+                cu=torch.arange(N + 1, dtype=torch.int32, device="cuda") * new)
+    o = run(many).cpu().double().view(N, new, 1, d)
+    assert ((o - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -8 * a + 1e-6 * a.max()).all()
