@@ -752,9 +752,10 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
       ok = ok && warp_wait(q_full + (seg & 1), (seg >> 1) & 1, s_abort);
       if (!ok) break;
       const int ex = s_ex[(seg & 1) * kRows + m * 128 + r];
-      const float rs = fabsf(p.scale_log2) * (ex == -128 ? __int_as_float(0x7fffffff)
-                                                         : __int_as_float((ex + 127) << 23));
       const int lim = live ? visible(g.s, tok) : 0;
+      // A row without keys has zeros whatever its q holds: no NaN meets its masked scores.
+      const float rs = lim == 0 ? 0.f : fabsf(p.scale_log2) * (ex == -128 ? __int_as_float(0x7fffffff)
+                                                                          : __int_as_float((ex + 127) << 23));
       const int min_lim = visible(g.s, (g.row0 + m * 128) / G);
       const int nan_base = visible(g.s, g.row0 / G) - kKeys;
       const bool part_tile = m * 128 + 128 > g.n_rows;

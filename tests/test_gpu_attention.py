@@ -375,3 +375,16 @@ def test_many_keys_of_the_smallest_scale(new, N, keys):
                 cu=torch.arange(N + 1, dtype=torch.int32, device="cuda") * new)
     o = run(many).cpu().double().view(N, new, 1, d)
     assert ((o - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -8 * a + 1e-6 * a.max()).all()
+
+
+@pytest.mark.parametrize("Hq,Hk,d", [(4, 2, 64), (8, 2, 128), (4, 1, 256)])
+@pytest.mark.parametrize("new,kv", [([4], [2]), ([140], [100]), ([300], [0]), ([1, 1], [0, 5])])
+def test_rows_without_keys_are_zero_whatever_q_holds(Hq, Hk, d, new, kv):
+    s = make(44, new, kv, Hq, Hk, d, 16)
+    empty = max(0, new[0] - kv[0])
+    s["q"][:empty] = float("nan")
+    s["q"][0, 0] = float("inf")
+    o = run(s)
+    assert (o[:empty] == 0).all()
+    s["q"][:empty] = 0.0
+    check(s, o)
