@@ -77,9 +77,11 @@ Cache cache(PyObject* const* a) {
   Cache c;
   c.k = &tensor(a[0], "k_cache: an 8-bit CUDA tensor expected");
   c.v = &tensor(a[1], "v_cache: an 8-bit CUDA tensor expected");
-  if (c.k->element_size() != 1 || c.v->element_size() != 1 || c.k->dim() != 4 || !same(*c.k, *c.v) ||
-      !c.k->is_contiguous() || !c.v->is_contiguous())
-    throw Refused{"k_cache, v_cache: contiguous 8-bit [num_blocks, Hk, B, d] expected"};
+  // e4m3 codes, or their bytes: another 8-bit type would be read as e4m3 all the same.
+  for (const at::TensorBase* t : {c.k, c.v})
+    if ((t->scalar_type() != at::kFloat8_e4m3fn && t->scalar_type() != at::kByte) || t->dim() != 4 ||
+        !t->is_contiguous() || !same(*t, *c.k))
+      throw Refused{"k_cache, v_cache: contiguous float8_e4m3fn or uint8 [num_blocks, Hk, B, d] expected"};
   c.ks = &packed(a[2], at::kFloat, 2, "k_scale: contiguous float32 [num_blocks, Hk] expected");
   c.vs = &packed(a[3], at::kFloat, 2, "v_scale: contiguous float32 [num_blocks, Hk] expected");
   for (const at::TensorBase* s : {c.ks, c.vs})

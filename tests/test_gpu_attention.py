@@ -388,3 +388,20 @@ def test_rows_without_keys_are_zero_whatever_q_holds(Hq, Hk, d, new, kv):
     assert (o[:empty] == 0).all()
     s["q"][:empty] = 0.0
     check(s, o)
+
+
+@pytest.mark.parametrize("dtype", [torch.float8_e5m2, torch.int8, torch.bool])
+def test_caches_of_another_8_bit_type_are_refused(dtype):
+    from gated_deltanet_linear_build_gb300 import gdn
+    s = make(45, [1, 1], [20, 30], 4, 2, 64, 16)
+    for key in ("kc", "vc"):
+        with pytest.raises(ValueError):
+            run(dict(s, **{key: s[key].view(dtype)}))
+    k = s["q"][:, :2].contiguous()
+    pieces = torch.tensor([[0, 0, 2, 0]], dtype=torch.int32, device="cuda")
+    before = s["kc"].view(torch.uint8).clone()
+    with pytest.raises(ValueError):
+        gdn.rotary_kv_append(None, k, k, None, None, pieces, pieces[0, 2:3], None, s["kc"].view(dtype),
+                             s["vc"].view(dtype), s["ks"], s["vs"])
+    assert torch.equal(before, s["kc"].view(torch.uint8))
+    assert torch.equal(run(s), run(dict(s, kc=s["kc"].view(torch.uint8), vc=s["vc"].view(torch.uint8))))
