@@ -121,7 +121,10 @@ __device__ void build_list(const PlanArgs& p, const ListArgs& a, PlanShared<kPla
   int2* sums = sh.sums;
   int* s_first = sh.first;
   items = units = 0;
-  for (int n0 = 0; n0 < p.N; n0 += kPlanThreads) {
+  // Well-formed offsets have no more tiles than the list has room for. With others,
+  // sequences may overlap: tiles beyond the room are dropped, and their units with
+  // them, so that the line is as long as its items.
+  for (int n0 = 0; n0 < p.N && items < a.cap; n0 += kPlanThreads) {
     int tiles = 0;
     Seq s = {0, 0, 0};
     if (n0 + tid < p.N) {
@@ -129,7 +132,7 @@ __device__ void build_list(const PlanArgs& p, const ListArgs& a, PlanShared<kPla
       const int64_t r = (int64_t)s.len * p.G;
       if (r > a.above && r <= a.upto) tiles = (int)((r + a.rows - 1) / a.rows);
     }
-    if (!__syncthreads_or(tiles > 1)) {
+    if (!__syncthreads_or(tiles > 1) && min(kPlanThreads, p.N - n0) <= a.cap - items) {
       // One tile a sequence: one scan gives its place and its units.
       Item it = {0, 0, 0, 0};
       if (tiles) it = item_of(p, a, s, n0 + tid, 0);
@@ -137,7 +140,7 @@ __device__ void build_list(const PlanArgs& p, const ListArgs& a, PlanShared<kPla
       const int2 inc = block_scan<kPlanThreads>(make_int2(tiles, it.units), sums, tot);
       it.cum = units + inc.y - it.units;
       const int at = items + inc.x - 1;
-      if (tiles && at < a.cap) {
+      if (tiles) {
         a.items[at] = it;
         if (at < kPlanThreads) sh.items[at] = it;
       }
@@ -145,14 +148,16 @@ __device__ void build_list(const PlanArgs& p, const ListArgs& a, PlanShared<kPla
       units += tot.y;
       continue;
     }
+    // The tiles' sum in two parts: with overlapping sequences it may pass 32 bits.
     int2 tot;
-    const int2 inc = block_scan<kPlanThreads>(make_int2(tiles, 0), sums, tot);
-    s_first[tid] = inc.x - tiles;
+    const int2 inc = block_scan<kPlanThreads>(make_int2(tiles & 0xfff, tiles >> 12), sums, tot);
+    s_first[tid] = (int)min(inc.x + ((long long)inc.y << 12) - tiles, 0x7fffffffll);
+    const int here = (int)min(tot.x + ((long long)tot.y << 12), (long long)(a.cap - items));
     __syncthreads();
-    for (int i0 = 0; i0 < tot.x; i0 += kPlanThreads) {
+    for (int i0 = 0; i0 < here; i0 += kPlanThreads) {
       const int i = i0 + tid;
       Item it = {0, 0, 0, 0};
-      if (i < tot.x && items + i < a.cap) {    // beyond: malformed offsets only
+      if (i < here) {
         int lo = 0, hi = kPlanThreads - 1;     // last sequence whose first tile is <= i
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
@@ -163,16 +168,15 @@ __device__ void build_list(const PlanArgs& p, const ListArgs& a, PlanShared<kPla
       int2 tot_units;
       const int2 cum = block_scan<kPlanThreads>(make_int2(0, it.units), sums, tot_units);
       it.cum = units + cum.y - it.units;
-      if (i < tot.x && items + i < a.cap) {
+      if (i < here) {
         a.items[items + i] = it;
         if (items + i < kPlanThreads) sh.items[items + i] = it;
       }
       units += tot_units.y;
     }
-    items += tot.x;
+    items += here;
     __syncthreads();                           // s_first is free again
   }
-  items = min(items, a.cap);
 }
 
 // Every CTA's piece of the list's line.

@@ -405,3 +405,53 @@ def test_caches_of_another_8_bit_type_are_refused(dtype):
                              s["vc"].view(dtype), s["ks"], s["vs"])
     assert torch.equal(before, s["kc"].view(torch.uint8))
     assert torch.equal(run(s), run(dict(s, kc=s["kc"].view(torch.uint8), vc=s["vc"].view(torch.uint8))))
+
+
+def plan_records(ws, which, grid):
+    """(starts, items) of one kernel's list in a workspace: dicts of int arrays."""
+    starts_at = 0 if which == "split" else 2 * 320 * 64
+    raw = ws.cpu().numpy()
+    st = raw[starts_at:starts_at + grid * 64].view(np.int32).reshape(grid, 16)
+    names = ("item", "head", "num", "units", "seq", "row0", "item_units", "cum", "first", "len", "kv", "c0")
+    out = {k: st[:, i].astype(np.int64) for i, k in enumerate(names)}
+    out["u"] = raw[starts_at:starts_at + grid * 64].view(np.int64).reshape(grid, 8)[:, 6]
+    out["count"], out["pieces"] = st[:, 14].astype(np.int64), st[:, 15].astype(np.int64)
+    return out
+
+
+@pytest.mark.parametrize("N", [300, 1100, 3000])
+@pytest.mark.parametrize("Hq,Hk,d,short", [(16, 2, 64, 20), (8, 8, 128, 70), (16, 1, 256, 8)])
+def test_overlapping_sequences_stay_inside_the_plan(N, Hq, Hk, d, short):
+    # Offsets that go back and forth: more tiles than a well-formed step of T tokens has. Every CTA's piece
+    # lies inside its item, the pieces are the line, and a call ends with the rows that the sequences share.
+    from gated_deltanet_linear_build_gb300 import gdn
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    T, kv, B = 600, 700, 64
+    s = make(48, [T], [kv], Hq, Hk, d, B)
+    want = run(s)
+    cu = np.where(np.arange(N + 1) % 2 == 0, 0, np.where(np.arange(N + 1) < 1024, T, short))
+    bad = dict(s, cu=torch.tensor(cu, dtype=torch.int32, device="cuda"), kv=s["kv"].repeat(N),
+               table=s["table"].repeat(N, 1), new=[T] + [0] * (N - 1))
+    ws = torch.empty(gdn.paged_attention_workspace_size(T, N, Hq, Hk, d), dtype=torch.uint8, device="cuda")
+    gdn.paged_attention_plan(bad["cu"], bad["kv"], ws, T=T, Hq=Hq, Hk=Hk, d=d, block_tokens=B,
+                             max_blocks=s["table"].shape[1], max_new_tokens=T)
+    p = plan_records(ws, "tile", min(sms, 160))
+    work = p["count"] > 0
+    assert work.any() and (p["units"] == p["units"][0]).all()
+    if (p["c0"] >= 0).all():                                     # a line cut into pieces
+        first = p["u"] - p["head"] * p["units"] - p["cum"]
+        assert (p["head"][work] < Hk).all() and (p["item"][work] < p["num"][work]).all()
+        assert (first[work] >= 0).all() and (first[work] < p["item_units"][work]).all()
+        assert (p["u"][1:][work[1:]] == (p["u"] + p["count"])[:-1][work[1:]]).all()
+        assert p["count"].sum() == p["units"][0] * Hk and p["u"][0] == 0
+        last = p["num"] - 1 == p["item"]                          # the last item ends the line
+        assert ((p["cum"] + p["item_units"])[last & work] == p["units"][last & work]).all()
+    else:                                                        # whole items
+        assert p["count"].sum() == p["num"][0] * Hk
+    o = run(bad, workspace=ws)
+    st = torch.empty(1, dtype=torch.int32, device="cuda")
+    gdn.device_status(st, clear=True)
+    assert int(st) == gdn.GDN_OK
+    # Equal ranges end at T and, behind sequence 1024, at `short`: the rows of the former are the whole step's.
+    rows = slice(short, T) if N > 1024 else slice(0, T)
+    assert torch.equal(o[rows], want[rows]) or (o[rows].float() - want[rows].float()).abs().max() <= 2.0 ** -6
