@@ -43,6 +43,8 @@ gdn_status_t check_plan(const int32_t* cu, const int32_t* kv, int32_t N, int32_t
   if (max_blocks < 0 || max_new_tokens < 0) return GDN_ERR_INVALID_ARG;
   if (!cache_dim_ok(d) || !block_tokens_ok(block_tokens) || Hq / Hk > 16)
     return GDN_ERR_UNSUPPORTED;
+  // Keys are counted in 32 bits, up to a few units past a sequence's end.
+  if ((int64_t)max_blocks * block_tokens > 0x7fffffff - 1023) return GDN_ERR_UNSUPPORTED;
   if (N == 0 || T == 0) {
     *nothing = true;
     return GDN_OK;
@@ -232,7 +234,9 @@ gdn_status_t gdn_paged_attention(const void* q, int64_t q_stride, const void* k_
       !aligned(v_scale, 4) || !aligned(block_table, 4))
     return GDN_ERR_ALIGNMENT;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool self_plan = (flags & GDN_FLAG_PLANNED) == 0 && attn::self_planned(N, T, Hq / Hk, max_new_tokens);
+  const bool self_plan = (flags & GDN_FLAG_PLANNED) == 0 && attn::self_planned(
+                                                              N, T, Hq / Hk, Hk, max_new_tokens,
+                                                              (int64_t)max_blocks * block_tokens);
   if ((flags & GDN_FLAG_PLANNED) == 0 && !self_plan) {
     rc = launch_attn_plan(cu_seqlens, kv_lens, N, T, Hq, Hk, d,
                           (int64_t)max_blocks * block_tokens, max_new_tokens, workspace, st);

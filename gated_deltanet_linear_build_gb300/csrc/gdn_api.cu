@@ -63,6 +63,7 @@ gdn_status_t gdn_device_status(int32_t* status, int32_t clear, void* stream) {
   if ((rc = gather_status_conv(status, clear, 0, st)) != GDN_OK) return rc;
   if ((rc = gather_status_decode(status, clear, 0, st)) != GDN_OK) return rc;
   if ((rc = gather_status_prefill_tc(status, clear, 0, st)) != GDN_OK) return rc;
+  if ((rc = gather_status_attn_plan(status, clear, 0, st)) != GDN_OK) return rc;
   if ((rc = gather_status_attn_split(status, clear, 0, st)) != GDN_OK) return rc;
   return gather_status_attn_tile(status, clear, 0, st);
 }

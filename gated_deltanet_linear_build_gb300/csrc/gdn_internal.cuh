@@ -296,6 +296,7 @@ gdn_status_t gather_status_api(int32_t* out, int clear, int first, cudaStream_t 
 gdn_status_t gather_status_conv(int32_t* out, int clear, int first, cudaStream_t st);
 gdn_status_t gather_status_decode(int32_t* out, int clear, int first, cudaStream_t st);
 gdn_status_t gather_status_prefill_tc(int32_t* out, int clear, int first, cudaStream_t st);
+gdn_status_t gather_status_attn_plan(int32_t* out, int clear, int first, cudaStream_t st);
 gdn_status_t gather_status_attn_split(int32_t* out, int clear, int first, cudaStream_t st);
 gdn_status_t gather_status_attn_tile(int32_t* out, int clear, int first, cudaStream_t st);
 #define GDN_DEFINE_STATUS_GATHER(name)                                                   \

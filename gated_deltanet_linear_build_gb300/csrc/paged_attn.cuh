@@ -68,14 +68,21 @@ inline Kernels kernels_of(int N, int T, int G, int Hk, int max_new_tokens, int64
   }
   return k;
 }
+// A list's units and costs are 32-bit numbers. Units that one head's line may have
+// (kv_max: the table's width), in sequences of any length up to it.
+inline int64_t most_units(int64_t tiles, int64_t kv_max, int keys) {
+  const int64_t kv = kv_max < 0x7fffffff ? kv_max : 0x7fffffff;
+  return tiles * ((kv + keys - 1) / keys);
+}
+constexpr int64_t kMaxUnits = 1 << 30;
 constexpr int kSelfPlan = 512;
 // Whether the split kernel's CTAs can plan the step by themselves: one tile a
 // sequence, no more of them than one block scans. A decode step of 32 requests
 // takes 17.0 us with a plan of its own, and 19.4 us with the
 // plan's kernel.
-inline bool self_planned(int N, int T, int G, int max_new_tokens) {
+inline bool self_planned(int N, int T, int G, int Hk, int max_new_tokens, int64_t kv_max) {
   const int64_t longest = N == 1 ? T : max_new_tokens;
-  return N <= kSelfPlan && longest * G <= split_rows(G);
+  return N <= kSelfPlan && longest * G <= split_rows(G) && most_units(N, kv_max, kUnit) * Hk <= kMaxUnits;
 }
 
 // CTAs of the split kernel: one wave.

@@ -51,6 +51,7 @@ using namespace attn;
 struct ListArgs {
   int rows, keys, above, upto, cap, grid;          // tiles of the sequences with above < rows <= upto
   int least, over;                                 // units of a piece; of an item's overhead (Cut)
+  int wide;                                        // the units may pass 32 bits
   Item *items, *sorted;                            // sorted: room for the items by length, or null
   Start* starts;
 };
@@ -115,12 +116,30 @@ __device__ __forceinline__ Item item_of(const PlanArgs& p, const ListArgs& a, co
   return it;
 }
 
+// Whether `units` more of each thread keep the list's costs within 32 bits; `all` is
+// their sum, over all calls.
+template <int kPlanThreads>
+__device__ bool room_for(const PlanArgs& p, const ListArgs& a, int2* sums, int units, long long& all) {
+  int2 tot;
+  block_scan<kPlanThreads>(make_int2(units & 0xfff, units >> 12), sums, tot);
+  all += tot.x + ((long long)tot.y << 12);
+  return all <= kMaxUnits && all * p.Hk <= kMaxUnits * a.grid;
+}
+
 template <int kPlanThreads>
 __device__ void build_list(const PlanArgs& p, const ListArgs& a, PlanShared<kPlanThreads>& sh, int& items, int& units) {
   const int tid = threadIdx.x;
   int2* sums = sh.sums;
   int* s_first = sh.first;
   items = units = 0;
+  long long all = 0;                   // units as a 64-bit number, of wide lists
+  // A list whose units do not fit is left empty, and the step with it unwritten.
+  auto fits = [&](int more) {
+    if (!a.wide || room_for<kPlanThreads>(p, a, sums, more, all)) return true;
+    items = units = 0;
+    if (tid == 0) record_device_status(GDN_ERR_UNSUPPORTED);
+    return false;
+  };
   // Well-formed offsets have no more tiles than the list has room for. With others,
   // sequences may overlap: tiles beyond the room are dropped, and their units with
   // them, so that the line is as long as its items.
@@ -136,6 +155,7 @@ __device__ void build_list(const PlanArgs& p, const ListArgs& a, PlanShared<kPla
       // One tile a sequence: one scan gives its place and its units.
       Item it = {0, 0, 0, 0};
       if (tiles) it = item_of(p, a, s, n0 + tid, 0);
+      if (!fits(it.units)) return;
       int2 tot;
       const int2 inc = block_scan<kPlanThreads>(make_int2(tiles, it.units), sums, tot);
       it.cum = units + inc.y - it.units;
@@ -165,6 +185,7 @@ __device__ void build_list(const PlanArgs& p, const ListArgs& a, PlanShared<kPla
         }
         it = item_of(p, a, seq_of(p.cu, p.kv, n0 + lo, p.T, p.kv_max), n0 + lo, i - s_first[lo]);
       }
+      if (!fits(it.units)) return;
       int2 tot_units;
       const int2 cum = block_scan<kPlanThreads>(make_int2(0, it.units), sums, tot_units);
       it.cum = units + cum.y - it.units;
@@ -362,23 +383,29 @@ gdn_status_t launch_attn_plan(const int32_t* cu, const int32_t* kv, int N, int T
   p.Hk = Hk;
   p.kv_max = kv_max;
   int lists = 0;
+  const int64_t rows = (int64_t)T * G;
+  auto wide = [&](int tile_rows, int keys, int grid) {
+    const int64_t most = most_units(rows / tile_rows + N, kv_max, keys);
+    return most > kMaxUnits || most * Hk > kMaxUnits * grid;
+  };
   // A piece of the split kernel gives each of its 8 warps a unit at least.
   if (use.split)
     p.list[lists++] = {l.split_rows, kUnit, 0, limit, l.item_cap, split_grid(d, l.split_rows), kWarps,
-                       kSplitOver, reinterpret_cast<Item*>(ws + l.items), nullptr,
+                       kSplitOver, wide(l.split_rows, kUnit, split_grid(d, l.split_rows)), reinterpret_cast<Item*>(ws + l.items), nullptr,
                        reinterpret_cast<Start*>(ws + l.starts)};
   if (use.tile)
     p.list[lists++] = {l.tile_rows, kTileKeys, limit, 0x7fffffff, l.tile_cap, tile_grid(), 1,
-                       kItemCost, reinterpret_cast<Item*>(ws + l.tiles),
+                       kItemCost, wide(l.tile_rows, kTileKeys, tile_grid()), reinterpret_cast<Item*>(ws + l.tiles),
                        reinterpret_cast<Item*>(ws + l.sorted_tiles),
                        reinterpret_cast<Start*>(ws + l.tile_starts)};
   // A warp more is a turn more for every instruction of the others: 256 threads
   // where they hold the sequences and the items (4 prompts: 6.1 -> 4.7 us).
-  const int64_t rows = (int64_t)T * G;
   const bool small = N <= 256 && (!use.split || rows / l.split_rows + N <= 256) &&
                      (!use.tile || rows / l.tile_rows + N <= 256);
   return check_launch(small ? launch_pdl(attn_plan_kernel<256>, dim3(lists), dim3(256), 0, st, p)
                             : launch_pdl(attn_plan_kernel<1024>, dim3(lists), dim3(1024), 0, st, p));
 }
+
+GDN_DEFINE_STATUS_GATHER(gather_status_attn_plan)
 
 }  // namespace gdn

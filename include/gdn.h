@@ -611,9 +611,13 @@ GDN_API gdn_status_t gdn_paged_attention_plan(const int32_t* cu_seqlens, const i
  *
  *   q           BF16 as above.   o  BF16 [T, Hq, d] contiguous (output).
  *   block_table device int32 [N, table_stride], row n naming the blocks of
- *               sequence n; kv_lens beyond max_blocks * B are cut off there. A
+ *               sequence n; kv_lens beyond max_blocks * B are cut off there
+ *               (max_blocks * B <= 2^31 - 1024, else GDN_ERR_UNSUPPORTED). A
  *               block outside [0, num_blocks) reads as zeros and is reported as
- *               GDN_ERR_INVALID_ARG by gdn_device_status.
+ *               GDN_ERR_INVALID_ARG by gdn_device_status. So is, as
+ *               GDN_ERR_UNSUPPORTED, a step whose row tiles see more than 2^35
+ *               keys together (of one kv head; 2^42 of all): o may then be left
+ *               unwritten.
  *   max_new_tokens  an upper bound of the l_n (1 for a decode step). It chooses the
  *               kernels; the rows of a longer sequence may be left unwritten.
  *   flags       0 or GDN_FLAG_PLANNED.

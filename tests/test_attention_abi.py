@@ -144,3 +144,11 @@ def test_phases(lib):
     assert all(abs(a / 4 - b) <= 2 ** 11 for a, b in zip(plain, out[:32]))
     assert f(64, 10000.0, 2, 4.0, 4096.0, 32.0, 1.0, out) == OK
     assert out[0] == plain[0] and abs(plain[31] / 4 - out[31]) <= 2 ** 11
+
+
+def test_tables_of_2_31_keys_a_row_are_refused(lib):
+    f, big = lib.gdn_paged_attention_plan, 1 << 30
+    for B in (16, 128):
+        assert f(A, A, 2, 4, 8, 2, 128, B, (1 << 31) // B, 2, A, big, None) == UNSUPPORTED
+        assert attend(lib, B=B, mb=(1 << 31) // B - 1, stride=1 << 40) == UNSUPPORTED
+    assert attend(lib, B=128, mb=(1 << 31) // 128 - 8, stride=1 << 40, ws=None) == WORKSPACE

@@ -455,3 +455,29 @@ def test_overlapping_sequences_stay_inside_the_plan(N, Hq, Hk, d, short):
     # Equal ranges end at T and, behind sequence 1024, at `short`: the rows of the former are the whole step's.
     rows = slice(short, T) if N > 1024 else slice(0, T)
     assert torch.equal(o[rows], want[rows]) or (o[rows].float() - want[rows].float()).abs().max() <= 2.0 ** -6
+
+
+@pytest.mark.parametrize("new,N,d,which", [(1, 200, 128, "split"), (1, 700, 64, "split"), (256, 40, 64, "tile"), (3000, 30, 256, "tile")])
+def test_a_plan_whose_units_pass_32_bits_is_reported_and_left_empty(new, N, d, which):
+    # Lengths of 2^31 - 1024 keys, as shared blocks would allow; the plan reads no table.
+    from gated_deltanet_linear_build_gb300 import gdn
+    props = torch.cuda.get_device_properties(0).multi_processor_count
+    T, Hq, Hk, B = new * N, 2, 2, 128
+    cu = torch.arange(N + 1, dtype=torch.int32, device="cuda") * new
+    ws = torch.empty(gdn.paged_attention_workspace_size(T, N, Hq, Hk, d), dtype=torch.uint8, device="cuda")
+    st = torch.empty(1, dtype=torch.int32, device="cuda")
+    gdn.device_status(st, clear=True)
+
+    def plan(kv, blocks):
+        ws.fill_(0x5A)
+        gdn.paged_attention_plan(cu, torch.full((N,), kv, dtype=torch.int32, device="cuda"), ws, T=T, Hq=Hq, Hk=Hk, d=d,
+                                 block_tokens=B, max_blocks=blocks, max_new_tokens=new)
+        gdn.device_status(st, clear=True)
+        return plan_records(ws, which, min(props, 160) if which == "tile" else props * (2 if d <= 128 else 1)), int(st)
+    p, status = plan(0x7fffffff, (1 << 24) - 8)
+    assert status == gdn.GDN_ERR_UNSUPPORTED and (p["count"] == 0).all() and (p["num"] == 0).all()
+    # A table as wide, of sequences that are not as long, is planned as ever.
+    p, status = plan(new + 5000, (1 << 24) - 8)
+    q, ok = plan(new + 5000, -(-(new + 5000) // B))
+    assert status == ok == gdn.GDN_OK and p["count"].sum() > 0
+    assert all(np.array_equal(p[k], q[k]) for k in p)
