@@ -295,8 +295,9 @@ __device__ __forceinline__ void append_piece(const AppendArgs& p, int unit, uint
   const int4 pc = __ldg(reinterpret_cast<const int4*>(p.pieces) + pi);
   const int block = pc.x, first = pc.y, len = pc.z, off = pc.w;
   const int B = 1 << p.log_b;
-  if (block < 0 || block >= p.num_blocks || off < 0 || len <= 0 || off + len > B || first < 0 ||
-      first + len > p.r.T)
+  // (Differences: the sums of arbitrary numbers may pass 32 bits.)
+  if (block < 0 || block >= p.num_blocks || off < 0 || off >= B || len <= 0 || len > B - off || first < 0 ||
+      first > p.r.T - len)
     return;
   const int J = 1 << p.r.log_j, d = 16 << p.r.log_j;
   const int j = tid & (J - 1), row0 = tid >> p.r.log_j;

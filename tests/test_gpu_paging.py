@@ -411,3 +411,17 @@ def test_append_with_a_small_scale_saturates_nothing(interleaved, d, rot, scale)
     for block, first, count, off in pieces:
         if off == 0:
             assert torch.equal(ks.cpu().double()[block], ref[block])
+
+
+def test_append_skips_pieces_whose_sums_pass_32_bits():
+    from gated_deltanet_linear_build_gb300 import gdn
+    rng = np.random.default_rng(11)
+    _, k, v = make_qkv(rng, 4, 1, 1, 64)
+    kc, vc, ks, vs = R.fill_cache(rng, 3, 1, 16, 64, "cuda")
+    before = [x.clone() for x in (kc.view(torch.uint8), vc.view(torch.uint8), ks, vs)]
+    top = 2 ** 31 - 1
+    bad = [[0, top, 1, 0], [0, top - 15, 16, 0], [0, 5, top, 1], [0, 1, top, 15], [0, 0, 1, top], [1, 0, 4, top - 1],
+           [top, 0, 1, 0], [-top - 1, 0, 1, 0], [0, -top - 1, 4, 0], [0, 0, -top - 1, 0], [0, 0, 4, -top - 1]]
+    gdn.rotary_kv_append(None, k, v, None, None, dev(bad), dev([len(bad)]), None, kc, vc, ks, vs)
+    for x, y in zip(before, (kc.view(torch.uint8), vc.view(torch.uint8), ks, vs)):
+        assert torch.equal(x, y)
