@@ -460,12 +460,15 @@ def paged_attention_plan(cu_seqlens, kv_lens, workspace, *, T: int, Hq: int, Hk:
                          block_tokens: int, max_blocks: int, max_new_tokens: int, stream=None):
     """Build the step's row tiles into ``workspace``; the step's attention
     calls then pass planned=True. max_blocks = block_table.shape[1]."""
-    for t, name in ((cu_seqlens, "cu_seqlens"), (kv_lens, "kv_lens")):
-        if t.dtype != torch.int32 or not t.is_contiguous():
-            raise ValueError(f"{name}: contiguous int32 expected")
+    N = cu_seqlens.numel() - 1
+    for t, n, name in ((cu_seqlens, N + 1, "cu_seqlens"), (kv_lens, N, "kv_lens")):
+        if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous int32 [{n}] on the device expected")
+    if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace: a contiguous tensor on the device expected")
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     rc = _lib().gdn_paged_attention_plan(
-        _ptr(cu_seqlens), _ptr(kv_lens), cu_seqlens.numel() - 1, T,
+        _ptr(cu_seqlens), _ptr(kv_lens), N, T,
         Hq, Hk, d, block_tokens, max_blocks, max_new_tokens, _ptr(workspace), nbytes,
         _stream(stream))
     _check(rc, "gdn_paged_attention_plan")

@@ -152,3 +152,28 @@ def test_tables_of_2_31_keys_a_row_are_refused(lib):
         assert f(A, A, 2, 4, 8, 2, 128, B, (1 << 31) // B, 2, A, big, None) == UNSUPPORTED
         assert attend(lib, B=B, mb=(1 << 31) // B - 1, stride=1 << 40) == UNSUPPORTED
     assert attend(lib, B=128, mb=(1 << 31) // 128 - 8, stride=1 << 40, ws=None) == WORKSPACE
+
+
+def test_plan_refuses_host_tensors_and_other_lengths(monkeypatch):
+    import torch
+    from gated_deltanet_linear_build_gb300 import gdn
+
+    class OnDevice(torch.Tensor):
+        is_cuda = True
+
+    def on(t):
+        return t.as_subclass(OnDevice)
+    calls = []
+    monkeypatch.setattr(gdn, "_lib", lambda: type("L", (), {"gdn_paged_attention_plan": lambda self, *a: calls.append(a) or 0})())
+    monkeypatch.setattr(gdn, "_stream", lambda s=None: 0)
+    kw = dict(T=4, Hq=8, Hk=2, d=128, block_tokens=64, max_blocks=5, max_new_tokens=2)
+    cu, kv = torch.tensor([0, 2, 4], dtype=torch.int32), torch.tensor([5, 6], dtype=torch.int32)
+    ws = torch.zeros(1024, dtype=torch.uint8)
+    for a in ((cu, on(kv), on(ws)), (on(cu), kv, on(ws)), (on(cu), on(kv), ws), (on(cu), on(kv[:1]), on(ws)),
+              (on(cu.long()), on(kv), on(ws)), (on(cu), on(torch.arange(4, dtype=torch.int32)[::2]), on(ws)),
+              (on(cu), on(kv), on(ws[::2])), (on(cu), on(kv[:, None]), on(ws))):
+        with pytest.raises(ValueError):
+            gdn.paged_attention_plan(*a, **kw)
+    assert not calls
+    gdn.paged_attention_plan(on(cu), on(kv), on(ws), **kw)
+    assert calls[0][2:4] == (2, 4) and calls[0][11] == 1024
