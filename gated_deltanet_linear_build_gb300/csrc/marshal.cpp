@@ -62,6 +62,11 @@ float real(PyObject* o) {
   if (v == -1.0 && PyErr_Occurred()) throw Refused{nullptr};
   return (float)v;
 }
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Refused{nullptr};
+  return v != 0;
+}
 void* stream(PyObject* o) {
   if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
   void* s = PyLong_AsVoidPtr(o);
@@ -170,7 +175,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     return gdn_rotary(q.data_ptr(), qs, kp, ks, ptr<int32_t>(pos), ptr<int64_t>(ph), qo.data_ptr(), qos,
                       kop, kos, fits(T), fits(q.size(1)), fits(Hk), fits(d), fits(2 * ph.size(0)),
-                      PyObject_IsTrue(a[6]), PyObject_IsTrue(a[7]), real(a[8]), stream(a[9]));
+                      truth(a[6]), truth(a[7]), real(a[8]), stream(a[9]));
   });
 }
 
@@ -214,7 +219,7 @@ PyObject* rotary_kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                 ptr<gdn_page_piece_t>(pieces), ptr<int32_t>(num), fits(pieces.size(0)),
                                 qop, qos, c.k->data_ptr(), c.v->data_ptr(), ptr<float>(*c.ks),
                                 ptr<float>(*c.vs), c.blocks, c.B, fits(T), fits(Hq), c.Hk, c.d,
-                                fits(rot), PyObject_IsTrue(a[12]), real(a[13]), stream(a[14]));
+                                fits(rot), truth(a[12]), real(a[13]), stream(a[14]));
   });
 }
 
@@ -244,7 +249,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                ptr<float>(*c.vs), c.blocks, c.B, ptr<int32_t>(table), stride, fits(M),
                                ptr<int32_t>(cu), ptr<int32_t>(kv), fits(N), fits(q.size(0)),
                                int32(a[11]), o.data_ptr(), fits(q.size(1)), c.Hk, c.d, real(a[10]),
-                               PyObject_IsTrue(a[12]) ? GDN_FLAG_PLANNED : 0, ws, bytes, stream(a[13]));
+                               truth(a[12]) ? GDN_FLAG_PLANNED : 0, ws, bytes, stream(a[13]));
   });
 }
 

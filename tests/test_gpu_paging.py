@@ -425,3 +425,18 @@ def test_append_skips_pieces_whose_sums_pass_32_bits():
     gdn.rotary_kv_append(None, k, v, None, None, dev(bad), dev([len(bad)]), None, kc, vc, ks, vs)
     for x, y in zip(before, (kc.view(torch.uint8), vc.view(torch.uint8), ks, vs)):
         assert torch.equal(x, y)
+
+
+def test_options_without_a_truth_value_raise_their_own_error():
+    from gated_deltanet_linear_build_gb300 import gdn
+    x = torch.zeros((2, 1, 64), dtype=torch.bfloat16, device="cuda")
+    pos, ph, neither = dev([0, 1]), gdn.rotary_phases(16, 10000.0), np.array([True, False])
+    for kw in (dict(interleaved=neither), dict(inverse=neither)):
+        with pytest.raises(ValueError, match="truth value"):
+            gdn.rotary(x, None, pos, ph, x, None, **kw)
+    kc, vc, ks, vs = R.fill_cache(np.random.default_rng(1), 3, 1, 16, 64, "cuda")
+    with pytest.raises(ValueError, match="truth value"):
+        gdn.rotary_kv_append(x, x, x, pos, ph, dev([[0, 0, 2, 0]]), dev([1]), x, kc, vc, ks, vs, interleaved=neither)
+    with pytest.raises(ValueError, match="truth value"):
+        gdn.paged_attention(x, kc, vc, ks, vs, dev([[0]]), dev([0, 2]), dev([2]), x, x, softmax_scale=1.0,
+                            max_new_tokens=2, planned=neither)
