@@ -10,6 +10,7 @@
 #include <exception>
 
 #include <ATen/core/TensorBase.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -21,10 +22,13 @@ struct Refused {                       // a failed check: ValueError
   const char* what;
 };
 
+int current_device = 0;                // of the call that runs (under the interpreter's lock)
+
 const at::TensorBase& tensor(PyObject* o, const char* what) {
   if (!THPVariable_Check(o)) throw Refused{what};
   const at::TensorBase& t = THPVariable_Unpack(o);
   if (!t.is_cuda()) throw Refused{what};
+  if (t.get_device() != current_device) throw Refused{"a tensor is not on the current device"};
   return t;
 }
 // A contiguous tensor of `dim` dimensions.
@@ -115,6 +119,7 @@ PyObject* call(Py_ssize_t n, Py_ssize_t want, F body) {
     return nullptr;
   }
   try {
+    current_device = c10::cuda::current_device();
     return PyLong_FromLong(body());
   } catch (const Refused& r) {
     if (r.what) PyErr_SetString(PyExc_ValueError, r.what);

@@ -370,7 +370,7 @@ def delta_rule_prefill_chunked_slots(q, k, v, a, b, cu_seqlens, S, has_initial_s
 # Softmax-attention layers over a paged 8-bit cache. The cache of one layer:
 # k_cache, v_cache [num_blocks, Hk, B, d] of e4m3 codes (torch.float8_e4m3fn or
 # uint8), k_scale, v_scale [num_blocks, Hk] float32, all contiguous; B is 16,
-# 32, 64 or 128 tokens.
+# 32, 64 or 128 tokens. Tensors are on the current device, and so is `stream`.
 # ----------------------------------------------------------------------------
 
 ROTARY_SCALINGS = {"plain": 0, "linear": 1, "by_parts": 2}

@@ -440,3 +440,16 @@ def test_options_without_a_truth_value_raise_their_own_error():
     with pytest.raises(ValueError, match="truth value"):
         gdn.paged_attention(x, kc, vc, ks, vs, dev([[0]]), dev([0, 2]), dev([2]), x, x, softmax_scale=1.0,
                             max_new_tokens=2, planned=neither)
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="one device")
+def test_tensors_of_another_device_are_refused():
+    from gated_deltanet_linear_build_gb300 import gdn
+    x = torch.zeros((2, 1, 64), dtype=torch.bfloat16, device="cuda:0")
+    pos, ph = dev([0, 1]), gdn.rotary_phases(16, 10000.0)
+    for bad in ((x.to("cuda:1"), pos, ph, x), (x, pos.to("cuda:1"), ph, x), (x, pos, ph.to("cuda:1"), x),
+                (x, pos, ph, x.to("cuda:1"))):
+        with pytest.raises(ValueError):
+            gdn.rotary(bad[0], None, bad[1], bad[2], bad[3], None)
+    with torch.cuda.device(1), pytest.raises(ValueError):
+        gdn.rotary(x, None, pos, ph, x, None)
