@@ -50,10 +50,12 @@ using namespace attn;
 
 // ---------------------------------------------------------------------------
 // MMA and copy wrappers
+// The MMAs are volatile: they stay in front of the copy that refills the slot whose
+// keys they take (see `issue`).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm(
+  asm volatile(
       "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -61,7 +63,7 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm(
+  asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -352,6 +354,13 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
     // two halves and V's.
     constexpr int kAhead = C::slots / 2;
     float sc_q[kAhead];
+    // Half unit h into the ring's next slot, whose last one this warp has read: the
+    // copy must not land before those reads have their data, and it is not ordered
+    // behind loads that are merely issued. It need not be: every load from a slot feeds
+    // an MMA of the same half unit, a warp issues in program order, and an MMA issues
+    // only once its registers have arrived. So it is enough that a slot's MMAs stand in
+    // front of its refill: they and the copy are volatile, with the wait for the next
+    // half unit between them, and __syncwarp() joins the lanes.
     auto issue = [&](int h, int q) {
       const int i = h >> 1, is_v = h & 1;
       if (i >= mine || dead) return;

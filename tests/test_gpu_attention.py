@@ -481,3 +481,21 @@ def test_a_plan_whose_units_pass_32_bits_is_reported_and_left_empty(new, N, d, w
     q, ok = plan(new + 5000, -(-(new + 5000) // B))
     assert status == ok == gdn.GDN_OK and p["count"].sum() > 0
     assert all(np.array_equal(p[k], q[k]) for k in p)
+
+
+@pytest.mark.parametrize("Hq,Hk,d", [(12, 1, 64), (32, 2, 64), (8, 2, 128), (24, 2, 128), (16, 1, 128), (16, 2, 256), (12, 1, 256),
+                                     (16, 1, 256)])
+def test_a_decode_step_repeats_bit_by_bit(Hq, Hk, d):
+    # The split kernel alone, both of its row forms: its ring's slots are refilled while a unit is computed.
+    from gated_deltanet_linear_build_gb300 import gdn
+    kv = list(range(50, 2050, 100)) + [9000, 31, 4096, 700]
+    s = make(33, [1] * len(kv), kv, Hq, Hk, d, 32)
+    ws = torch.empty(gdn.paged_attention_workspace_size(len(kv), len(kv), Hq, Hk, d), dtype=torch.uint8, device="cuda")
+    first = run(s, workspace=ws)
+    check(s, first)
+    o, off = torch.empty_like(first), torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(4000):
+        gdn.paged_attention(s["q"], s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["cu"], s["kv"], o, ws,
+                            softmax_scale=s["scale"], max_new_tokens=1)
+        off += (o != first).any()
+    assert int(off) == 0
