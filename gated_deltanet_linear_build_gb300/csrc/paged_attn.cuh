@@ -145,17 +145,20 @@ struct Args {
   float* tile_partials;
 };
 
-// Lengths of sequence n, malformed ones as an empty sequence.
+// Lengths of sequence n, malformed ones as an empty sequence. kPlain: without
+// ld.global.nc, for a kernel that reads them without a wait of its own.
 struct Seq {
   int first, len, kv;
 };
+template <bool kPlain = false>
 __device__ __forceinline__ Seq seq_of(const int32_t* cu, const int32_t* kv, int n, int T,
                                       int64_t kv_max) {
+  auto at = [](const int32_t* p) { return kPlain ? *p : __ldg(p); };
   Seq s;
-  s.first = __ldg(cu + n);
-  s.len = __ldg(cu + n + 1) - s.first;
+  s.first = at(cu + n);
+  s.len = at(cu + n + 1) - s.first;
   if (s.first < 0 || s.len < 0 || s.first > T - s.len) s.first = s.len = 0;
-  const int64_t k = __ldg(kv + n);
+  const int64_t k = at(kv + n);
   s.kv = (int)(k < 0 ? 0 : k > kv_max ? kv_max : k);
   return s;
 }

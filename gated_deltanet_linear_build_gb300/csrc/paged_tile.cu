@@ -280,9 +280,9 @@ __device__ __forceinline__ void pass(const Args& p, Line& l, const Seg& g) {
     }
   }
   if (l.more()) {
-    const int4 raw = __ldg(reinterpret_cast<const int4*>(from) + l.lo);
+    const int4 raw = reinterpret_cast<const int4*>(from)[l.lo];
     l.it = {raw.x, raw.y, raw.z, raw.w};
-    l.s = seq_of(p.cu, p.kv, l.it.seq, p.T, (int64_t)p.max_blocks << p.log_b);
+    l.s = seq_of<true>(p.cu, p.kv, l.it.seq, p.T, (int64_t)p.max_blocks << p.log_b);
   }
 }
 
@@ -394,10 +394,14 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
-  // Behind the split kernel, the plan and the step's inputs are two launches back,
-  // hence complete: this kernel goes on as soon as it has an SM, and waits for the
-  // split kernel at its end, for those that follow. The fence takes the place of
-  // the wait's acquire: nothing that this SM's L1 holds from before is read.
+  // Behind the split kernel, the plan and the step's inputs are two launches back:
+  // this kernel goes on as soon as it has an SM, and waits for the split kernel at its
+  // end, for those that follow. Why it may: it can start only when every CTA of the
+  // split kernel has let it, which each does behind its own wait, so all that this
+  // kernel reads was complete, and in L2, before its first instruction; and what the
+  // split kernel writes it does not read. TMA reads L2. What this SM's L1 holds from
+  // earlier kernels the fence (an acquire at GPU scope) discards, and the loads behind
+  // it are plain, coherent ones: no ld.global.nc, for which a fence promises nothing.
   if constexpr (kAfterSplit) {
     __threadfence();
   } else {
@@ -529,7 +533,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
         const int n = g.count;
         auto id_at = [&](int i) {
           const int key = key_first + i * kKeys + page * box_keys;
-          return i < n && key < g.key_end ? __ldg(table + (key >> p.log_b)) : -1;
+          return i < n && key < g.key_end ? table[key >> p.log_b] : -1;
         };
         int next = id_at(0);
         for (int i = 0; i < n; ++i) {
@@ -553,8 +557,8 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
             if (lane < 4) {
               float a = 1.f, v = 1.f;
               if (key0 + lane * 16 < g.key_end && (unsigned)blk < (unsigned)p.num_blocks) {
-                a = __ldg(p.ks + (size_t)blk * p.Hk + l.head);
-                v = __ldg(p.vs + (size_t)blk * p.Hk + l.head);
+                a = p.ks[(size_t)blk * p.Hk + l.head];
+                v = p.vs[(size_t)blk * p.Hk + l.head];
               }
               v = fmaxf(v, 7.888609052210118e-31f);     // 2^-100
               float* sc = s_sc + (unit & 7) * 12;
@@ -616,7 +620,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
                                      (int64_t)(l.head * G + qrow - qt * G) * D + cq * 8;
 #pragma unroll
           for (int k = 0; k < passes; ++k)
-            w[k] = local < g.n_rows ? ldg16(src + k * 32) : make_uint4(0, 0, 0, 0);
+            w[k] = local < g.n_rows ? *reinterpret_cast<const uint4*>(src + k * 32) : make_uint4(0, 0, 0, 0);
         };
         uint4 w[passes], ahead[passes];
         fetch(0, ahead);
