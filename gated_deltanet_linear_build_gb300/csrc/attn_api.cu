@@ -11,6 +11,8 @@ namespace {
 bool block_tokens_ok(int b) { return b == 16 || b == 32 || b == 64 || b == 128; }
 bool cache_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
 bool rotary_dim_ok(int d) { return d == 16 || d == 32 || cache_dim_ok(d); }
+// Loops over sequences or tokens in strides of a block or a grid end below 2^31.
+constexpr int32_t kMaxCount = 0x7fff0000;
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // A BF16 tensor of T tokens x H heads x d values, read or written by rows.
@@ -41,7 +43,7 @@ gdn_status_t check_plan(const int32_t* cu, const int32_t* kv, int32_t N, int32_t
   *nothing = false;
   if (N < 0 || T < 0 || Hq <= 0 || Hk <= 0 || Hq % Hk != 0) return GDN_ERR_INVALID_ARG;
   if (max_blocks < 0 || max_new_tokens < 0) return GDN_ERR_INVALID_ARG;
-  if (!cache_dim_ok(d) || !block_tokens_ok(block_tokens) || Hq / Hk > 16)
+  if (!cache_dim_ok(d) || !block_tokens_ok(block_tokens) || Hq / Hk > 16 || N > kMaxCount)
     return GDN_ERR_UNSUPPORTED;
   // Keys are counted in 32 bits, up to a few units past a sequence's end.
   if ((int64_t)max_blocks * block_tokens > 0x7fffffff - 1023) return GDN_ERR_UNSUPPORTED;
@@ -72,7 +74,7 @@ gdn_status_t gdn_build_block_tables(const int32_t* cu_seqlens, const int32_t* co
   if (N < 0 || T < 0 || num_free < 0 || max_blocks < 0 || piece_capacity < 0 ||
       table_stride < max_blocks)
     return GDN_ERR_INVALID_ARG;
-  if (!block_tokens_ok(block_tokens)) return GDN_ERR_UNSUPPORTED;
+  if (!block_tokens_ok(block_tokens) || N > kMaxCount || T > kMaxCount) return GDN_ERR_UNSUPPORTED;
   if (N == 0) return T == 0 ? GDN_OK : GDN_ERR_INVALID_ARG;
   if (!cu_seqlens || !context_lens || !kv_lens || !counts) return GDN_ERR_INVALID_ARG;
   if ((num_free > 0 && !free_blocks) || (max_blocks > 0 && !block_table) ||
@@ -189,7 +191,8 @@ gdn_status_t gdn_rotary_kv_append(const void* q, int64_t q_stride, const void* k
 
 size_t gdn_paged_attention_workspace_size(int32_t T, int32_t N, int32_t Hq, int32_t Hk,
                                           int32_t d) {
-  if (T < 0 || N < 0 || Hq <= 0 || Hk <= 0 || Hq % Hk != 0 || Hq / Hk > 16 || !cache_dim_ok(d))
+  if (T < 0 || N < 0 || Hq <= 0 || Hk <= 0 || Hq % Hk != 0 || Hq / Hk > 16 || !cache_dim_ok(d) ||
+      N > kMaxCount)
     return 0;
   if ((int64_t)T * (Hq / Hk) > 0x3fffffff || (int64_t)N * Hk > 0x7fffffff) return 0;
   return attn::layout(T, N, Hq, Hk, d).total;

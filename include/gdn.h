@@ -498,7 +498,8 @@ typedef struct gdn_page_piece_t {
  *                 GDN_ERR_WORKSPACE when the free list, a row of the table or
  *                 `pieces` is too short. In both cases the counts are 0, every
  *                 slot is -1, and nothing else is written.
- * One launch. N = 0 enqueues nothing; T = 0 writes kv_lens and the counts.
+ * One launch. N = 0 enqueues nothing; T = 0 writes kv_lens and the counts. N and T
+ * beyond 2^31 - 65536 are GDN_ERR_UNSUPPORTED (N in the attention calls too).
  */
 GDN_API gdn_status_t gdn_build_block_tables(
     const int32_t* cu_seqlens, const int32_t* context_lens, const int32_t* free_blocks,

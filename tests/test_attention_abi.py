@@ -177,3 +177,12 @@ def test_plan_refuses_host_tensors_and_other_lengths(monkeypatch):
     assert not calls
     gdn.paged_attention_plan(on(cu), on(kv), on(ws), **kw)
     assert calls[0][2:4] == (2, 4) and calls[0][11] == 1024
+
+
+def test_counts_at_the_end_of_32_bits_are_refused(lib):
+    top = (1 << 31) - 1
+    for n in (top, top - 65535 + 1):
+        assert tables(lib, N=n) == UNSUPPORTED and tables(lib, T=n) == UNSUPPORTED
+        assert attend(lib, N=n, Hq=1, Hk=1, bytes=1 << 60) == UNSUPPORTED
+        assert lib.gdn_paged_attention_workspace_size(4, n, 1, 1, 128) == 0
+    assert lib.gdn_paged_attention_workspace_size(4, top - 65535, 1, 1, 128) > 0
