@@ -499,3 +499,106 @@ def test_a_decode_step_repeats_bit_by_bit(Hq, Hk, d):
                             softmax_scale=s["scale"], max_new_tokens=1)
         off += (o != first).any()
     assert int(off) == 0
+
+
+@pytest.mark.parametrize("new,kv", [([1, 1, 2], [700, 60, 9]), ([150, 40], [400, 40]), ([1, 90, 1], [900, 333, 20])])
+@pytest.mark.parametrize("scale", [-0.11, 0.0, -0.0])
+def test_softmax_scales_of_any_sign(new, kv, scale):
+    s = make(46, new, kv, 8, 2, 128, 32)
+    s["scale"] = scale
+    check(s, run(s))
+
+
+@pytest.mark.parametrize("new,kv", [([1, 2], [700, 60]), ([150, 90], [400, 2000]), ([300], [300])])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_outputs_off_a_32_byte_boundary_and_wide_tables(new, kv, d):
+    from gated_deltanet_linear_build_gb300 import gdn
+    s = make(47, new, kv, 4, 1, d, 32)
+    a = run(s)
+    check(s, a)
+    T, N, M = sum(new), len(new), s["table"].shape[1]
+    wide = torch.full((N, M + 5), -1, dtype=torch.int32, device="cuda")
+    wide[:, :M] = s["table"]
+    buf = torch.full((T * 4 * d + 8,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    o = buf[8:].view(T, 4, d)
+    assert o.data_ptr() % 32 == 16
+    ws = torch.empty(gdn.paged_attention_workspace_size(T, N, 4, 1, d), dtype=torch.uint8, device="cuda")
+    gdn.paged_attention(s["q"], s["kc"], s["vc"], s["ks"], s["vs"], wide[:, :M], s["cu"], s["kv"], o, ws,
+                        softmax_scale=s["scale"], max_new_tokens=max(new))
+    assert torch.equal(o, a) and torch.isnan(buf[:8]).all()
+
+
+@pytest.mark.parametrize("decode,prompts,planned", [(20, 3, False), (20, 3, True), (0, 3, True), (24, 0, False)])
+def test_steps_in_a_graph(decode, prompts, planned):
+    # Tables, append and attention of two layers captured once; replays on other inputs in the same buffers
+    # equal the calls made one by one.
+    from gated_deltanet_linear_build_gb300 import gdn
+    Hq, Hk, d, B = 16, 4, 128, 32
+    new = [1] * decode + [130, 90, 300][:prompts]
+    ctx = list(range(50, 50 + 60 * decode, 60)) + [700, 1200, 0][:prompts]
+    N, T, L = len(new), sum(new), 2
+    want = [-(-(c + l) // B) for c, l in zip(ctx, new)]
+    blocks, width = sum(want), max(want)
+    ids = np.random.default_rng(5).permutation(blocks)
+    table, free, at = np.zeros((N, width), np.int32), [], 0
+    for n in range(N):
+        have = -(-ctx[n] // B)
+        table[n, :want[n]] = ids[at:at + want[n]]
+        free += list(table[n, have:want[n]])
+        table[n, have:] = 0
+        at += want[n]
+
+    def ints(a):
+        return torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+    cu, ctx_d, free_d, tab0 = ints(np.concatenate([[0], np.cumsum(new)])), ints(ctx), ints(free + [0]), ints(table)
+    tab, kv, pos, counts = tab0.clone(), ints([0] * N), ints([0] * T), ints([0, 0])
+    slots, pieces = torch.zeros(T, dtype=torch.int64, device="cuda"), ints(np.zeros((T // B + 2 * N, 4)))
+    kc0, vc0, ks0, vs0 = R.fill_cache(np.random.default_rng(6), L * blocks, Hk, B, d, "cuda")
+    cache = [x.clone().unflatten(0, (L, blocks)) for x in (kc0, vc0, ks0, vs0)]
+    x = torch.zeros((L, T, (Hq + 2 * Hk) * d), dtype=torch.bfloat16, device="cuda")
+    q_rot, o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device="cuda"), torch.empty((L, T, Hq, d), dtype=torch.bfloat16, device="cuda")
+    ph = gdn.rotary_phases(64, 10000.0)
+    ws = torch.empty(gdn.paged_attention_workspace_size(T, N, Hq, Hk, d), dtype=torch.uint8, device="cuda")
+
+    def step():
+        gdn.build_block_tables(cu, ctx_d, free_d, tab, kv, pos, slots, pieces, counts, block_tokens=B)
+        if planned:
+            gdn.paged_attention_plan(cu, kv, ws, T=T, Hq=Hq, Hk=Hk, d=d, block_tokens=B, max_blocks=width,
+                                     max_new_tokens=max(new))
+        for l in range(L):
+            q, k, v = (t.unflatten(1, (-1, d)) for t in x[l].split([Hq * d, Hk * d, Hk * d], 1))
+            kc, vc, ks, vs = (c[l] for c in cache)
+            gdn.rotary_kv_append(q, k, v, pos, ph, pieces, counts, q_rot, kc, vc, ks, vs)
+            gdn.paged_attention(q_rot, kc, vc, ks, vs, tab, cu, kv, o[l], ws, softmax_scale=d ** -0.5,
+                                max_new_tokens=max(new), planned=planned)
+
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    inputs = [torch.randn(x.shape, generator=gen, device="cuda").bfloat16() for _ in range(3)]
+
+    def reset(i):
+        x.copy_(inputs[i])
+        tab.copy_(tab0)
+        for c, c0 in zip(cache, (kc0, vc0, ks0, vs0)):
+            c.copy_(c0.unflatten(0, (L, blocks)))
+        o.fill_(float("nan"))
+    expect = []
+    for i in range(3):
+        reset(i)
+        step()
+        torch.cuda.synchronize()
+        expect.append([t.clone() for t in (o, *cache)])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in list(range(3)) * 20:
+        reset(i)
+        graph.replay()
+        for got, ref in zip((o, *cache), expect[i]):
+            assert torch.equal(got.view(torch.uint8), ref.view(torch.uint8))
+    ref, a = R.attention(q_rot, *(c[1] for c in cache), tab, new, kv.tolist(), d ** -0.5)
+    assert ((o[1].cpu().double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -8 * a + 1e-6 * a.max()).all()
