@@ -602,3 +602,16 @@ def test_steps_in_a_graph(decode, prompts, planned):
             assert torch.equal(got.view(torch.uint8), ref.view(torch.uint8))
     ref, a = R.attention(q_rot, *(c[1] for c in cache), tab, new, kv.tolist(), d ** -0.5)
     assert ((o[1].cpu().double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -8 * a + 1e-6 * a.max()).all()
+
+
+@pytest.mark.parametrize("new,kv", [([1, 2], [700, 60]), ([150], [400])])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_key_scales_at_either_end(new, kv, d):
+    s = make(49, new, kv, 4, 1, d, 16)
+    every = torch.arange(len(s["ks"]), device="cuda")[:, None]
+    ks = s["ks"].clone()
+    s["ks"].copy_(torch.where(every % 2 == 0, 2.0 ** -100, ks))   # scores of a block of zeros: all zero
+    check(s, run(s))
+    s["ks"].copy_(ks * 2.0 ** 100)                               # with q as much smaller: the scores as before
+    s["q"] *= 2.0 ** -100
+    check(s, run(s))
