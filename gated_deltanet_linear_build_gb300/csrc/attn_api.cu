@@ -180,7 +180,7 @@ gdn_status_t gdn_rotary_kv_append(const void* q, int64_t q_stride, const void* k
   if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned(k_scale, 4) ||
       !aligned(v_scale, 4) || !aligned16(pieces) || !aligned(num_pieces, 4))
     return GDN_ERR_ALIGNMENT;
-  // A q without rotation has nothing to be done to it.
+  // Without q: k and v alone. Without rotation q is copied.
   const bool turn_q = with_q && Hq > 0;
   return launch_rotary_kv_append(turn_q ? q : nullptr, q_stride, k, k_stride, v, v_stride,
                                  positions, phases, pieces, num_pieces, piece_capacity, q_out,

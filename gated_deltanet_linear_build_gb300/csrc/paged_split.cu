@@ -17,10 +17,12 @@
 //   wasted on few queries), P^T the 8-column one, whose register layout is
 //   that of the scores. V codes become f16 exactly (e4m3 is a subset); P is
 //   rounded to f16 (11 bits) on a scale of 2^7 to 2^15, so that a key whose
-//   weight is 2^-29 of the largest one's still keeps its digits.
+//   weight is 2^-21 of the largest one's still keeps its digits.
 // * The block's V scale enters the exponent: P' = 2^(s + log2 vs - m), and the
 //   sum takes P' / vs. Blocks of any scale then share one accumulator, and the
-//   largest contribution, not the largest weight, sets the range.
+//   largest contribution, not the largest weight, sets the range. Where scales lie so
+//   far apart that a P' leaves float32's range while P' / vs does not, the sum takes
+//   it on another range (kFarUnit).
 // * The accumulator is rescaled only when a row's maximum grows by more than
 //   2^8 (the headroom of P's range): most units skip it.
 //
@@ -32,10 +34,10 @@
 // registers (48 requests of 3k-30k tokens: 232 -> 335 us).
 //
 // Measured: 48 requests of 3k-30k tokens, 32 query and 8 kv heads of 128, 1.42 GB:
-// 233 us, 6.1 TB/s, 90% of the copy rate. 16 rows a tile (12 heads a kv head) have
-// twice the instructions a byte and half of the warps: 66%. 32 requests of 512 to
-// 1,143 tokens, 16 + 2 heads of 256, 28 MB: 15.7 us, of which 10.6 are there for a
-// single request.
+// 234 us, 6.1 TB/s, 90% of the copy rate. 16 rows a tile (12 heads a kv head) have
+// twice the instructions a byte and half of the warps: 64%. 32 requests of 512 to
+// 1,143 tokens, 16 + 2 heads of 256, 28 MB: 16.0 us (planned once a step: 14.2), of
+// which 10.7 are there for a single request.
 #include <algorithm>
 
 #include <cuda_fp16.h>

@@ -27,10 +27,10 @@
 // a tile cut by the end of a piece leaves float32 partial results, which another
 // kernel joins in CTA order.
 //
-// Measured: 4,096 tokens of a 16,384-token prompt, 32 + 8 heads of 128: 725 us, 1,325
+// Measured: 4,096 tokens of a 16,384-token prompt, 32 + 8 heads of 128: 733 us, 1,312
 // TFLOP/s, 69% of the BF16 rate (the MMAs with a softmax that does nothing: 667
-// us). 8,192-token prompt: 463 us; 16 + 2 heads of 256: 380 us, 1,445 TFLOP/s. 2,048
-// tokens of 4 prompts, 16 + 2 heads of 256: 35 us, latency.
+// us). 8,192-token prompt: 461 us; 16 + 2 heads of 256: 380 us, 1,445 TFLOP/s. 2,048
+// tokens of 4 prompts, 16 + 2 heads of 256: 35 us (planned once a step: 30.6), latency.
 //
 // Roles (four warpgroups): 0 .. kM - 1: softmax of one 128-row tile each; the
 // others up to 2: Q, widening of V; warps 12 and 15: MMAs of a tile each; warp

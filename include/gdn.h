@@ -569,7 +569,7 @@ GDN_API gdn_status_t gdn_rotary(const void* q, int64_t q_stride, const void* k,
  * is to nearest even; infinities become +-448 * scale and NaN stays NaN.
  *
  *   v           BF16 like k.   rot_dim  0 appends without rotation (q and q_out
- *               may then be NULL: nothing is done to q).
+ *               may then be NULL; a q that is given is copied to q_out).
  *   pieces, num_pieces, piece_capacity  from gdn_build_block_tables (num_pieces
  *               = its counts). Pieces outside the cache or the step are skipped.
  *   The other arguments as above; distinct pieces must name distinct blocks.
@@ -622,7 +622,14 @@ GDN_API gdn_status_t gdn_paged_attention_plan(const int32_t* cu_seqlens, const i
  *   max_new_tokens  an upper bound of the l_n (1 for a decode step). It chooses the
  *               kernels; the rows of a longer sequence may be left unwritten.
  *   flags       0 or GDN_FLAG_PLANNED.
- * Sums, maxima and the accumulator are float32. Hq % Hk == 0, Hq / Hk <= 16.
+ * Hq % Hk == 0, Hq / Hk <= 16.
+ *
+ * Precision: scores, maxima, sums and the accumulator are float32, exponentials
+ * the hardware's (2^-22). q enters the tensor cores as the sum of two e4m3 parts:
+ * exact for values within 2^-8 of their row's largest, else to 2^-17 of it. The
+ * weights enter the second product as f16, times their block's V scale: 11 bits
+ * down to 2^-21 of the row's largest such product, fewer below, none below 2^-31.
+ * The sum of the weights takes them unrounded.
  */
 GDN_API gdn_status_t gdn_paged_attention(
     const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
