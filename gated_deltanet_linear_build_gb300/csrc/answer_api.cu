@@ -73,6 +73,8 @@ gdn_status_t gdn_w4_linear(const void* x, int64_t x_stride, const void* packed, 
                           static_cast<cudaStream_t>(stream));
 }
 
+size_t gdn_token_logprobs_workspace_size(int32_t, int32_t, int32_t) { return 0; }
+
 gdn_status_t gdn_token_logprobs(const void* logits, int64_t stride, int32_t type, const int32_t* tokens,
                                 float* logprobs, float* entropy, int32_t* ranks, int32_t* top_ids,
                                 float* top_logprobs, int32_t T, int32_t V, int32_t top_k, float temperature,

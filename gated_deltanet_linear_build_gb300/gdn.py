@@ -57,6 +57,7 @@ EXPORTED_SYMBOLS = (
     "gdn_w4_unpack",
     "gdn_w4_linear_workspace_size",
     "gdn_w4_linear",
+    "gdn_token_logprobs_workspace_size",
     "gdn_token_logprobs",
     "gdn_selftest_bounded_wait",
     "gdn_device_status",
@@ -136,6 +137,7 @@ _SIGNATURES = {
     "gdn_w4_linear_workspace_size": (ctypes.c_size_t, [_I32, _I32, _I32]),
     "gdn_w4_linear": (ctypes.c_int, [_P, _I64, _P, ctypes.c_size_t, _P, _I64, _I32, _I32, _I32,
                                      _I32, _P, ctypes.c_size_t, _P]),
+    "gdn_token_logprobs_workspace_size": (ctypes.c_size_t, [_I32, _I32, _I32]),
     "gdn_token_logprobs": (ctypes.c_int, [_P, _I64, _I32, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32,
                                           _F32, _P]),
     "gdn_selftest_bounded_wait": (ctypes.c_int, [_P, _I64, _P]),
@@ -542,14 +544,20 @@ def w4_linear(x, packed, y, workspace, *, stream=None):
         _check(rc, "gdn_w4_linear")
 
 
-def token_logprobs(logits, tokens, logprobs, entropy, ranks, top_ids, top_logprobs, *,
+def token_logprobs_workspace_size(T: int, V: int, top_k: int) -> int:
+    """Bytes of workspace of token_logprobs: 0, it needs none."""
+    return int(_lib().gdn_token_logprobs_workspace_size(T, V, top_k))
+
+
+def token_logprobs(logits, tokens, logprobs, entropy, ranks, top_ids, top_logprobs, workspace=None, *,
                    temperature: float = 1.0, stream=None):
     """For each row of logits [T, V] (BF16 or float32; rows may lie in wider ones): log
     probability and rank of tokens int32 [T] into logprobs float32 [T] and ranks int32
     [T], the entropy float32 [T], and the best tokens (equal logits: the lowest index
     first) with their log probabilities into top_ids int32 and top_logprobs float32
     [T, k], k at most 32. Outputs that are None are left out (both of the last two
-    together; tokens may be None where logprobs and ranks are)."""
+    together; tokens may be None where logprobs and ranks are). workspace: not used, for
+    programs that keep one for each call (token_logprobs_workspace_size bytes: none)."""
     rc = (_MARSHAL or _marshal()).token_logprobs(logits, tokens, logprobs, entropy, ranks, top_ids, top_logprobs,
                                                  temperature, _handle(stream))
     if rc:

@@ -710,6 +710,12 @@ GDN_API gdn_status_t gdn_w4_linear(const void* x, int64_t x_stride, const void* 
                                    size_t workspace_bytes, void* stream);
 
 /*
+ * Bytes of device workspace of gdn_token_logprobs: 0, it needs none. (For programs that
+ * size one for each call of a step.) Pure host arithmetic.
+ */
+GDN_API size_t gdn_token_logprobs_workspace_size(int32_t T, int32_t V, int32_t top_k);
+
+/*
  * What a request asks about its logits. With z = logit / temperature and
  * log p(i) = z_i - log sum_j e^(z_j), for each row t:
  *   logprobs[t]      log p of tokens[t];
