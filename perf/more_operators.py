@@ -170,6 +170,7 @@ def prepare(case, seed):
         f = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)  # noqa: E731
         i = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)  # noqa: E731
         s.update(logprobs=f(t), entropy=f(t), ranks=i(t), top_ids=i(t, case["top"]), top_logprobs=f(t, case["top"]))
+        s["workspace"] = None
     return s
 
 
@@ -282,8 +283,11 @@ def _own_linear(s):
 def _own_logprobs(s):
     from gated_deltanet_linear_build_gb300 import gdn
     c = s["case"]
+    if s["workspace"] is None:          # kept by a serving program for its whole life
+        size = gdn.token_logprobs_workspace_size(c["t"], c["v"], c["top"])
+        s["workspace"] = torch.empty(size, dtype=torch.uint8, device=s["dev"])
     gdn.token_logprobs(s["logits"], s["tokens"], s["logprobs"], s["entropy"], s["ranks"], s["top_ids"],
-                       s["top_logprobs"], temperature=c["temperature"])
+                       s["top_logprobs"], s["workspace"], temperature=c["temperature"])
     return {name: s[name] for name in ("logprobs", "entropy", "ranks", "top_ids", "top_logprobs")}
 
 
