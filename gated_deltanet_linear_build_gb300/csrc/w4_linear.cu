@@ -164,7 +164,7 @@ struct Smem {
   static constexpr int o_w = kXBytes;
   static constexpr int o_bar = o_w + kWBytes;
   static constexpr int max_w = kWBytes / (2 * kTileBytes), max_a = 4;
-  static constexpr int n_bar = 2 * max_w + 2 * kMaxXStages + 2 * max_a + 4 + 2;
+  static constexpr int n_bar = 2 * max_w + 2 * kMaxXStages + 2 * max_a + 4 + 4;     // (one is spare)
   static constexpr int o_misc = o_bar + n_bar * 8;       // tmem base, abort, last [2]
   static constexpr int o_exps = o_misc + 16;             // of a tile's tokens, for each result warp
   static constexpr int total = o_exps + 4 * kMaxTokens * 4;
@@ -254,8 +254,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_linear_kernel(const Args p) {
   uint64_t* a_empty = a_full + C::a_bufs;
   uint64_t* d_full = a_empty + C::a_bufs;  // [2]
   uint64_t* d_empty = d_full + 2;        // [2]
-  uint64_t* parted = d_empty + 2;        // the result warps have stored their part
-  uint64_t* drained = parted + 1;
+  uint64_t* parted = d_empty + 2;        // [2]: the result warps have stored a part, one for each part
+  uint64_t* drained = parted + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + Smem::o_misc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + Smem::o_misc + 4);
   volatile int* s_last = reinterpret_cast<volatile int*>(smem + Smem::o_misc + 8);
@@ -281,8 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_linear_kernel(const Args p) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(d_full + i, 1);
       tc::mbar_init(d_empty + i, 4);
+      tc::mbar_init(parted + i, 4);
     }
-    tc::mbar_init(parted, 4);
     tc::mbar_init(drained, 1);
     *s_abort = s_last[0] = s_last[1] = 0;
   }
@@ -467,7 +467,6 @@ __global__ void __launch_bounds__(kThreads, 1) w4_linear_kernel(const Args p) {
     const int r = (warp & 3) * 32 + lane;
     int* s_exps = reinterpret_cast<int*>(smem + Smem::o_exps) + (warp & 3) * kMaxTokens;
     int64_t u = u0;
-    uint32_t parts = 0;                  // phase of a divided tile
     for (int seg = 0; u < u1; ++seg) {
       const int64_t tile = u / p.kb;
       const int from = (int)(u - tile * p.kb), to = (int)min((int64_t)p.kb, from + (u1 - u));
@@ -487,7 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_linear_kernel(const Args p) {
       tc::fence_after_sync();
       const uint32_t d = tc::tmem_warp_addr(tmem, (seg % nd) * p.nt);
       // A CTA has two parts at most: of its first tile, and of its last.
-      float* part = p.partials + ((size_t)c * 2 + (from == 0 && seg > 0 ? 1 : 0)) * p.nt * kRows;
+      const int slot = from == 0 && seg > 0 ? 1 : 0;
+      float* part = p.partials + ((size_t)c * 2 + slot) * p.nt * kRows;
       // Where all of the warp's scales are float32's own, one product applies one.
       const bool near = __all_sync(0xffffffffu, abs(e_n) + far <= 126);
       for (int t = 0; t < cols; t += 16) {
@@ -525,18 +525,19 @@ __global__ void __launch_bounds__(kThreads, 1) w4_linear_kernel(const Args p) {
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(d_empty + seg % nd);
       if (whole) continue;
-      // Counted once all four warps have stored theirs.
+      // Counted once all four warps have stored theirs. (Each part has a barrier of its own:
+      // with two accumulators a warp may be through with both before another has stored the
+      // first.)
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(parted);
+      if (lane == 0) tc::mbar_arrive(parted + slot);
       if (warp == 12) {
-        if (!warp_wait(parted, parts, s_abort)) break;
+        if (!warp_wait(parted + slot, 0, s_abort)) break;
         if (lane == 0) {
           __threadfence();
           if (atomicAdd(p.counters + tile, 1) == owner(p, tile * p.kb + p.kb - 1) - owner(p, tile * p.kb))
             s_last[from == 0] = 1;
         }
       }
-      parts ^= 1;
     }
   }
   // Every role is here, done or given up.

@@ -4,7 +4,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_answer import ask, rows
+import answerref as R
+from test_gpu_answer import ask, bf16, pack, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -21,3 +22,51 @@ def test_logprobs_with_a_workspace():
             ws = torch.empty(size, dtype=torch.uint8, device="cuda")
             gdn.token_logprobs(x, tokens, *out, ws, temperature=1.0)
             assert all(torch.equal(f, g) for f, g in zip(first, out))
+
+
+class Repeated:
+    """Products over weights of many rows that are copies of a few: every output is compared, at the price
+    of the few. The workspace holds NaN before each call."""
+
+    def __init__(self, N, K, seed=0):
+        rng = np.random.default_rng(seed)
+        self.N, self.K = N, K
+        base = bf16(rng, 151, K)
+        self.rows = torch.from_numpy(rng.integers(0, 151, N)).cuda()
+        self.packed = pack(base.cuda()[self.rows])
+        self.held = R.held(base).cuda()
+
+    def workspace(self, T):
+        from gated_deltanet_linear_build_gb300 import gdn
+        return torch.full((gdn.w4_linear_workspace_size(T, self.N, self.K),), 0xFF, dtype=torch.uint8, device="cuda")
+
+    def __call__(self, x, workspace, out=torch.float32):
+        from gated_deltanet_linear_build_gb300 import gdn
+        y = torch.full((x.shape[0], self.N), 77.0, dtype=out, device="cuda")
+        gdn.w4_linear(x, self.packed, y, workspace)
+        return y
+
+    def check(self, x, y):
+        xd = x.double()
+        tol = (self.K / 16 + 16) * 2.0 ** -23 * (xd.abs() @ self.held.abs().T) + 2.0 ** -149
+        tol = tol + 2.0 ** -22 * xd.abs().amax(1, True) * self.held.abs().sum(1)
+        ref = xd @ self.held.T
+        if y.dtype == torch.bfloat16:
+            tol = tol + 2.0 ** -8 * (ref.abs() + tol)
+        off = (y.double() - ref[:, self.rows]).abs() - tol[:, self.rows]
+        assert torch.isfinite(y).all() and off.max() <= 0, float(off.max())
+
+
+@pytest.mark.parametrize("T,N,K", [(96, 4096, 8192), (70, 4096, 4096), (64, 4096, 16384), (33, 20000, 8192)])
+def test_product_of_ctas_with_two_parts(T, N, K):
+    # Tiles divided so that CTAs end one and begin the next, with an accumulator for each.
+    p = Repeated(N, K, T)
+    x = bf16(np.random.default_rng(T), T, K).cuda()
+    ws = p.workspace(T)
+    first = p(x, ws)
+    assert not (ws == 0xFF).all()        # (the kernel for few tokens has no use for it)
+    p.check(x, first)
+    for _ in range(100):
+        ws.fill_(0xFF)
+        again = p(x, ws)
+        assert torch.equal(again, first)
