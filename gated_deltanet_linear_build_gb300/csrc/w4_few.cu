@@ -282,7 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_few_kernel(const __grid_consta
     const uint64_t xd = x_desc(tc::smem_u32(smem + Smem::o_x));
     const int x_step = x_tile / 16;
     // It waits for a buffer at a named barrier, where the warps that fill it arrive: no
-    // polls beside theirs. (So every step is passed, also when a wait has run out.)
+    // polls beside theirs. A named barrier knows no limit, so every step is passed, in
+    // order, also when a wait has run out: the buffer is then given back as it is.
     int ab = 0;
     convert();
     for (int row = 0; row < rows; ++row) {
@@ -307,6 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_few_kernel(const __grid_consta
           }
           tc::mma_commit(a_empty + ab);
           if (b + S >= kn) tc::mma_commit(d_full + db);
+        } else if (one) {
+          tc::mbar_arrive(a_empty + ab);
         }
         x += (uint32_t)(S * x_step);
         if (++ab == kABufs) ab = 0;
@@ -352,7 +355,12 @@ __global__ void __launch_bounds__(kThreads, 1) w4_few_kernel(const __grid_consta
     while (row < rows) {
       const int m = min(S, kn - b), filled = ab;
       uint32_t to = tc::tmem_warp_addr(a_base, ab * kACols);
-      ok = ok && granted(place_ready, s_abort);
+      // (Not without the place, whatever has run out: two buffers' arrivals at one named
+      // barrier would leave the warp of the MMAs there for good. It passes every step.)
+      if (!granted(place_ready, s_abort)) {
+        ok = false;
+        place_wait(place_ready);
+      }
       tc::fence_after_sync();
       // (Codes are asked for from here on: the place is free, so three steps back all have
       // been widened, and no stage is more than one phase away from what is asked.)
@@ -404,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_few_kernel(const __grid_consta
       const int n = (cid + row * clusters) * kRows + r, db = row & 1;
       const int e_n = exponent(p.powers[n]);
       if (!warp_wait(d_full + db, (row >> 1) & 1, s_abort, 100)) break;
+      if (__any_sync(0xffffffffu, *s_abort)) break;      // (MMAs of a buffer that was not filled)
       tc::fence_after_sync();
       const uint32_t d = tc::tmem_warp_addr(tmem, db * kFewTokens);
       if (P == 1) {
