@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, kResident) token_logprobs_kernel(con
   __shared__ Search s_search;
   __shared__ Part s_part[kMaxCluster];
   __shared__ Sums s_sums[kWarps];
-  __shared__ int s_before;
+  __shared__ int s_before[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t rank, C;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -435,7 +435,6 @@ __global__ void __launch_bounds__(kThreads, kResident) token_logprobs_kernel(con
   const int first = -off;                // element of vector 0
   const RowPart<In> in = {row, p.V, first, v0, v1};
   const float c = 1.4426950408889634f / p.temperature;
-  if (tid == 0) s_before = 0;
   // (That all CTAs of the cluster have begun is asked for where one writes to another.)
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait();
@@ -558,8 +557,7 @@ __global__ void __launch_bounds__(kThreads, kResident) token_logprobs_kernel(con
   }
   s.n = __reduce_add_sync(0xffffffffu, s.n);
   const int n = __reduce_add_sync(0xffffffffu, (int)before);
-  if (lane == 0) atomicAdd(&s_before, n);
-  if (lane == 0) s_sums[warp] = s;
+  if (lane == 0) s_sums[warp] = s, s_before[warp] = n;
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   bad = __syncthreads_or(bad);
   Part* part = &s_part[0];
@@ -577,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, kResident) token_logprobs_kernel(con
       all = joined(all, o, c);
     }
     if (bad) all.w = NAN;
+    const int stand = __reduce_add_sync(0xffffffffu, lane < kWarps ? s_before[lane] : 0);
     // To the first CTA of the cluster.
     if (C > 1) {
       uint32_t at;
@@ -589,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, kResident) token_logprobs_kernel(con
         put(4, __float_as_uint(all.r));
         put(8, __float_as_uint(all.w));
         put(12, (uint32_t)all.n);
-        put(16, (uint32_t)s_before);
+        put(16, (uint32_t)stand);
       }
       if (kTop && lane < p.k) {
         put(24 + lane * 8, (uint32_t)s_search.list[lane]);
@@ -597,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, kResident) token_logprobs_kernel(con
       }
     } else if (lane == 0) {
       part->s = all;
-      part->before = s_before;
+      part->before = stand;
     }
   }
   __syncwarp();
@@ -624,8 +623,8 @@ __global__ void __launch_bounds__(kThreads, kResident) token_logprobs_kernel(con
   const bool none = isnan(all.w);
   int place = given ? part->before + token + (mark == -INFINITY ? 0 : off) : -1;
   if (none && (kTop || given)) {
-    by_keys(row, p, s_search, given ? token : -1, &s_before);
-    if (given) place = s_before;
+    by_keys(row, p, s_search, given ? token : -1, s_before);
+    if (given) place = s_before[0];
   }
   const Row of(all, p.temperature);
   if (tid == 0) {

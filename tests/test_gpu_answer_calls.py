@@ -70,3 +70,16 @@ def test_product_of_ctas_with_two_parts(T, N, K):
         ws.fill_(0xFF)
         again = p(x, ws)
         assert torch.equal(again, first)
+
+
+@pytest.mark.parametrize("T,V", [(608, 1025), (16, 9000)])
+def test_ranks_of_rows_of_a_round_or_two(T, V):
+    # A warp may be through with its part of a row before another has begun; again and again.
+    x = rows(np.random.default_rng(V), T, V, torch.float32).cuda()
+    tokens = (torch.arange(T, device="cuda") * 37 % V).int()
+    mine = x.gather(1, tokens.long()[:, None])
+    index = torch.arange(V, device="cuda")
+    ref = ((x > mine) | ((x == mine) & (index < tokens[:, None]))).sum(1).int()
+    for k in (0, 3):
+        for _ in range(200):
+            assert torch.equal(ask(x, tokens, k)[2], ref)
