@@ -31,8 +31,8 @@ class Repeated:
     def __init__(self, N, K, seed=0):
         rng = np.random.default_rng(seed)
         self.N, self.K = N, K
-        base = bf16(rng, 151, K)
-        self.rows = torch.from_numpy(rng.integers(0, 151, N)).cuda()
+        base = bf16(rng, 40, K)
+        self.rows = torch.from_numpy(rng.integers(0, 40, N)).cuda()
         self.packed = pack(base.cuda()[self.rows])
         self.held = R.held(base).cuda()
 
@@ -64,12 +64,48 @@ def test_product_of_ctas_with_two_parts(T, N, K):
     x = bf16(np.random.default_rng(T), T, K).cuda()
     ws = p.workspace(T)
     first = p(x, ws)
-    assert not (ws == 0xFF).all()        # (the kernel for few tokens has no use for it)
+    assert not (ws == 0xFF).all()        # (the few-token kernel has no use for it)
     p.check(x, first)
     for _ in range(100):
         ws.fill_(0xFF)
         again = p(x, ws)
         assert torch.equal(again, first)
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 60000, 512), (9, 60000, 2048), (33, 40000, 640), (64, 60000, 1000),
+                                   (64, 20000, 256), (1, 12000, 12000), (20, 9000, 8192), (33, 5000, 8192),
+                                   (48, 8192, 6000), (64, 6000, 8192), (1, 131072, 64), (8, 3001, 16384),
+                                   (9, 8192, 12000), (33, 9000, 6000), (64, 5000, 4096), (64, 3000, 8192)])
+def test_product_of_few_tokens_over_several_row_tiles(T, N, K):
+    # One row tile to seven for each cluster of one CTA or several: both accumulators, parts sent again and
+    # again, a ring of codes that goes on from tile to tile. (Which of the cases with K of 4,096 and more go to
+    # the general kernel instead depends on how many clusters a device holds.)
+    p = Repeated(N, K, N + T)
+    x = bf16(np.random.default_rng(N), T, K).cuda()
+    x[T // 2] *= 2.0 ** -20              # (a token that has to be scaled beside others that have not)
+    ws = p.workspace(T)
+    for out in (torch.float32, torch.bfloat16):
+        y = p(x, ws, out)
+        p.check(x, y)
+        for _ in range(20):
+            assert torch.equal(p(x, ws, out), y)
+
+
+@pytest.mark.parametrize("T,N,K,out", [
+    (48, 12288, 4096, torch.bfloat16), (32, 131072, 4096, torch.float32), (32, 40000, 4096, torch.float32),
+    (64, 30000, 1536, torch.bfloat16), (16, 60000, 8192, torch.float32), (20, 20000, 8192, torch.bfloat16),
+    (9, 20000, 8192, torch.float32), (40, 5000, 16384, torch.bfloat16), (128, 4096, 8192, torch.float32),
+    (112, 3001, 5000, torch.bfloat16), (256, 4096, 8192, torch.float32), (65, 20000, 2048, torch.float32)])
+def test_product_whole_and_divided_by_the_general_kernel(T, N, K, out):
+    # Up to 64 tokens, whole tiles and divided ones, and one accumulator or two behind them.
+    p = Repeated(N, K, N + T)
+    x = bf16(np.random.default_rng(N), T, K).cuda()
+    ws = p.workspace(T)
+    y = p(x, ws, out)
+    p.check(x, y)
+    for _ in range(20):
+        ws.fill_(0xFF)
+        assert torch.equal(p(x, ws, out), y)
 
 
 @pytest.mark.parametrize("T,V", [(608, 1025), (16, 9000)])
