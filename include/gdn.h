@@ -736,6 +736,8 @@ GDN_API size_t gdn_token_logprobs_workspace_size(int32_t T, int32_t V, int32_t t
  * A logit of -inf is a masked token: p = 0, log p = -inf. In a row that is masked
  * altogether every log p is -inf and the entropy 0. A row that holds a NaN or +inf has
  * NaN for each log p and its entropy; a NaN stands behind all other tokens in the order.
+ * Such a row is looked through twice more, by one SM: it holds up the call (200,003 logits
+ * by 0.1 ms).
  */
 GDN_API gdn_status_t gdn_token_logprobs(const void* logits, int64_t stride, int32_t type,
                                         const int32_t* tokens, float* logprobs, float* entropy,

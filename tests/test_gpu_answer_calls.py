@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import answerref as R
-from test_gpu_answer import ask, bf16, pack, rows
+from test_gpu_answer import ask, bf16, compare, pack, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +119,52 @@ def test_ranks_of_rows_of_a_round_or_two(T, V):
     for k in (0, 3):
         for _ in range(200):
             assert torch.equal(ask(x, tokens, k)[2], ref)
+
+
+def rows_without_probabilities(T, V, dtype):
+    x = rows(np.random.default_rng(V), T, V, torch.float32)
+    x[0, V // 3] = torch.nan
+    x[1 % T, V // 2] = torch.inf
+    if T > 7:
+        x[2] = torch.nan
+        x[3] = torch.inf
+        x[4, ::2], x[4, 1::2] = torch.nan, -torch.inf
+        x[5, 5:] = torch.nan                       # less than k tokens stand before the first NaN
+        x[6, :] = 1.0
+        x[6, V - 1] = torch.nan
+        x[7] = torch.where(torch.arange(V) // 32 % 256 < 4, x[7].abs() + 9.0, x[7])     # the large in few lanes
+        x[7, 0] = torch.inf
+    return x.to(dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,V", [(9, 1025), (9, 4099), (700, 3001), (1, 70001), (8, 150001), (400, 60001)])
+def test_asked_long_rows_without_probabilities(T, V, dtype):
+    # NaN and +inf in rows that a CTA or a cluster looks through, rows with probabilities between them.
+    x = rows_without_probabilities(T, V, dtype)
+    keep = list(range(min(T, 9)))
+    for j, k in ((0, 32), (1, 5), (2, 0)):
+        tokens = torch.tensor([(V // 3, V - 1, 3)[(t + j) % 3] for t in range(T)], dtype=torch.int32, device="cuda")
+        got = [t[keep] for t in ask(x, tokens, k, 0.7)]
+        compare(got, R.asked(x[keep], tokens[keep].cpu(), k, 0.7), V)
+
+
+def test_a_nan_does_not_hold_up_a_call():
+    # A row without probabilities is looked through again, but not once for each of the best.
+    x = torch.randn((1, 3_000_017), device="cuda")
+    tokens = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def time():
+        ask(x, tokens, 32)
+        times = []
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            ask(x, tokens, 32)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+    clean = time()
+    x[0, 1_000_000] = torch.nan
+    assert time() < 100 * clean
