@@ -295,12 +295,22 @@ T* optional(PyObject* o, at::ScalarType type, int64_t rows, int64_t columns, con
   return ptr<T>(t);
 }
 
+// Packed weights [N, K], of their size to the byte: where their parts lie goes by N and K,
+// which they do not hold, so that weights of other sizes would be read as nonsense. (Too
+// few bytes the library refuses.)
+const at::TensorBase& packed_weights(PyObject* o, int64_t N, int64_t K) {
+  const at::TensorBase& p = packed(o, at::kByte, 1, "packed: contiguous uint8 expected");
+  const size_t size = gdn_w4_packed_size(fits(N), fits(K));
+  if (size > 0 && (size_t)p.numel() > size) throw Refused{"packed: weights of other sizes (w4_packed_size(N, K) bytes expected)"};
+  return p;
+}
+
 // weight, packed, stream
 PyObject* w4_pack(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call(n, 3, [&]() -> int {
     int64_t ws;
     const auto& w = bf16_matrix(a[0], &ws, "weight: bfloat16 [N, K] with contiguous rows expected");
-    const auto& p = packed(a[1], at::kByte, 1, "packed: contiguous uint8 expected");
+    const auto& p = packed_weights(a[1], w.size(0), w.size(1));
     return gdn_w4_pack(w.data_ptr(), ws, fits(w.size(0)), fits(w.size(1)), p.data_ptr(), (size_t)p.numel(),
                        stream(a[2]));
   });
@@ -310,8 +320,8 @@ PyObject* w4_pack(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* w4_unpack(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call(n, 3, [&]() -> int {
     int64_t ws;
-    const auto& p = packed(a[0], at::kByte, 1, "packed: contiguous uint8 expected");
     const auto& w = bf16_matrix(a[1], &ws, "weight: bfloat16 [N, K] with contiguous rows expected");
+    const auto& p = packed_weights(a[0], w.size(0), w.size(1));
     return gdn_w4_unpack(p.data_ptr(), (size_t)p.numel(), fits(w.size(0)), fits(w.size(1)), w.data_ptr(), ws,
                          stream(a[2]));
   });
@@ -322,9 +332,9 @@ PyObject* w4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call(n, 5, [&]() -> int {
     int64_t xs, ys;
     const auto& x = bf16_matrix(a[0], &xs, "x: bfloat16 [T, K] with contiguous rows expected");
-    const auto& p = packed(a[1], at::kByte, 1, "packed: contiguous uint8 expected");
     const char* y_what = "y: bfloat16 or float32 [T, N] with contiguous rows expected";
     const auto& y = matrix(a[2], &ys, y_what);
+    const auto& p = packed_weights(a[1], y.size(1), x.size(1));
     const int32_t type = either_type(y, y_what);
     if (y.size(0) != x.size(0)) throw Refused{"w4_linear: x and y have different rows"};
     const Bytes ws = bytes(a[3], "workspace: a contiguous tensor expected");

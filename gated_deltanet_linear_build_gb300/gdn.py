@@ -516,8 +516,9 @@ def w4_packed_size(N: int, K: int) -> int:
 
 def w4_pack(weight, packed, *, stream=None):
     """Weights [N, K] BF16 (rows may lie in wider ones) to 4 bits, into ``packed``
-    (uint8, w4_packed_size(N, K) bytes): codes, an e4m3 scale for each 16 values of a
-    row, a power of two for each row."""
+    (uint8, w4_packed_size(N, K) bytes, no more): codes, an e4m3 scale for each 16 values
+    of a row, a power of two for each row. N and K are not kept in it: the calls that read
+    it take them from their other tensors, and refuse weights of another number of bytes."""
     rc = (_MARSHAL or _marshal()).w4_pack(weight, packed, _handle(stream))
     if rc:
         _check(rc, "gdn_w4_pack")

@@ -168,3 +168,24 @@ def test_a_nan_does_not_hold_up_a_call():
     clean = time()
     x[0, 1_000_000] = torch.nan
     assert time() < 100 * clean
+
+
+def test_packed_weights_of_other_sizes_are_refused():
+    from gated_deltanet_linear_build_gb300 import gdn
+    w = torch.randn((300, 200), device="cuda").bfloat16()
+    whole = pack(w)
+    x, y = w[:5], torch.empty((5, 300), device="cuda")
+    ws = torch.empty(gdn.w4_linear_workspace_size(5, 300, 200), dtype=torch.uint8, device="cuda")
+    gdn.w4_linear(x, whole, y, ws)
+    for N, K in ((300, 128), (256, 200), (1, 200), (300, 1)):
+        with pytest.raises(ValueError, match="other sizes"):
+            gdn.w4_linear(x[:, :K] if K > 1 else x[:1, :1], whole, y[:, :N] if K > 1 else y[:1], ws)
+        with pytest.raises(ValueError, match="other sizes"):
+            gdn.w4_unpack(whole, w[:N, :K])
+        with pytest.raises(ValueError, match="other sizes"):
+            gdn.w4_pack(w[:N, :K], whole)
+    with pytest.raises(RuntimeError):
+        gdn.w4_linear(x, whole[:-1], y, ws)
+    with pytest.raises(RuntimeError):
+        gdn.w4_unpack(whole, torch.empty((400, 200), dtype=torch.bfloat16, device="cuda"))
+    gdn.w4_linear(x[:0], whole, y[:0], ws)
