@@ -88,6 +88,11 @@ __device__ __forceinline__ void tma_x(void* dst, const CUtensorMap* map, int x, 
 __device__ __forceinline__ void remote_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
 }
+// 2^d, d <= 0, as what a part counts: below 2^-149 that, next to nothing and not nothing,
+// so that an infinity stays one.
+__device__ __forceinline__ float weight_of(int d) {
+  return d >= -126 ? pow2(d) : __int_as_float(1 << (max(d, -149) + 149));
+}
 // A warp's bounded wait for arrivals of other CTAs.
 __device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   bool ok = true;
@@ -465,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_few_kernel(const __grid_consta
           for (int q = 1; q < (int)P; ++q) most = max(most, s_exps[q * kFewTokens + own0 + t]);
           s_most[t] = most;
           for (int q = 0; q < (int)P; ++q)
-            s_weight[q * kFewTokens + t] = pow2(max(-126, s_exps[q * kFewTokens + own0 + t] - most));
+            s_weight[q * kFewTokens + t] = weight_of(s_exps[q * kFewTokens + own0 + t] - most);
         }
         __syncwarp();
       }

@@ -1,11 +1,13 @@
 """The answer side's calls on the GPU as programs hold them, and at sizes that take each of its paths.
 Tolerances as in test_gpu_answer.py."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
 import answerref as R
-from test_gpu_answer import ask, bf16, compare, pack, rows
+from test_gpu_answer import Linear, ask, bf16, compare, pack, rows, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -189,3 +191,26 @@ def test_packed_weights_of_other_sizes_are_refused():
     with pytest.raises(RuntimeError):
         gdn.w4_unpack(whole, torch.empty((400, 200), dtype=torch.bfloat16, device="cuda"))
     gdn.w4_linear(x[:0], whole, y[:0], ws)
+
+
+@pytest.mark.parametrize("T", [1, 12])
+def test_product_of_slices_that_lie_far_apart(T):
+    # A token's largest value, 2^110, meets weights of zero; what is left is 2^-100 and smaller. Parts of other
+    # slices than the largest value's count by 2^-149 of it at most, f16's largest times the weights a value.
+    rng = np.random.default_rng(T)
+    N, K = 200, 12000                    # (a cluster shares K)
+    w = bf16(rng, N, K).float()
+    w[:, :48] = 0.0
+    lin = Linear(w.bfloat16())
+    x = (bf16(rng, T, K).float() * 2.0 ** -100).bfloat16()
+    x[:, 3] = 2.0 ** 110
+    ref = x.double() @ lin.ref.T
+    tol = K * 2.0 ** 15 * 2.0 ** -149 * 2.0 ** (110 - 14) * lin.ref.abs().amax(1)
+    assert (ref.abs().amax(1) > 0).all()
+    y = lin(wide(x, 0)).cpu().double()
+    assert ((y - ref).abs() <= tol).all(), float(((y - ref).abs() / tol).max())
+    x[T // 2, K - 1] = math.inf
+    y, ref = lin(wide(x, 0)).cpu().double(), x.double() @ lin.ref.T
+    row = ref[T // 2]
+    assert torch.equal(torch.isnan(y[T // 2]), torch.isnan(row)) and torch.equal(y[T // 2] == math.inf, row == math.inf)
+    assert torch.equal(y[T // 2] == -math.inf, row == -math.inf)
