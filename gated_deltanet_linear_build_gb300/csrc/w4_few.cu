@@ -556,6 +556,8 @@ bool x_tensor(CUtensorMap* map, const void* x, int64_t stride, int T, int K, int
     return reinterpret_cast<EncodeTiled>(fn);
   }();
   if (!encode) return false;
+  // (A single row's stride says nothing, and may be more than a tensor map takes.)
+  if (T == 1) stride = (K + 7) / 8 * 8;
   const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)T}, strides[1] = {(cuuint64_t)stride * 2};
   const cuuint32_t box[2] = {kK, (cuuint32_t)rows}, step[2] = {1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(x), dims, strides, box, step,

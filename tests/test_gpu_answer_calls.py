@@ -214,3 +214,18 @@ def test_product_of_slices_that_lie_far_apart(T):
     row = ref[T // 2]
     assert torch.equal(torch.isnan(y[T // 2]), torch.isnan(row)) and torch.equal(y[T // 2] == math.inf, row == math.inf)
     assert torch.equal(y[T // 2] == -math.inf, row == -math.inf)
+
+
+@pytest.mark.parametrize("stride", [256, 1 << 30, 1 << 39, 1 << 60])
+def test_product_of_one_row_of_any_stride(stride):
+    from gated_deltanet_linear_build_gb300 import gdn
+    rng = np.random.default_rng(6)
+    lin = Linear(bf16(rng, 70, 200))
+    x = wide(bf16(rng, 1, 200), 0)
+    first = lin(x)
+    y = torch.zeros_like(first)
+    ws = torch.empty(gdn.w4_linear_workspace_size(1, 70, 200), dtype=torch.uint8, device="cuda")
+    rc = gdn.load_library().gdn_w4_linear(x.data_ptr(), stride, lin.packed.data_ptr(), lin.packed.numel(),
+                                          y.data_ptr(), stride, 1, 1, 70, 200, ws.data_ptr(), ws.numel(),
+                                          torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and torch.equal(y, first)
