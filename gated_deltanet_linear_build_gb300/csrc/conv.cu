@@ -666,19 +666,12 @@ gdn_status_t launch_conv_fwd(const void* x, int64_t x_stride, const void* w, con
                              int32_t units, int32_t T, int32_t C, int32_t N, int32_t silu,
                              void* y, cudaStream_t st, StateSlots slots) {
   if (units <= 0) return GDN_OK;
-  static const int num_sms = [] {
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    cudaFuncSetAttribute(conv_fwd_stream_kernel<true>,
-                         cudaFuncAttributeMaxDynamicSharedMemorySize, kCvSmem);
-    cudaFuncSetAttribute(conv_fwd_stream_kernel<false>,
-                         cudaFuncAttributeMaxDynamicSharedMemorySize, kCvSmem);
-    return n > 0 ? n : 1;
-  }();
-  const int NB = (C + kCvChan - 1) / kCvChan;
-  const int R = std::max(1, std::min(num_sms / NB, (int)units));
+  static DeviceOnce once[2];
   auto kern = silu ? conv_fwd_stream_kernel<true> : conv_fwd_stream_kernel<false>;
+  const cudaError_t set = allow_smem(once[silu != 0], kern, kCvSmem);
+  if (set != cudaSuccess) return check_launch(set);
+  const int NB = (C + kCvChan - 1) / kCvChan;
+  const int R = std::max(1, std::min(num_sms() / NB, (int)units));
   return check_launch(launch_pdl(
       kern, dim3(NB * R), dim3(kCvThreads), kCvSmem, st, static_cast<const __nv_bfloat16*>(x),
       x_stride, static_cast<const __nv_bfloat16*>(w), static_cast<const __nv_bfloat16*>(bias),

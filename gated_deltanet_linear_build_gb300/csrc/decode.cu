@@ -561,23 +561,12 @@ gdn_status_t launch_decode_dv(int dv, const void* q, const void* k, int64_t qk_s
   return GDN_ERR_UNSUPPORTED;
 }
 
-int decode_sm_count() {
-  static const int n = [] {
-    int dev = 0, c = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&c, cudaDevAttrMultiProcessorCount, dev);
-    cudaFuncSetAttribute(delta_decode_stream_kernel<false>,
-                         cudaFuncAttributeMaxDynamicSharedMemorySize, DecStage<false>::kSmem);
-    cudaFuncSetAttribute(delta_decode_stream_kernel<true>,
-                         cudaFuncAttributeMaxDynamicSharedMemorySize, DecStage<true>::kSmem);
-    return c > 0 ? c : 1;
-  }();
-  return n;
-}
-
 template <bool kFused>
 gdn_status_t launch_decode_stream(const DecodeArgs& p, cudaStream_t st) {
-  const int sms = decode_sm_count();
+  static DeviceOnce once;
+  const cudaError_t set = allow_smem(once, delta_decode_stream_kernel<kFused>, DecStage<kFused>::kSmem);
+  if (set != cudaSuccess) return check_launch(set);
+  const int sms = num_sms();
   const int grid = p.units < sms ? p.units : sms;
   return check_launch(launch_pdl(delta_decode_stream_kernel<kFused>, dim3(grid),
                                 dim3(DecStage<kFused>::kThreads), DecStage<kFused>::kSmem, st, p));

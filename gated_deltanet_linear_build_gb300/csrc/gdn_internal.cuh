@@ -5,9 +5,11 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <utility>
 
 #include "gdn.h"
+#include "per_device.h"
 #include "tc_ptx.cuh"
 
 namespace gdn {
@@ -199,14 +201,26 @@ __device__ __forceinline__ float gate_write(float x, bool logits) {
 // ---------------------------------------------------------------------------
 // Host-side helpers
 // ---------------------------------------------------------------------------
+// The calling thread's device, -1 where there is none.
+inline int current_device() {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
 inline int num_sms() {
-  static const int n = [] {
-    int dev = 0, v = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-    return v > 0 ? v : 1;
-  }();
-  return n;
+  static DeviceNumber sms;
+  const int dev = current_device();
+  const int n = sms(dev, [&] {
+    int v = 0;
+    return cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, std::max(dev, 0)) == cudaSuccess ? v : 0;
+  });
+  return std::max(n, 1);
+}
+// Lets a kernel have `bytes` of dynamic shared memory on the current device: `once` is the
+// call site's own.
+template <typename Kernel>
+inline cudaError_t allow_smem(DeviceOnce& once, Kernel kernel, size_t bytes) {
+  return once(current_device(),
+              [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes); });
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -5,6 +5,7 @@
 #include <cuda.h>
 
 #include "gdn_internal.cuh"
+#include "tensor_map.cuh"
 
 namespace gdn {
 namespace attn {

@@ -772,8 +772,8 @@ attn_split_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
 
 template <int D, int QM>
 gdn_status_t launch_split(const Args& a, cudaStream_t st) {
-  static const cudaError_t set = cudaFuncSetAttribute(
-      attn_split_kernel<D, QM>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, QM>::total);
+  static DeviceOnce once;
+  const cudaError_t set = allow_smem(once, attn_split_kernel<D, QM>, Cfg<D, QM>::total);
   if (set != cudaSuccess) return check_launch(set);
   const int B = 1 << a.log_b;
   const int64_t pages = (int64_t)a.num_blocks * a.Hk;

@@ -930,8 +930,8 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
 
 template <int D, bool kAfterSplit>
 gdn_status_t launch_tile(const Args& a, cudaStream_t st) {
-  static const cudaError_t set = cudaFuncSetAttribute(
-      attn_tile_kernel<D, kAfterSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize, TC<D>::total);
+  static DeviceOnce once;
+  const cudaError_t set = allow_smem(once, attn_tile_kernel<D, kAfterSplit>, TC<D>::total);
   if (set != cudaSuccess) return check_launch(set);
   const int B = 1 << a.log_b;
   const int64_t pages = (int64_t)a.num_blocks * a.Hk;
@@ -949,25 +949,10 @@ gdn_status_t launch_tile(const Args& a, cudaStream_t st) {
 
 namespace attn {
 
-namespace {
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-}  // namespace
-
 // The cache as (d, token of the block, block x head), boxes of `rows` tokens.
 bool cache_map(CUtensorMap* map, const void* cache, int d, int B, int64_t pages, int rows) {
   const int row = box_row(d);
-  static const EncodeTiled encode = [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      fn = nullptr;
-    return reinterpret_cast<EncodeTiled>(fn);
-  }();
+  const EncodeTiled encode = encode_tiled();
   if (!encode) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)B, (cuuint64_t)(pages > 0 ? pages : 1)};
   const cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)d * B};

@@ -307,16 +307,12 @@ gdn_status_t launch_prefill_t(const void* q, const void* k, int64_t qk_stride, c
       sizeof(float) * (SL * PK + 3 * kChunk * PK + 2 * kChunk * PS + kChunk * PT + kChunk);
   auto k1 = intra_chunk_kernel<DK, DV>;
   auto k2 = state_pass_kernel<DK, DV, SL>;
-  // Opt in to more than 48 KB of dynamic shared memory, once per process (not a
+  // Opt in to more than 48 KB of dynamic shared memory, once per device (not a
   // stream operation, so it is also safe while a stream is being captured).
-  static const bool smem_attrs = [] {
-    cudaFuncSetAttribute(intra_chunk_kernel<DK, DV>,
-                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem1);
-    cudaFuncSetAttribute(state_pass_kernel<DK, DV, SL>,
-                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem2);
-    return true;
-  }();
-  (void)smem_attrs;
+  static DeviceOnce once1, once2;
+  cudaError_t set = allow_smem(once1, k1, smem1);
+  if (set == cudaSuccess) set = allow_smem(once2, k2, smem2);
+  if (set != cudaSuccess) return check_launch(set);
   k1<<<dim3(L.capacity, Hv), kThreads, smem1, st>>>(kp, qk_stride, vp, v_stride, a, b, count,
                                                      desc, T, Hk, Hv, flags, g_ws, w_ws, u_ws);
   if ((rc = check_launch()) != GDN_OK) return rc;

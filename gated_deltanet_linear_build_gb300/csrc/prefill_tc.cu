@@ -1044,12 +1044,10 @@ gdn_status_t launch_prefill_tc(const void* q, const void* k, int64_t qk_stride, 
   int32_t* hdr = reinterpret_cast<int32_t*>(ws);
   auto desc = reinterpret_cast<gdn_conv_chunk_t*>(ws + L.desc_off);
   unsigned char* records = ws + L.rec_off;
-  static const bool attrs = [] {
-    cudaFuncSetAttribute(tc_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kS1_BYTES);
-    cudaFuncSetAttribute(tc_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kS2_BYTES);
-    return true;
-  }();
-  (void)attrs;
+  static DeviceOnce once1, once2;
+  cudaError_t set = allow_smem(once1, tc_chunk_kernel, kS1_BYTES);
+  if (set == cudaSuccess) set = allow_smem(once2, tc_state_kernel, kS2_BYTES);
+  if (set != cudaSuccess) return check_launch(set);
   if (cudaMemsetAsync(hdr + 2, 0, sizeof(int32_t), st) != cudaSuccess) return check_launch();
   int32_t* order = reinterpret_cast<int32_t*>(ws + L.order_off);
   gdn_status_t rc = GDN_OK;

@@ -760,10 +760,6 @@ gdn_status_t launch_short(const Args& a, int T, cudaStream_t st) {
 // Shared memory with which `each` CTAs go to an SM and one more does not. (28 KB: the
 // kernel's own, about.)
 constexpr int apart(int each) { return (228 * 1024 / (each + 1) + 228 * 1024 / each) / 2 - 28 * 1024; }
-template <auto kernel>
-cudaError_t spread() {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, apart(1));
-}
 
 template <typename In>
 gdn_status_t launch(const Args& a, int T, cudaStream_t st) {
@@ -785,8 +781,9 @@ gdn_status_t launch(const Args& a, int T, cudaStream_t st) {
   // by it: 32 x 131,072 12.2 -> 16.1.)
   const int64_t each = ((int64_t)T + sms - 1) / sms;
   if (cluster == 1 && each < kResident) {
-    static const cudaError_t set[2] = {spread<token_logprobs_kernel<In, false>>(), spread<token_logprobs_kernel<In, true>>()};
-    if (set[a.k > 0] != cudaSuccess) return check_launch(set[a.k > 0]);
+    static DeviceOnce once[2];
+    const cudaError_t set = allow_smem(once[a.k > 0], kernel, apart(1));
+    if (set != cudaSuccess) return check_launch(set);
     cfg.dynamicSmemBytes = apart((int)each);
   }
   cudaLaunchAttribute attr[2];

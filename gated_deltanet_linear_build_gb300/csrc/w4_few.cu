@@ -16,10 +16,8 @@
 // become f16. us (floor), as N x K: 4,096 x 8,192 for 1 token 10.8 (2.8), 16 11.8, 32 13.1;
 // 5,003 x 1,111 for 7 6.5 (0.5); 131,072 x 4,096 for 1 69 (45).
 #include <algorithm>
-#include <array>
 
-#include <cuda.h>
-
+#include "tensor_map.cuh"
 #include "w4_mma.cuh"
 
 namespace gdn {
@@ -522,15 +520,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4_few_kernel(const __grid_consta
 }
 
 // Clusters of P CTAs that the device holds at a time (0: unknown).
-int max_clusters(int P) {
-  static const auto counts = [] {
-    std::array<int, kMaxParts + 1> n = {};
-    if (cudaFuncSetAttribute(w4_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::total) != cudaSuccess)
-      return n;
-    for (int P = 1; P <= kMaxParts; ++P) n[P] = clusters_of(w4_few_kernel, P, kThreads, Smem::total);
-    return n;
-  }();
-  return counts[P];
+int max_clusters(int device, int P) {
+  static DeviceNumber counts[kMaxParts + 1];
+  return counts[P](device, [&] { return clusters_of(w4_few_kernel, P, kThreads, Smem::total); });
 }
 
 // Tokens whose results a CTA of the cluster adds up.
@@ -542,19 +534,8 @@ int few_stages(int T, int kn, int P) {
 }
 
 // x as (k, token), boxes of 64 k and `rows` tokens; zeros outside.
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 bool x_tensor(CUtensorMap* map, const void* x, int64_t stride, int T, int K, int rows) {
-  static const EncodeTiled encode = [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
-            cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      fn = nullptr;
-    return reinterpret_cast<EncodeTiled>(fn);
-  }();
+  const EncodeTiled encode = encode_tiled();
   if (!encode) return false;
   // (A single row's stride says nothing, and may be more than a tensor map takes.)
   if (T == 1) stride = (K + 7) / 8 * 8;
@@ -570,6 +551,12 @@ bool x_tensor(CUtensorMap* map, const void* x, int64_t stride, int T, int K, int
 bool launch_w4_few(const void* x, int64_t x_stride, const void* packed, void* y, int64_t y_stride, int32_t y_type,
                    int32_t T, int32_t N, int32_t K, cudaStream_t st, gdn_status_t* rc) {
   if (T > kFewTokens) return false;
+  static DeviceOnce once;
+  if (allow_smem(once, w4_few_kernel, Smem::total) != cudaSuccess) {
+    cudaGetLastError();                  // clear it
+    return false;
+  }
+  const int device = current_device();
   const Shape s(N, K);
   Args a;
   a.nr = (T + 7) / 8 * 8;
@@ -581,7 +568,7 @@ bool launch_w4_few(const void* x, int64_t x_stride, const void* packed, void* y,
   int parts = 0;
   double least = w4_general_cost(T, N, K);
   for (int P = 1; P <= std::min(kMaxParts, s.kb); ++P) {
-    const int kn = (s.kb + P - 1) / P, clusters = max_clusters(P);
+    const int kn = (s.kb + P - 1) / P, clusters = max_clusters(device, P);
     if (clusters == 0 || few_stages(T, kn, P) < kMinWStages) continue;
     const double cost = (double)((s.rt + clusters - 1) / clusters) * (kn + (P > 1 ? 20 : 1)) + kn * a.nr * 128 / 10000.0 +
                         (P > 1 ? 40 : 20);
@@ -615,7 +602,7 @@ bool launch_w4_few(const void* x, int64_t x_stride, const void* packed, void* y,
     *rc = GDN_ERR_CUDA;
     return true;
   }
-  *rc = check_launch(launch_clusters(w4_few_kernel, std::min(s.rt, max_clusters(parts)), parts, kThreads, Smem::total, st,
+  *rc = check_launch(launch_clusters(w4_few_kernel, std::min(s.rt, max_clusters(device, parts)), parts, kThreads, Smem::total, st,
                                      a, map));
   return true;
 }

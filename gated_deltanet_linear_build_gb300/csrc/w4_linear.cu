@@ -553,8 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_linear_kernel(const Args p) {
 
 template <int S>
 gdn_status_t launch_product(Args& a, int grid, cudaStream_t st) {
-  static const cudaError_t set =
-      cudaFuncSetAttribute(w4_linear_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::total);
+  static DeviceOnce once;
+  const cudaError_t set = allow_smem(once, w4_linear_kernel<S>, Smem::total);
   if (set != cudaSuccess) return check_launch(set);
   a.x_stages = std::min(kMaxXStages, kXBytes / (Cfg<S>::x_tiles * a.nr * 128));
   return check_launch(launch_pdl(w4_linear_kernel<S>, dim3((unsigned)grid), dim3(kThreads), Smem::total, st, a));

@@ -686,8 +686,9 @@ GDN_API gdn_status_t gdn_w4_unpack(const void* packed, size_t packed_bytes, int3
 
 /*
  * Bytes of device workspace that a product of T tokens needs (0 for invalid sizes).
- * Pure host arithmetic. The workspace is 256-byte aligned, and one for T tokens serves
- * fewer of the same N and K; calls that may run at the same time need one each.
+ * Host arithmetic, with the current device's number of SMs. The workspace is 256-byte
+ * aligned, and one for T tokens serves fewer of the same N and K on that device; calls
+ * that may run at the same time need one each.
  */
 GDN_API size_t gdn_w4_linear_workspace_size(int32_t T, int32_t N, int32_t K);
 
