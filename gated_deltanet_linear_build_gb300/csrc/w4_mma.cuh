@@ -38,11 +38,6 @@ __device__ __forceinline__ bool granted(const Asked& q, volatile int* abort) {
   if (__all_sync(0xffffffffu, q.ok)) return true;
   return __all_sync(0xffffffffu, q.ok || mbar_wait_abortable(q.bar, q.parity, abort));
 }
-// The wait of `ask` again, for what comes also when other waits have run out.
-__device__ __forceinline__ void place_wait(const Asked& q) {
-  if ((threadIdx.x & 31) == 0 && !tc::mbar_wait(q.bar, q.parity)) record_device_status(GDN_ERR_TIMEOUT);
-  __syncwarp();
-}
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.b32 %0, 1, 0, q;\n\t}" : "=r"(p));

@@ -129,6 +129,6 @@ def test_arriving_without_the_place_would_not_end():
 
 def test_the_kernel_takes_the_place_before_it_arrives():
     widen = SRC[SRC.index("// ======================= codes to f16"):SRC.index("// ======================= results")]
-    assert widen.index("place_wait(place_ready)") < widen.index("filled_arrive(filled)")
+    assert widen.index("place_wait(place_ready") < widen.index("filled_arrive(filled)")
     issue = SRC[SRC.index("// ======================= MMA ="):SRC.index("// ======================= codes to f16")]
     assert "else if (one)" in issue and "tc::mbar_arrive(a_empty + ab)" in issue
