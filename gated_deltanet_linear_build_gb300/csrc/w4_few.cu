@@ -14,7 +14,7 @@
 //
 // Bound: latency up to some tens of MB of weights, then HBM, at the rate at which codes
 // become f16. us (floor), as N x K: 4,096 x 8,192 for 1 token 10.8 (2.8), 16 11.8, 32 13.1;
-// 5,003 x 1,111 for 7 6.5 (0.5); 131,072 x 4,096 for 1 69 (45).
+// 5,003 x 1,111 for 7 6.5 (0.5); 131,072 x 4,096 for 1 61 (45).
 #include <algorithm>
 
 #include "tensor_map.cuh"
@@ -24,9 +24,10 @@ namespace gdn {
 namespace {
 using namespace w4;
 
-// Warps: 0 copies codes, 1 issues the MMAs, 2 copies x, 4 to 11 widen codes, 12 to 15
-// take the results; 1 to 3 and 12 to 16 make f16 of x before all else.
-constexpr int kTurns = 2, kResults = 4 + 4 * kTurns, kThreads = (kResults + 5) * 32;
+// Warps: 0 copies codes, 1 issues the MMAs, 2 copies x, those from 4 on widen codes, in two
+// warpgroups or three, the next four take the results; 1 to 3 and the last five make f16
+// of x before all else.
+constexpr int few_threads(int turns) { return (4 + 4 * turns + 5) * 32; }
 constexpr int kFewTokens = 64;
 constexpr int kMaxParts = 8;           // CTAs of a cluster
 constexpr int S = 4;                   // tiles of 64 k a step
@@ -183,7 +184,10 @@ __device__ __noinline__ void convert_x(unsigned char* smem, const Args& p, int k
   asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
-__global__ void __launch_bounds__(kThreads, 1) w4_few_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtensorMap x_map) {
+template <int kTurns>
+__global__ void __launch_bounds__(few_threads(kTurns), 1)
+w4_few_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtensorMap x_map) {
+  constexpr int kResults = 4 + 4 * kTurns;
   extern __shared__ __align__(1024) unsigned char smem[];
   uint64_t* w_full = reinterpret_cast<uint64_t*>(smem + Smem::o_bar);
   uint64_t* w_empty = w_full + kMaxWStages;
@@ -524,13 +528,21 @@ __global__ void __launch_bounds__(kThreads, 1) w4_few_kernel(const __grid_consta
 }
 
 // Clusters of P CTAs that the device holds at a time (0: unknown).
+// (The shared memory decides, not the number of threads.)
 int max_clusters(int device, int P) {
   static DeviceNumber counts[kMaxParts + 1];
-  return counts[P](device, [&] { return clusters_of(w4_few_kernel, P, kThreads, Smem::total); });
+  return counts[P](device, [&] { return clusters_of(w4_few_kernel<3>, P, few_threads(3), Smem::total); });
 }
 
 // Tokens whose results a CTA of the cluster adds up.
 int few_share(int T, int P) { return ((T + P - 1) / P + 3) / 4 * 4; }
+// Warpgroups that widen, for CTAs with `rows` row tiles of kn tiles of 64 k. A third one
+// hides more of a step's chain of waits where a CTA has many steps, and comes late where it
+// has few or where x and the results of more than 16 tokens are the work. us by two and
+// three, 1 token: 131,072 x 4,096 66.1 and 61.1, 131,072 x 1,024 19.8 and 19.1, 20,000 x 4,096
+// 22.4 and 21.6; 60,000 x 512 (4 x 8 tiles) 8.7 and 9.1, 4,096 x 4,096 (a row) 8.0 and 8.2; 24
+// tokens: 131,072 x 1,024 23.4 and 24.0.
+int few_turns(int T, int rows, int kn) { return T <= 16 && rows > 1 && rows * kn >= 64 ? 3 : 2; }
 // What x's slice and the parts leave for the codes, in stages.
 int few_stages(int T, int kn, int P) {
   const int left = Smem::total - Smem::o_x - kn * ((T + 7) / 8 * 8) * 128 - 1024 - (P > 1 ? P * few_share(T, P) * kRows * 4 : 0);
@@ -555,8 +567,9 @@ bool x_tensor(CUtensorMap* map, const void* x, int64_t stride, int T, int K, int
 bool launch_w4_few(const void* x, int64_t x_stride, const void* packed, void* y, int64_t y_stride, int32_t y_type,
                    int32_t T, int32_t N, int32_t K, cudaStream_t st, gdn_status_t* rc) {
   if (T > kFewTokens) return false;
-  static DeviceOnce once;
-  if (allow_smem(once, w4_few_kernel, Smem::total) != cudaSuccess) {
+  static DeviceOnce once[2];
+  if (allow_smem(once[0], w4_few_kernel<2>, Smem::total) != cudaSuccess ||
+      allow_smem(once[1], w4_few_kernel<3>, Smem::total) != cudaSuccess) {
     cudaGetLastError();                  // clear it
     return false;
   }
@@ -606,8 +619,10 @@ bool launch_w4_few(const void* x, int64_t x_stride, const void* packed, void* y,
     *rc = GDN_ERR_CUDA;
     return true;
   }
-  *rc = check_launch(launch_clusters(w4_few_kernel, std::min(s.rt, max_clusters(device, parts)), parts, kThreads, Smem::total, st,
-                                     a, map));
+  const int clusters = std::min(s.rt, max_clusters(device, parts));
+  const int turns = few_turns(T, (s.rt + clusters - 1) / clusters, kn);
+  *rc = check_launch(launch_clusters(turns == 3 ? w4_few_kernel<3> : w4_few_kernel<2>, clusters, parts,
+                                     few_threads(turns), Smem::total, st, a, map));
   return true;
 }
 

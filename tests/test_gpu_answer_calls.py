@@ -229,3 +229,18 @@ def test_product_of_one_row_of_any_stride(stride):
                                           y.data_ptr(), stride, 1, 1, 70, 200, ws.data_ptr(), ws.numel(),
                                           torch.cuda.current_stream().cuda_stream)
     assert rc == 0 and torch.equal(y, first)
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 131072, 1024), (16, 131072, 640), (7, 60000, 1040), (12, 40000, 4160),
+                                   (3, 20000, 2104), (16, 39000, 2304)])
+def test_product_of_few_tokens_by_three_warpgroups(T, N, K):
+    # CTAs of many steps: a third warpgroup widens; numbers of steps that three divides and does not, last
+    # steps of one to four tiles.
+    p = Repeated(N, K, N + T)
+    x = bf16(np.random.default_rng(K), T, K).cuda()
+    ws = p.workspace(T)
+    y = p(x, ws)
+    p.check(x, y)
+    for _ in range(50):
+        assert torch.equal(p(x, ws), y)
+    assert torch.equal(p(x, ws, torch.bfloat16), y.bfloat16())
