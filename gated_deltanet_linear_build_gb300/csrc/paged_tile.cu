@@ -148,20 +148,6 @@ __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr) : "memory");
 }
-// 16 columns of this warp's 32 lanes.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr) : "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -169,21 +155,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_st32_async(uint32_t taddr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
-      :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
-         "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
-         "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
-         "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-      : "memory");
 }
 
 __device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t two) {
@@ -199,13 +170,6 @@ __device__ __forceinline__ void regs_up() {
 template <int kRegs>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegs));
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-               : "=r"(p));
-  return p != 0;
 }
 
 // A bounded wait of a whole warp: all lanes go on, or none does.
@@ -421,7 +385,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
     // (4,096 tokens of 16,384, d = 128: 797 -> 731 us).
     if (warp == 12 || (kM == 2 && warp == 15)) {
       const int m = warp == 12 ? 0 : 1;
-      const bool one = elect_one();
+      const bool one = tc::elect_one();
       constexpr uint32_t id_qk = idesc_f32(128, kKeys), id_pv = idesc_f32(128, D) | tc::kTransB;
       const uint32_t s_buf = tmem + m * 128, o_buf = tmem + C::c_o(0) + m * D;
       const uint64_t qd = tc::tile_desc(tc::smem_u32(smem + C::o_q) + m * 2 * C::q_part, D / 2, 0);
@@ -841,7 +805,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
 #pragma unroll 1
               for (int c = 0; c < D; c += 16) {
                 float v[16];
-                tmem_ld16(to + c, v);
+                tc::tmem_ld16(to + c, v);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) v[k] *= al;
                 tc::tmem_st16(to + c, *reinterpret_cast<uint32_t(*)[16]>(v));
@@ -856,7 +820,7 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
 #pragma unroll 1
           for (int gr = 0; gr < 4; ++gr) {
             float y[16];
-            tmem_ld16(ts + gr * 16, y);
+            tc::tmem_ld16(ts + gr * 16, y);
             const float iv = fabsf(sc[8 + gr]), a = factor(rs * sc[gr]), b = sc[4 + gr] - ref + far_shift(iv);
             float sum = 0.f;
 #pragma unroll
@@ -866,8 +830,8 @@ attn_tile_kernel(const Args p, const __grid_constant__ CUtensorMap k_map,
           }
         }
         l_run += lsum;
-        tmem_st32_async(ts, pk);
-        tmem_wait_st();
+        tc::tmem_st32_async(ts, pk);
+        tc::tmem_wait_st();
         tc::fence_before_sync();
         tc::mbar_arrive(p_full + buf);
       }

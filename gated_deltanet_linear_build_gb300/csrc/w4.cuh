@@ -46,6 +46,14 @@ __device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t two) {
   return r;
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+// 8 values of a row from k on, zeros behind its end.
+__device__ __forceinline__ uint4 load8(const __nv_bfloat16* row, int k, int K) {
+  if (k + 8 <= K) return ldg16(row + k);
+  uint32_t w[4] = {0, 0, 0, 0};
+  for (int i = 0; i < 8 && k + i < K; ++i)
+    w[i >> 1] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(row) + k + i) << (16 * (i & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 }  // namespace w4
 }  // namespace gdn

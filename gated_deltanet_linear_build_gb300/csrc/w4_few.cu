@@ -171,7 +171,7 @@ __device__ __noinline__ void convert_x(unsigned char* smem, const Args& p, int k
       if (!as_is(t))
         for (int b = b0; b < kn; b += step) {
           const uint4 v = load8(row, (k0 + b) * kK + ((c ^ (t & 7)) << 3), p.K);
-          if (pass == 0) top = max(top, top8(v));
+          if (pass == 0) top = max(top, finite_top8(v));
           else *reinterpret_cast<uint4*>(smem + Smem::o_x + t * 128 + c * 16 + b * stride) = to_half8(v, pow2(-e));
         }
       if (pass == 0) atomicMax(s_exp + t, (int)top);
@@ -290,7 +290,7 @@ w4_few_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtensorMa
     __syncwarp();
   } else if (warp == 1) {
     // ======================= MMA ===================================================
-    const bool one = elect_one();
+    const bool one = tc::elect_one();
     const uint32_t id = idesc_f16(p.nt);
     const uint64_t xd = x_desc(tc::smem_u32(smem + Smem::o_x));
     const int x_step = x_tile / 16;
@@ -402,7 +402,7 @@ w4_few_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtensorMa
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(emptied);
       }
-      tmem_wait_st();
+      tc::tmem_wait_st();
       tc::fence_before_sync();
       filled_arrive(filled);
     }
@@ -429,7 +429,7 @@ w4_few_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtensorMa
       if (P == 1) {
         for (int t = 0; t < p.T; t += 16) {
           float v[16];
-          tmem_ld16(d + t, v);
+          tc::tmem_ld16(d + t, v);
 #pragma unroll
           for (int k = 0; k < 16; ++k)
             if (t + k < p.T && n < p.N)
@@ -450,7 +450,7 @@ w4_few_kernel(const __grid_constant__ Args p, const __grid_constant__ CUtensorMa
       uint32_t to = remote(s_part + rank * p.share * kRows + r * 4, 0), bar = remote(parts_full, 0);
       for (int t = 0; t < p.T; t += 16) {
         float v[16];
-        tmem_ld16(d + t, v);
+        tc::tmem_ld16(d + t, v);
 #pragma unroll
         for (int k = 0; k < 16; k += 4) {
           if (t + k >= p.T) break;

@@ -133,8 +133,8 @@ __global__ void __launch_bounds__(kXThreads) w4_x_kernel(const __nv_bfloat16* x,
 #pragma unroll
   for (int i = 0; i < kXKept; ++i) kept[i] = load8(row, (i * kXThreads + tid) * 8, K);
 #pragma unroll
-  for (int i = 0; i < kXKept; ++i) top = max(top, top8(kept[i]));
-  for (int k = (kXKept * kXThreads + tid) * 8; k < K; k += kXThreads * 8) top = max(top, top8(load8(row, k, K)));
+  for (int i = 0; i < kXKept; ++i) top = max(top, finite_top8(kept[i]));
+  for (int k = (kXKept * kXThreads + tid) * 8; k < K; k += kXThreads * 8) top = max(top, finite_top8(load8(row, k, K)));
   top = __reduce_max_sync(0xffffffffu, top);
   if ((tid & 31) == 0) s_top[tid >> 5] = top;
   __syncthreads();
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_linear_kernel(const Args p) {
     __syncwarp();
   } else if (warp == 1) {
     // ======================= MMA ===================================================
-    const bool one = elect_one();
+    const bool one = tc::elect_one();
     const uint32_t id = idesc_f16(p.nt);
     const uint64_t xd = x_desc(tc::smem_u32(smem + Smem::o_x));
     const int x_tile = p.nr * 128 / 16, x_stage = C::x_tiles * x_tile;
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_linear_kernel(const Args p) {
           widen_codes(now, to);
           to += 32;
         }
-        tmem_wait_st();
+        tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) {
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_linear_kernel(const Args p) {
       const bool near = __all_sync(0xffffffffu, abs(e_n) + far <= 126);
       for (int t = 0; t < cols; t += 16) {
         float v[16];
-        tmem_ld16(d + t, v);
+        tc::tmem_ld16(d + t, v);
         if (!whole) {
 #pragma unroll
           for (int k = 0; k < 16; ++k) part[(t + k) * kRows + r] = v[k];

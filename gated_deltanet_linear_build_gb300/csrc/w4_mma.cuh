@@ -38,37 +38,6 @@ __device__ __forceinline__ bool granted(const Asked& q, volatile int* abort) {
   if (__all_sync(0xffffffffu, q.ok)) return true;
   return __all_sync(0xffffffffu, q.ok || mbar_wait_abortable(q.bar, q.parity, abort));
 }
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.b32 %0, 1, 0, q;\n\t}" : "=r"(p));
-  return p != 0;
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
-      :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
-         "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
-         "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]),
-         "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr) : "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
 // K-major operand of 128-byte swizzled rows, 8-row groups 1,024 bytes apart.
 __device__ __forceinline__ uint64_t x_desc(uint32_t addr) { return tc::smem_desc(addr, 16, 1024) | (2ull << 61); }
 // kind::f16: f16 A and B, float32 D.
@@ -127,7 +96,7 @@ __device__ __forceinline__ void widen_codes(const Codes& c, uint32_t taddr) {
   uint32_t h[32];
   widen32(c.a, __byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232), h);
   widen32(c.b, __byte_perm(s23, 0, 0x1010), __byte_perm(s23, 0, 0x3232), h + 16);
-  tmem_st32(taddr, h);
+  tc::tmem_st32_async(taddr, h);
 }
 
 // y = acc * 2^e in two steps, each within float32's range.
@@ -143,7 +112,7 @@ __device__ __forceinline__ void store(void* y, int f32, int64_t at, float v) {
 // Exponent of a power of two.
 __device__ __forceinline__ int exponent(float power) { return (__float_as_int(power) >> 23) - 127; }
 // Largest finite magnitude of 8 BF16 values, as bits.
-__device__ __forceinline__ uint32_t top8(const uint4& v) {
+__device__ __forceinline__ uint32_t finite_top8(const uint4& v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t top = 0;
 #pragma unroll
@@ -152,14 +121,6 @@ __device__ __forceinline__ uint32_t top8(const uint4& v) {
     top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
   }
   return top;
-}
-// 8 values of a row from k on, zeros behind its end.
-__device__ __forceinline__ uint4 load8(const __nv_bfloat16* row, int k, int K) {
-  if (k + 8 <= K) return ldg16(row + k);
-  uint32_t w[4] = {0, 0, 0, 0};
-  for (int i = 0; i < 8 && k + i < K; ++i)
-    w[i >> 1] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(row) + k + i) << (16 * (i & 1));
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // The exponent e under which a row with that largest magnitude becomes f16: x * 2^-e
 // has its largest in [2^14, 2^15).

@@ -22,14 +22,6 @@ constexpr int kPackRows = 8;            // of a CTA
 constexpr int kWarps = 8;               // (a row each at first)
 constexpr int kThreads = kWarps * 32;
 
-// 8 values of a row from k on, zeros behind its end.
-__device__ __forceinline__ uint4 load8(const __nv_bfloat16* row, int k, int K) {
-  if (k + 8 <= K) return ldg16(row + k);
-  uint32_t w[4] = {0, 0, 0, 0};
-  const unsigned short* at = reinterpret_cast<const unsigned short*>(row);
-  for (int i = 0; i < 8 && k + i < K; ++i) w[i >> 1] |= (uint32_t)__ldg(at + k + i) << (16 * (i & 1));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 // Largest magnitude of 8 BF16 values, as their bits (infinities and NaN above all).
 __device__ __forceinline__ uint32_t top8(const uint4& v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
