@@ -229,7 +229,10 @@ __device__ __forceinline__ int count_above(const uint64_t* list, int n, int* i) 
   return above;
 }
 
-// The k-th largest of the groups' maxima (0: less than k are not 0). All threads.
+// The k-th largest of the groups' maxima (0: less than k are not 0). All threads. (kUser:
+// rows without probabilities have copies of their own. With one for both the kernel's calls
+// became longer: 1 x 200,003, twenty best, 11.2 -> 11.7 us.)
+template <int kUser>
 __device__ __noinline__ uint64_t group_threshold(Search& s, uint64_t mine, int k) {
   const int tid = threadIdx.x;
 #pragma unroll
@@ -245,6 +248,7 @@ __device__ __noinline__ uint64_t group_threshold(Search& s, uint64_t mine, int k
 
 // The k largest of the first n entries of the list, to its front in their order; the
 // rest of the first k places is 0. All threads; n is cut off at the list's length.
+template <int kUser>
 __device__ __noinline__ void keep_best(Search& s, int n, int k) {
   const int tid = threadIdx.x;
   constexpr int kEach = kList / kThreads;
@@ -260,7 +264,7 @@ __device__ __noinline__ void keep_best(Search& s, int n, int k) {
       mine[j] = i < n ? s.list[i] : 0;
       most = max(most, mine[j]);
     }
-    const uint64_t t = group_threshold(s, most, k);
+    const uint64_t t = group_threshold<kUser>(s, most, k);
     if (tid == 0) s.count = 0;
     __syncthreads();
 #pragma unroll
@@ -310,7 +314,7 @@ __device__ __forceinline__ void find_candidates(Search& s, const RowPart<In>& pa
   uint32_t* const notes = &s.notes[tid / 32][0][0];
   float most = -INFINITY;
   for (int r = 0; r < slots; ++r) most = fmaxf(most, __uint_as_float(notes[r * 32 + lane]));
-  uint64_t threshold = group_threshold(s, (uint64_t)ordered(most) << 32, k);
+  uint64_t threshold = group_threshold<0>(s, (uint64_t)ordered(most) << 32, k);
   // The warp's own notes that pass: slot * 32 + lane, from the notes' front.
   int n = 0;
   for (int r = 0; r < slots; ++r) {
@@ -377,7 +381,7 @@ __device__ __forceinline__ void find_candidates(Search& s, const RowPart<In>& pa
     } else {
       for (int i = tid; i < kList; i += kThreads) best = max(best, s.list[i]);
     }
-    threshold = max(threshold, group_threshold(s, best, k));
+    threshold = max(threshold, group_threshold<0>(s, best, k));
   }
 }
 
@@ -412,10 +416,10 @@ __device__ __forceinline__ void each_key(const RowPart<In>& row, F f) {
 // 200,003, twenty best: 118 us, without it 12; of 2^26, 32 best: 38 ms. By a pass for each
 // of the best 772 us and 564 ms.)
 template <typename In>
-__device__ __noinline__ void by_keys(const In* logits, const Args& p, Search& s, int token, int* rank) {
-  const int tid = threadIdx.x, k = p.k;
+__device__ __noinline__ void by_keys(const In* logits, int V, int k, Search& s, int token, int* rank) {
+  const int tid = threadIdx.x;
   const int off = (int)((reinterpret_cast<uintptr_t>(logits) & 15) / sizeof(In));
-  const RowPart<In> row = {logits, p.V, -off, 0, (int)(((int64_t)p.V + off + Vec<In>::n - 1) / Vec<In>::n)};
+  const RowPart<In> row = {logits, V, -off, 0, (int)(((int64_t)V + off + Vec<In>::n - 1) / Vec<In>::n)};
   const uint64_t mine = token >= 0 ? key_of((float)logits[token], token) : ~0ull;
   uint64_t best = 0;
   int before = 0;
@@ -430,7 +434,7 @@ __device__ __noinline__ void by_keys(const In* logits, const Args& p, Search& s,
   if (tid % 32 == 0) atomicAdd(rank, before);
   uint64_t threshold = 0;
   while (k > 0) {
-    threshold = max(threshold, group_threshold(s, best, k));
+    threshold = max(threshold, group_threshold<1>(s, best, k));
     if (tid == 0) s.count = 0;
     __syncthreads();
     each_key(row, [&](uint64_t key) {
@@ -444,7 +448,7 @@ __device__ __noinline__ void by_keys(const In* logits, const Args& p, Search& s,
     best = 0;
     for (int i = tid; i < kList; i += kThreads) best = max(best, s.list[i]);
   }
-  if (k > 0) keep_best(s, s.count, k);
+  if (k > 0) keep_best<1>(s, s.count, k);
   __syncthreads();
 }
 
@@ -596,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, kResident) token_logprobs_kernel(con
   Part* part = &s_part[0];
   if constexpr (kTop) {
     find_candidates(s_search, in, rounds, shift, p.k);
-    keep_best(s_search, s_search.count, p.k);
+    keep_best<0>(s_search, s_search.count, p.k);
   }
   if (warp == 0) {
     Sums all = lane < kWarps ? s_sums[lane] : s_sums[0];
@@ -641,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, kResident) token_logprobs_kernel(con
       int n = 0;                         // (A part with less than k tokens has zeros behind them.)
       __syncthreads();
       n = (int)C * p.k;
-      keep_best(s_search, n, p.k);
+      keep_best<0>(s_search, n, p.k);
     }
     if (tid == 0)
       for (int q = 1; q < (int)C; ++q) {
@@ -656,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, kResident) token_logprobs_kernel(con
   const bool none = isnan(all.w);
   int place = given ? part->before + token + (mark == -INFINITY ? 0 : off) : -1;
   if (none && (kTop || given)) {
-    by_keys(row, p, s_search, given ? token : -1, s_before);
+    by_keys(row, p.V, p.k, s_search, given ? token : -1, s_before);
     if (given) place = s_before[0];
   }
   const Row of(all, p.temperature);
