@@ -12,8 +12,9 @@
 // * The P partial results of a token go straight to the shared memory of one of the CTAs
 //   (every CTA has some of the tokens), which adds them up in a fixed order.
 //
-// Bound: latency up to some tens of MB of weights, then HBM, at the rate at which codes
-// become f16. us (floor), as N x K: 4,096 x 8,192 for 1 token 10.8 (2.8), 16 11.8, 32 13.1;
+// Bound: latency; up to some tens of MB of weights that of setting up and of the tail, then
+// that of a step's chain (place free, codes there, read, widened, stored, told), with
+// HBM two thirds busy and no unit of the SM full. us (floor), as N x K: 4,096 x 8,192 for 1 token 10.8 (2.8), 16 11.8, 32 13.1;
 // 5,003 x 1,111 for 7 6.5 (0.5); 131,072 x 4,096 for 1 61 (45).
 #include <algorithm>
 

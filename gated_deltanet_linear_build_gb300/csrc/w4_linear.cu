@@ -21,15 +21,15 @@
 //
 // Bound: up to some 300 tokens the weights' bytes, then the tensor cores.
 //   tokens x N x K          us   floor
-//     32 x 131,072 x 4,096   70     47   4.5 TB/s
-//     48 x 12,288 x 4,096    16      4   one tile a CTA: its 64 steps of 0.13 us, and 8 us
+//     32 x 131,072 x 4,096   68     47   4.7 TB/s
+//     48 x 12,288 x 4,096    15      4   one tile a CTA: its 64 steps of 0.13 us, and 8 us
 //                                        around them (x's kernel, the first codes, results)
-//    512 x 4,096 x 8,192     46     18
-//  2,048 x 4,096 x 8,192    116     72   1.18 PFLOP/s: a tile of 64 k takes 512 cycles of the
+//    512 x 4,096 x 8,192     44     18
+//  2,048 x 4,096 x 8,192    115     72   1.19 PFLOP/s: a tile of 64 k takes 512 cycles of the
 //                                        tensor core, some 200 go by beside them; results
 //                                        are not taken while the next tile runs (one
 //                                        accumulator of 256 columns beside W's f16)
-//  2,048 x 16,384 x 4,096   223    143
+//  2,048 x 16,384 x 4,096   220    143
 #include <algorithm>
 #include <cmath>
 

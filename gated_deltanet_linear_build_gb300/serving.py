@@ -81,8 +81,9 @@ class SyntheticServingStack:
     ``weights`` holds numpy arrays: embed [V, C] and head [C, V] (BF16 bits),
     conv_w[l] [C, 4] (BF16 bits), gate_u[l], gate_r[l] [Hv, d] and
     res_scale[l] [C] (float32), prompts (token id arrays), and the sizes
-    layers, hk, hv, d, C, vocab. ``head_bits`` 16 keeps the head as it is, 4
-    holds it in 4 bits (a quarter of the bytes that a decode step reads of it).
+    layers, hk, hv, d, C, vocab. ``head_bits`` 16 keeps the head's BF16 values,
+    widened to float32, 4 holds it in 4 bits (a seventh of the bytes that a
+    step reads of it).
     """
 
     def __init__(self, weights, device="cuda", budget: int = 2048, *, head_bits: int = 16):

@@ -701,9 +701,14 @@ GDN_API size_t gdn_w4_linear_workspace_size(int32_t T, int32_t N, int32_t K);
  *           y_stride + n, y_stride >= N, aligned as its type (output). It must not
  *           overlap x.
  * Precision: the operands of the tensor cores are f16, products exact and sums in
- * float32. Weights are exact there; of x, what lies below 2^-11 of the token's largest
- * value may be off by 2^-22 of that at most, all else is exact. An infinity or NaN in a
- * token's x reaches that token's outputs alone.
+ * float32, 16 k at a time and cut off instead of rounded: some 2^-28 of a result's size
+ * for each 16 k that one accumulator takes, which is all of K, or a slice of it where few
+ * tokens share it out (K = 8,192: 4e-7 for a token, 2.4e-6 for thousands; a product
+ * with rounded float32 sums has 1e-7 to 3e-7). Weights are exact; of x, what lies below
+ * 2^-11 of the token's largest value may be off by 2^-22 of that at most, all else is
+ * exact. How much is lost there, and the order of the sums, go by T, N and K: a token's
+ * outputs may differ in these last bits by how many tokens stand beside it. An infinity
+ * or NaN in a token's x reaches that token's outputs alone.
  */
 GDN_API gdn_status_t gdn_w4_linear(const void* x, int64_t x_stride, const void* packed,
                                    size_t packed_bytes, void* y, int64_t y_stride, int32_t y_type,
